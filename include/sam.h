@@ -267,6 +267,79 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
                                          float alpha, float beta,
                                          uint64_t* bytes);
 
+/* Low-rank adapters of many requests beside a shared projection: every row
+ * gets the shared weight and the adapter pair of its own request,
+ *   Y[m] = X[m] W + scale[a] (X[m] A[a]^T) B[a],   a = ids[m],
+ * and only X[m] W where ids[m] names no adapter (any value outside 0 ..
+ * n_adapters - 1, -1 by custom). Rows may come in any order; rows of one
+ * request next to each other cost least. What another request's adapter
+ * holds (Inf and NaN too) never reaches a row.
+ *   dtype   SAM_BF16 or SAM_F16: X, W, A and B.
+ *   X       device, M rows of K values, row stride ldx >= K.
+ *   W       device, K rows of N values (trans_w SAM_OP_N, ldw >= N) or N rows
+ *           of K values (SAM_OP_T, ldw >= K).
+ *   A       device, n_adapters x rank rows of K values, compact.
+ *   B       device, n_adapters x rank rows of N values, compact.
+ *   ids     device, M int32. 4-byte aligned, like scale.
+ *   scale   device, n_adapters floats, or NULL for 1.
+ *   out     the type of Y: SAM_F32 or dtype (rounded once, to nearest even).
+ *   Y       device, M rows of N values, row stride ldy >= N; write-only.
+ * rank 1 .. 128 (adapters of lower rank: zero rows); n_adapters 0 is the
+ * plain projection; N, K >= 1; M == 0 is a no-op. Sums are FP32; the rank-r
+ * intermediate is kept to 16 (SAM_BF16) or 22 (SAM_F16) bits relative to its
+ * row's largest value. Other base addresses must be 16-byte aligned; rows
+ * that are no whole 16-byte pieces (K or N not a multiple of 8, or such a
+ * stride) are copied into the workspace first. Y must not overlap anything
+ * else. Workspace: sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when
+ * short. N, K and strides up to 2.08 M values. Asynchronous on `stream`, no
+ * atomics on results, fixed summation order. */
+sam_status sam_adapter_gemm(sam_dtype dtype, sam_op trans_w, int64_t M,
+                            int64_t N, int64_t K, int64_t n_adapters,
+                            int64_t rank, const void* X, int64_t ldx,
+                            const void* W, int64_t ldw, const void* A,
+                            const void* B, const int32_t* ids,
+                            const float* scale, sam_dtype out, void* Y,
+                            int64_t ldy, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes sam_adapter_gemm needs for these arguments (host only). */
+sam_status sam_adapter_gemm_workspace(sam_dtype dtype, sam_op trans_w,
+                                      int64_t M, int64_t N, int64_t K,
+                                      int64_t n_adapters, int64_t rank,
+                                      int64_t ldx, int64_t ldw,
+                                      uint64_t* bytes);
+
+/* Gradients of sam_adapter_gemm for a given gradient dY of Y (dtype, M rows
+ * of N, row stride lddy); W is frozen. For the rows m of adapter a:
+ *   dX[m] = dY[m] W^T + scale[a] (dY[m] B[a]^T) A[a]
+ *   dA[a] = scale[a] sum_m (dY[m] B[a]^T)^T X[m]      (rank x K, FP32)
+ *   dB[a] = scale[a] sum_m (X[m] A[a]^T)^T dY[m]      (rank x N, FP32)
+ * and dX[m] = dY[m] W^T for rows without an adapter. dA and dB (compact,
+ * n_adapters x rank rows) are written whole, zeros for adapters without
+ * rows. dX (type `out`: SAM_F32 or dtype, row stride lddx >= K) may be NULL,
+ * and so may dA and dB together; what is not wanted is not computed. Rows
+ * are added up in row order in chunks of a fixed size: the same bits every
+ * time. Everything else as for sam_adapter_gemm. With M == 0 dA and dB are
+ * zeros. */
+sam_status sam_adapter_backward(sam_dtype dtype, sam_op trans_w, int64_t M,
+                                int64_t N, int64_t K, int64_t n_adapters,
+                                int64_t rank, const void* dY, int64_t lddy,
+                                const void* X, int64_t ldx, const void* W,
+                                int64_t ldw, const void* A, const void* B,
+                                const int32_t* ids, const float* scale,
+                                sam_dtype out, void* dX, int64_t lddx,
+                                float* dA, float* dB, void* workspace,
+                                uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes sam_adapter_backward needs (host only). want_dx, want_dab:
+ * whether dX, and dA with dB, will be asked for. */
+sam_status sam_adapter_backward_workspace(sam_dtype dtype, sam_op trans_w,
+                                          int64_t M, int64_t N, int64_t K,
+                                          int64_t n_adapters, int64_t rank,
+                                          int64_t lddy, int64_t ldx,
+                                          int64_t ldw, int32_t want_dx,
+                                          int32_t want_dab, uint64_t* bytes);
+
 /* Number of entries in the variant table (ids 0 .. count-1). */
 int32_t sam_variant_count(void);
 

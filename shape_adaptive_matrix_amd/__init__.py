@@ -109,6 +109,14 @@ def lib() -> ctypes.CDLL:
         "sam_gemm_mxfp4": ([vp, vp, vp, vp, vp, i64, i64, i64, vp, u64, vp], ctypes.c_int),
         "sam_gemm_mxfp4_variant": ([i32, i32, vp, vp, vp, vp, vp, i64, i64, i64, vp, u64, vp], ctypes.c_int),
         "sam_gemm_noalloc": ([ctypes.c_int, vp, vp, vp, i64, i64, i64, vp], ctypes.c_int),
+        "sam_adapter_gemm": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                              ctypes.c_int, vp, i64, vp, u64, vp], ctypes.c_int),
+        "sam_adapter_gemm_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64, i64, i64,
+                                        ctypes.POINTER(u64)], ctypes.c_int),
+        "sam_adapter_backward": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp,
+                                  vp, vp, vp, ctypes.c_int, vp, i64, vp, vp, vp, u64, vp], ctypes.c_int),
+        "sam_adapter_backward_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64, i64, i64, i64, i32,
+                                            i32, ctypes.POINTER(u64)], ctypes.c_int),
         "sam_device_check": ([], ctypes.c_int),
         "sam_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "sam_last_error": ([], ctypes.c_char_p),
@@ -466,3 +474,110 @@ def gemm_mxfp4_variant(vid: int, A, SA, Bt, SB, C=None, split_k: int = 0, worksp
     _check(lib().sam_gemm_mxfp4_variant(vid, p["split_k"], _ptr(A), _ptr(SA), _ptr(Bt), _ptr(SB), _ptr(C), M, N, K,
                                         _ptr(workspace), ws_bytes, _stream_ptr(stream)))
     return C
+
+
+# -- low-rank adapters beside a shared projection --------------------------------
+def _adapter_operands(X, W, A, B, ids, scale, trans_w):
+    """Checks of the tensors that the adapter calls share; (code, M, N, K, n, rank, ldx, ldw)."""
+    import torch
+    if X.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"X must be bfloat16 or float16 (got {X.dtype})")
+    for t, name in ((W, "W"), (A, "A"), (B, "B")):
+        if t.dtype != X.dtype:
+            raise TypeError(f"{name} is {t.dtype}, X is {X.dtype}")
+    ldx, ldw = _rows(X, "X"), _rows(W, "W")
+    M, K = X.shape
+    Kw, N = (W.shape[1], W.shape[0]) if trans_w else (W.shape[0], W.shape[1])
+    if Kw != K:
+        raise ValueError(f"X has rows of {K}, W {tuple(W.shape)} (trans_w={bool(trans_w)}) takes {Kw}")
+    if A.dim() != 3 or B.dim() != 3 or A.shape[:2] != B.shape[:2] or A.shape[2] != K or B.shape[2] != N:
+        raise ValueError(f"A must be [n, rank, {K}] and B [n, rank, {N}] (got {tuple(A.shape)}, {tuple(B.shape)})")
+    if not (A.is_contiguous() and B.is_contiguous()):
+        raise ValueError("A and B must be contiguous")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,) or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous int32 tensor of {M} (got {ids.dtype} {tuple(ids.shape)})")
+    n, rank = int(A.shape[0]), int(A.shape[1])
+    if scale is not None and (scale.dtype != torch.float32 or tuple(scale.shape) != (n,) or not scale.is_contiguous()):
+        raise ValueError(f"scale must be a contiguous float32 tensor of {n}")
+    return _torch_dtype_code(X, None), M, N, K, n, rank, ldx, ldw
+
+
+def _adapter_result(Y, rows, cols, out_dtype, like, name):
+    """The result tensor (given or new) and its type code."""
+    import torch
+    if Y is not None:
+        if out_dtype is not None and Y.dtype != out_dtype:
+            raise TypeError(f"{name} is {Y.dtype}, out_dtype {out_dtype}")
+        out_dtype = Y.dtype
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.float32, like.dtype):
+        raise TypeError(f"{name} must be float32 or {like.dtype} (got {out_dtype})")
+    if Y is None:
+        Y = torch.empty((rows, cols), dtype=out_dtype, device=like.device)
+    elif tuple(Y.shape) != (rows, cols):
+        raise ValueError(f"{name} must have shape ({rows}, {cols}) (got {tuple(Y.shape)})")
+    return Y, _torch_dtype_code(Y, None)
+
+
+def adapter_gemm(X, W, A, B, ids, scale=None, Y=None, trans_w=False, out_dtype=None, workspace=None, stream=None):
+    """Y[m] = X[m]·W + scale[a]·(X[m]·A[a]^T)·B[a] with a = ids[m]
+    (sam_adapter_gemm); rows whose id is outside 0 .. n-1 get X[m]·W alone.
+
+    X [M, K] and W [K, N] (trans_w: [N, K]), bfloat16 or float16, may be views
+    with padded rows; A [n, rank, K], B [n, rank, N], ids int32 [M], scale
+    float32 [n]. Returns Y [M, N], float32 unless out_dtype (or Y) is of the
+    operands' type."""
+    code, M, N, K, n, rank, ldx, ldw = _adapter_operands(X, W, A, B, ids, scale, trans_w)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    dev = _on_device((X, W, A, B, ids, scale, Y, workspace), ("X", "W", "A", "B", "ids", "scale", "Y", "workspace"))
+    Y, out = _adapter_result(Y, M, N, out_dtype, X, "Y")
+    ldy = _rows(Y, "Y")
+    if workspace is None:
+        b = ctypes.c_uint64()
+        _check(lib().sam_adapter_gemm_workspace(code, int(trans_w), M, N, K, n, rank, ldx, ldw, ctypes.byref(b)))
+        workspace = workspace_for({"workspace_bytes": b.value}, dev, stream)
+    _check(lib().sam_adapter_gemm(code, int(trans_w), M, N, K, n, rank, _ptr(X), ldx, _ptr(W), ldw, _ptr(A), _ptr(B),
+                                  _ptr(ids), _ptr(scale), out, _ptr(Y), ldy, _ptr(workspace),
+                                  _workspace_bytes(workspace), _stream_ptr(stream)))
+    return Y
+
+
+def adapter_backward(dY, X, W, A, B, ids, scale=None, dX=None, dA=None, dB=None, trans_w=False, out_dtype=None,
+                     need_dx=True, need_dab=True, workspace=None, stream=None):
+    """Gradients of adapter_gemm for dY [M, N] (sam_adapter_backward): (dX, dA,
+    dB), dX [M, K] float32 unless out_dtype (or dX) is of the operands' type,
+    dA [n, rank, K] and dB [n, rank, N] float32. need_dx / need_dab False:
+    that part is not computed and None is returned for it."""
+    import torch
+    code, M, N, K, n, rank, ldx, ldw = _adapter_operands(X, W, A, B, ids, scale, trans_w)
+    if dY.dtype != X.dtype or tuple(dY.shape) != (M, N):
+        raise ValueError(f"dY must be {X.dtype} [{M}, {N}] (got {dY.dtype} {tuple(dY.shape)})")
+    lddy = _rows(dY, "dY")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    dev = _on_device((dY, X, W, A, B, ids, scale, dX, dA, dB, workspace),
+                     ("dY", "X", "W", "A", "B", "ids", "scale", "dX", "dA", "dB", "workspace"))
+    out, lddx = F32, max(K, 1)
+    if need_dx:
+        dX, out = _adapter_result(dX, M, K, out_dtype, X, "dX")
+        lddx = _rows(dX, "dX")
+    else:
+        dX = None
+    if need_dab:
+        dA, dB = (torch.empty(s, dtype=torch.float32, device=dev) if t is None else t
+                  for t, s in ((dA, A.shape), (dB, B.shape)))
+        for t, like, name in ((dA, A, "dA"), (dB, B, "dB")):
+            if t.dtype != torch.float32 or t.shape != like.shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous float32 {tuple(like.shape)}")
+    else:
+        dA = dB = None
+    if workspace is None:
+        b = ctypes.c_uint64()
+        _check(lib().sam_adapter_backward_workspace(code, int(trans_w), M, N, K, n, rank, lddy, ldx, ldw, int(need_dx),
+                                                    int(need_dab), ctypes.byref(b)))
+        workspace = workspace_for({"workspace_bytes": b.value}, dev, stream)
+    _check(lib().sam_adapter_backward(code, int(trans_w), M, N, K, n, rank, _ptr(dY), lddy, _ptr(X), ldx, _ptr(W), ldw,
+                                      _ptr(A), _ptr(B), _ptr(ids), _ptr(scale), out, _ptr(dX), lddx, _ptr(dA),
+                                      _ptr(dB), _ptr(workspace), _workspace_bytes(workspace), _stream_ptr(stream)))
+    return dX, dA, dB

@@ -11,6 +11,7 @@
 #include <string.h>
 
 #include "../../include/sam.h"
+#include "sam_check.h"
 #include "sam_internal.h"
 
 #ifndef SAM_BUILD_STAMP
@@ -73,14 +74,8 @@ sam_status device_check_impl()
     return SAM_OK;
 }
 
-bool ranges_overlap(const void* a, unsigned long long abytes, const void* b, unsigned long long bbytes)
-{
-    if (!a || !b || abytes == 0 || bbytes == 0) return false;
-    const unsigned long long x = (unsigned long long)a, y = (unsigned long long)b;
-    return x < y + bbytes && y < x + abytes;
-}
-
-bool aligned16(const void* p) { return ((unsigned long long)p & 15ull) == 0; }
+using sam::aligned16;
+using sam::ranges_overlap;
 
 constexpr long long kMaxDim = (1ll << 31) - 1;
 
@@ -356,7 +351,7 @@ struct ExLayout {
     sam::Plan plan;
 };
 
-unsigned long long align256(unsigned long long x) { return (x + 255ull) & ~255ull; }
+using sam::align256;
 
 // A forced plan for the general entry point: variant, split and raster as
 // for sam_gemm_variant_r.
@@ -525,6 +520,27 @@ sam_status gemm_ex_run(const ExLayout& L, sam_dtype dtype, sam_op trans_a, sam_o
 }
 
 }  // namespace
+
+namespace sam {
+
+sam_status api_fail(sam_status st, const char* fmt, ...)
+{
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return st;
+}
+
+sam_status api_ok()
+{
+    g_err[0] = '\0';
+    return SAM_OK;
+}
+
+sam_status api_device_check() { return device_check_impl(); }
+
+}  // namespace sam
 
 extern "C" {
 

@@ -127,16 +127,31 @@ __device__ __forceinline__ int nsw(int row) { return (4 * (row & 3)) ^ (2 * ((ro
 // candidates and heuristics update - #4856", section "Swap microbenchmarks
 // across M, N, and K", in its form for a symmetric matrix instruction).
 //
+// HOOK: what a kernel adds to the tile's product. RingPlain adds nothing. A
+// hook with ON (16x16x32 operand-swap blocks, loads straight into LDS) gets
+// three calls: `before` ahead of the ring's first loads, `start` behind them,
+// with the accumulators still zero, and `store` in place of the stores of C.
+// b_rows: how many rows B given transposed has (a hook may run with N, the
+// stored width, rounded up).
+struct RingPlain {
+    static constexpr bool ON = false;
+    typedef int Args;
+    static __device__ __forceinline__ int b_rows(const GemmArgs& a, const int*) { return a.N; }
+};
+
 // One output tile over K values [kbeg, kend). SEG = false: the tile goes to C
 // or to split `ostride`'s partial slice; SEG = true (a segment of a stream-K
 // workgroup): to `outp` with row stride `ostride`, of which `orows` x `ocols`
 // are stored. The ring is this function's own LDS array, so a kernel that
 // instantiates it once holds one ring.
-template <int DT, int BM, int BN, int WM, int WN, int BK, int NBUF, int MODE, int BLK, int SWAP, bool SEG>
+template <int DT, int BM, int BN, int WM, int WN, int BK, int NBUF, int MODE, int BLK, int SWAP, bool SEG,
+          class HOOK = RingPlain>
 __device__ __forceinline__ void ring16_segment(const GemmArgs& args, int tm, int tn, int kbeg, int kend, float* outp,
-                                               int ostride, int orows, int ocols, bool to_c)
+                                               int ostride, int orows, int ocols, bool to_c,
+                                               const typename HOOK::Args* hook = nullptr)
 {
     using namespace dma;
+    static_assert(!HOOK::ON || (BLK == 16 && SWAP == 1 && !SEG && (MODE == 0 || MODE == 3)), "hook");
     static_assert(DT == DT_BF16 || DT == DT_F16, "16-bit operands only");
     static_assert(BK == 32 || BK == 64, "K per stage: 64- or 128-byte A rows");
     constexpr int NW = WM * WN;
@@ -236,9 +251,10 @@ __device__ __forceinline__ void ring16_segment(const GemmArgs& args, int tm, int
             const int row = I * RPA + lane / CPA;
             const int c = (lane % CPA) ^ ((row / RSW) % CPA);
             const int gk = k0 + c * 8;
-            const bool ok = n0 + row < N && gk < kend;
+            const int NB = HOOK::b_rows(args, hook);
+            const bool ok = n0 + row < NB && gk < kend;
             const i4 rBt = rsrc_words(static_cast<const char*>(args.B) + (long long)n0 * ldb * 2,
-                                      (long long)(N - n0) * ldb * 2);
+                                      (long long)(NB - n0) * ldb * 2);
             lds_load16(rBt, lds_addr(buf + A_BYTES + I * 1024), ok ? (row * ldb + gk) * 2 : kOOB);
         } else {
             const int I = wave + (q - A_PW) * NW;
@@ -445,10 +461,13 @@ __device__ __forceinline__ void ring16_segment(const GemmArgs& args, int tm, int
     u2 fb[2][TN][2];
     if constexpr (DIRECT) {
         // Fill the whole ring, then wait for stage 0.
+        if constexpr (HOOK::ON) HOOK::template before<BM>(*hook, m0, wave, lane);
 #pragma unroll
         for (int st = 0; st < NBUF; ++st)
 #pragma unroll
             for (int q = 0; q < LPS; ++q) issue_one(st, q);
+        if constexpr (HOOK::ON)
+            HOOK::template start<DT, BM, BN, NW, TM, TN, NBUF * LPS>(*hook, acc, m0, n0, wm0, wn0, wave, lane);
         wait_cnt<(NBUF - 1) * LPS, 15>();
     } else if constexpr (MODE == 1) {
 #pragma unroll
@@ -524,6 +543,10 @@ __device__ __forceinline__ void ring16_segment(const GemmArgs& args, int tm, int
         for (; k < nk; ++k) stage(k, std::false_type{});
     wait_cnt<0, 0>();   // no LDS load may still be in flight when the segment ends
 
+    if constexpr (HOOK::ON) {
+        HOOK::template store<DT, TM, TN>(*hook, acc, m0, n0, wm0, wn0, lane);
+        return;
+    }
     // The data-parallel form stores to C or to split `ostride`'s partial
     // slice, at (m0, n0) with row stride ldc (N for partials; formed here,
     // so nothing of it is live through the K loop).

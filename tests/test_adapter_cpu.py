@@ -1,0 +1,104 @@
+"""What the adapter entry points refuse, and their workspace queries, without a
+GPU: everything is rejected on the host before any device call."""
+import ctypes
+
+import pytest
+import torch
+
+import shape_adaptive_matrix_amd as sam
+
+L = sam.lib()
+P = 1 << 20   # made-up device addresses, 16-byte aligned and far apart: refused before they are used
+
+
+def forward(dtype=sam.BF16, trans=0, M=8, N=64, K=64, n=2, r=8, X=P, ldx=64, W=2 * P, ldw=64, A=3 * P, B=4 * P,
+            ids=5 * P, scale=6 * P, out=sam.F32, Y=7 * P, ldy=64, ws=8 * P, wsb=1 << 19):
+    return L.sam_adapter_gemm(dtype, trans, M, N, K, n, r, X, ldx, W, ldw, A, B, ids, scale, out, Y, ldy, ws, wsb, None)
+
+
+def backward(dtype=sam.BF16, trans=0, M=8, N=64, K=64, n=2, r=8, dY=P, lddy=64, X=2 * P, ldx=64, W=3 * P, ldw=64,
+             A=4 * P, B=5 * P, ids=6 * P, scale=None, out=sam.F32, dX=7 * P, lddx=64, dA=8 * P, dB=9 * P, ws=10 * P,
+             wsb=1 << 19):
+    return L.sam_adapter_backward(dtype, trans, M, N, K, n, r, dY, lddy, X, ldx, W, ldw, A, B, ids, scale, out, dX, lddx,
+                                  dA, dB, ws, wsb, None)
+
+
+INVALID, MISALIGNED, WORKSPACE, DEVICE = -1, -2, -3, -5
+
+REFUSED = [
+    (dict(dtype=sam.F32), INVALID), (dict(dtype=sam.MXFP8), INVALID), (dict(trans=2), INVALID),
+    (dict(out=sam.F16), INVALID), (dict(M=-1), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(n=-1), INVALID),
+    (dict(r=0), INVALID), (dict(r=129), INVALID), (dict(ldx=63), INVALID), (dict(ldw=63), INVALID),
+    (dict(M=1 << 31), INVALID), (dict(ldx=1 << 23), INVALID), (dict(X=None), INVALID), (dict(W=None), INVALID),
+    (dict(A=None), INVALID), (dict(B=None), INVALID), (dict(ids=None), INVALID), (dict(X=P + 8), MISALIGNED),
+    (dict(W=2 * P + 2), MISALIGNED), (dict(ids=5 * P + 2), MISALIGNED), (dict(wsb=16), WORKSPACE),
+    (dict(ws=None), WORKSPACE),
+]
+
+
+@pytest.mark.parametrize("change,status", REFUSED, ids=[str(c) for c, _ in REFUSED])
+def test_both_passes_refuse(change, status):
+    for call in (forward, backward):
+        assert call(**change) == status, call.__name__
+        assert sam.last_error()
+
+
+def test_forward_refuses():
+    for change, status in [(dict(ldy=63), INVALID), (dict(Y=None), INVALID), (dict(Y=P), INVALID), (dict(Y=8 * P), INVALID),
+                           (dict(Y=5 * P), INVALID), (dict(Y=7 * P + 4), MISALIGNED), (dict(scale=6 * P + 1), MISALIGNED),
+                           (dict(ws=4 * P), INVALID)]:
+        assert forward(**change) == status, change
+
+
+def test_backward_refuses():
+    for change, status in [(dict(lddy=63), INVALID), (dict(lddx=63), INVALID), (dict(dA=None), INVALID),
+                           (dict(dB=None), INVALID), (dict(dA=9 * P), INVALID), (dict(dX=2 * P), INVALID),
+                           (dict(dB=10 * P), INVALID), (dict(dA=8 * P + 4), MISALIGNED)]:
+        assert backward(**change) == status, change
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks what is said without a GPU")
+def test_good_calls_reach_the_device_check():
+    assert forward() == DEVICE and backward() == DEVICE
+    assert backward(dX=None) == DEVICE and backward(dA=None, dB=None) == DEVICE
+    assert forward(n=0, A=None, B=None, scale=None) == DEVICE
+
+
+def test_nothing_to_do():
+    assert forward(M=0) == 0
+    assert backward(dX=None, dA=None, dB=None) == 0
+
+
+def test_workspace_queries():
+    b = ctypes.c_uint64()
+    q = lambda *a: L.sam_adapter_gemm_workspace(*a, ctypes.byref(b))  # noqa: E731
+    assert q(sam.BF16, 0, 4096, 4096, 4096, 8, 16, 4096, 4096) == 0
+    assert b.value == 4096 * 16 * 4 + 4096 * 4          # T and its factors alone
+    assert q(sam.BF16, 0, 0, 64, 64, 8, 16, 64, 64) == 0 and b.value == 0
+    assert q(sam.F32, 0, 8, 64, 64, 8, 16, 64, 64) == INVALID
+    assert L.sam_adapter_gemm_workspace(sam.BF16, 0, 8, 64, 64, 8, 16, 64, 64, None) == INVALID
+    q = lambda *a: L.sam_adapter_backward_workspace(*a, ctypes.byref(b))  # noqa: E731
+    assert q(sam.BF16, 0, 64, 64, 64, 2, 8, 64, 64, 64, 1, 1) == 0
+    whole = b.value
+    assert q(sam.BF16, 0, 64, 64, 64, 2, 8, 64, 64, 64, 0, 1) == 0 and b.value <= whole
+
+
+def _tensors():
+    t = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    return dict(X=t(4, 32), W=t(32, 48), A=t(2, 8, 32), B=t(2, 8, 48), ids=torch.zeros(4, dtype=torch.int32),
+                scale=torch.ones(2))
+
+
+@pytest.mark.parametrize("change", [
+    dict(X=torch.zeros(4, 32)), dict(W=torch.zeros(32, 48, dtype=torch.float16)), dict(W=torch.zeros(48, 32, dtype=torch.bfloat16)),
+    dict(A=torch.zeros(2, 4, 32, dtype=torch.bfloat16)), dict(B=torch.zeros(2, 48, 8, dtype=torch.bfloat16).transpose(1, 2)),
+    dict(ids=torch.zeros(4, dtype=torch.int64)), dict(ids=torch.zeros(3, dtype=torch.int32)), dict(scale=torch.ones(3)),
+    dict(scale=torch.ones(2, dtype=torch.bfloat16)), dict(out_dtype=torch.float16),
+    dict(X=torch.zeros(32, 4, dtype=torch.bfloat16).t()), dict()], ids=lambda c: ",".join(c) or "host tensors")
+def test_binding_refuses(change):
+    args = {**_tensors(), **change}
+    with pytest.raises((TypeError, ValueError)):
+        sam.adapter_gemm(**args)
+    dY = torch.zeros(4, 48, dtype=torch.bfloat16)
+    with pytest.raises((TypeError, ValueError)):
+        sam.adapter_backward(dY, **args)

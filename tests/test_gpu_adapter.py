@@ -1,0 +1,218 @@
+"""Adapter projection on the GPU against its definition in 64 bits, with
+element-wise bounds from the sums' lengths and the types' half steps."""
+import pytest
+import torch
+
+import shape_adaptive_matrix_amd as sam
+from tests import adapter_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+# (M, K, N, rank, adapters): one row; every narrow tile; partials over one and
+# several K ranges; ranks that fill no block of 16 and more than 64; rows that
+# are no whole 16-byte pieces; short K (whole tiles with the term inside), the
+# last two of them on 256 x 256 and 192 x 256 tiles.
+SHAPES = [(1, 64, 64, 1, 1), (1, 4096, 512, 16, 4), (5, 200, 136, 8, 3), (16, 1, 1, 3, 2), (17, 264, 260, 4, 5),
+          (33, 1000, 300, 24, 2), (64, 512, 1032, 16, 40), (100, 777, 333, 12, 7), (300, 130, 515, 64, 3),
+          (129, 256, 640, 128, 2), (257, 2048, 384, 33, 3), (300, 2056, 8200, 48, 5), (4096, 64, 4096, 16, 8),
+          (2049, 72, 4097, 40, 5)]
+
+
+def make(M, K, N, r, n, dtype, seed, trans_w=False, runs=True):
+    g = torch.Generator().manual_seed(seed)
+    dt = TYPES[dtype]
+    t = lambda *s, by=1.0: (torch.randn(*s, generator=g) * by).to(dt).cuda()  # noqa: E731
+    X, W = t(M, K), t(*((N, K) if trans_w else (K, N)), by=K ** -0.5)
+    A, B = t(n, r, K, by=K ** -0.5), t(n, r, N, by=r ** -0.5)
+    ids = torch.randint(0, n, (M,), generator=g, dtype=torch.int32)
+    if runs and M > 8:   # sequences of one request, and single rows of others in between
+        seq = torch.sort(torch.randint(-1, n, (M,), generator=g, dtype=torch.int32)).values
+        ids = torch.where(torch.rand(M, generator=g) < 0.9, seq, ids)
+    for i, v in enumerate((-1, n, -7, 2 ** 31 - 1)):   # all of them: no adapter
+        ids[3 + 5 * i::29] = v
+    scale = torch.rand(n, generator=g).cuda() * 2 - 0.5
+    return X, W, A, B, ids.cuda(), scale
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_forward(shape, dtype):
+    for i, (trans_w, out) in enumerate(((False, None), (True, TYPES[dtype]))):
+        X, W, A, B, ids, scale = make(*shape, dtype, 11 + i, trans_w, runs=i == 0)
+        Y = sam.adapter_gemm(X, W, A, B, ids, scale, trans_w=trans_w, out_dtype=out)
+        assert Y.dtype == (out or torch.float32)
+        ref.close(Y, *ref.forward(X, W, A, B, ids, scale, trans_w), f"trans_w={trans_w}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_backward(shape, dtype):
+    M, K, N, r, n = shape
+    for i, (trans_w, out) in enumerate(((False, TYPES[dtype]), (True, None))):
+        X, W, A, B, ids, scale = make(*shape, dtype, 23 + i, trans_w, runs=i == 0)
+        dY = (torch.randn(M, N, generator=torch.Generator().manual_seed(5)) * 0.1).to(X.dtype).cuda()
+        got = sam.adapter_backward(dY, X, W, A, B, ids, scale, trans_w=trans_w, out_dtype=out)
+        want = ref.backward(dY, X, W, A, B, ids, scale, trans_w)
+        for g, w, name in zip(got, want, ("dX", "dA", "dB")):
+            ref.close(g, *w, f"{name} trans_w={trans_w}")
+
+
+@pytest.mark.parametrize("M", [40, 2049])
+def test_other_requests_inf_and_nan_stay_out(M):
+    K, N, r, n = (2048, 384, 16, 6) if M == 40 else (72, 4097, 16, 6)
+    X, W, A, B, ids, scale = make(M, K, N, r, n, "bf16", 3, runs=False)
+    clean = sam.adapter_gemm(X, W, A, B, ids, scale)
+    dY = torch.randn(M, N, device="cuda").to(X.dtype)
+    clean_b = sam.adapter_backward(dY, X, W, A, B, ids, scale)
+    A2, B2, s2 = A.clone(), B.clone(), scale.clone()
+    A2[2], B2[2], B2[4, 0, 0], s2[5] = float("nan"), float("inf"), float("nan"), float("inf")
+    dirty = sam.adapter_gemm(X, W, A2, B2, ids, s2)
+    keep = (ids != 2) & (ids != 4) & (ids != 5)
+    assert torch.equal(dirty[keep], clean[keep])
+    assert not torch.isfinite(dirty[ids == 2]).any()
+    dirty_b = sam.adapter_backward(dY, X, W, A2, B2, ids, s2)
+    assert torch.equal(dirty_b[0][keep], clean_b[0][keep])
+    for a in (0, 1, 3):
+        assert torch.equal(dirty_b[1][a], clean_b[1][a]) and torch.equal(dirty_b[2][a], clean_b[2][a])
+
+
+def test_inf_in_a_row_stays_in_it():
+    X, W, A, B, ids, scale = make(50, 512, 256, 8, 3, "f16", 4, runs=False)
+    clean = sam.adapter_gemm(X, W, A, B, ids, scale)
+    X2 = X.clone()
+    X2[7, 100], X2[20] = float("inf"), float("nan")
+    dirty = sam.adapter_gemm(X2, W, A, B, ids, scale)
+    keep = torch.ones(50, dtype=torch.bool, device="cuda")
+    keep[7] = keep[20] = False
+    assert torch.equal(dirty[keep], clean[keep])
+    assert torch.isnan(dirty[20]).all()
+
+
+@pytest.mark.parametrize("shape", [(9, 512, 256), (2049, 72, 4104)], ids=str)
+def test_no_adapter_is_the_plain_projection(shape):
+    M, K, N = shape
+    X, W, A, B, ids, scale = make(M, K, N, 16, 3, "bf16", 6)
+    none = torch.full_like(ids, -1)
+    want = ref.forward(X, W, A, B, none, scale, False)
+    Y = sam.adapter_gemm(X, W, A, B, none, scale)
+    ref.close(Y, *want)
+    assert torch.equal(Y, sam.adapter_gemm(X, W, A[:0], B[:0], ids))   # no adapters at all
+    dY = torch.randn(M, N, device="cuda").to(X.dtype)
+    dX, dA, dB = sam.adapter_backward(dY, X, W, A, B, none, scale)
+    assert not dA.any() and not dB.any()
+    ref.close(dX, *ref.forward(dY, W, B, A, none, scale, True))
+
+
+def test_no_rows():
+    X, W, A, B, ids, scale = make(1, 64, 72, 8, 3, "bf16", 6)
+    assert sam.adapter_gemm(X[:0], W, A, B, ids[:0], scale).shape == (0, 72)
+    dX, dA, dB = sam.adapter_backward(X.new_empty(0, 72), X[:0], W, A, B, ids[:0], scale,
+                                      dA=torch.full((3, 8, 64), 7.0, device="cuda"))
+    assert dX.shape == (0, 64) and not dA.any() and not dB.any()
+
+
+@pytest.mark.parametrize("pad", [8, 3])
+@pytest.mark.parametrize("shape", [(20, 512, 264, 16, 3), (1000, 128, 4000, 16, 3)], ids=str)
+def test_views_with_padded_rows(shape, pad):
+    M, K, N, r, n = shape
+    X, W, A, B, ids, scale = make(*shape, "bf16", 8)
+    nan = lambda rows, cols: torch.full((rows, cols), float("nan"), device="cuda").to(X.dtype)  # noqa: E731
+    Xp, Wp, Yp = nan(M, K + pad), nan(K, N + pad), nan(M + 1, N + pad)
+    Xp[:, :K], Wp[:, :N] = X, W
+    Yp.fill_(-77.0)
+    Y = sam.adapter_gemm(Xp[:, :K], Wp[:, :N], A, B, ids, scale, Y=Yp[:M, :N])
+    ref.close(Y, *ref.forward(X, W, A, B, ids, scale, False))
+    assert (Yp[:, N:] == -77.0).all() and (Yp[M] == -77.0).all()
+    dY = torch.randn(M, N, device="cuda").to(X.dtype)
+    dYp = nan(M, N + pad)
+    dYp[:, :N] = dY
+    dXp = torch.full((M + 1, K + pad), -77.0, device="cuda")
+    sam.adapter_backward(dYp[:, :N], Xp[:, :K], Wp[:, :N], A, B, ids, scale, dX=dXp[:M, :K])
+    ref.close(dXp[:M, :K], *ref.forward(dY, W, B, A, ids, scale, True))
+    assert (dXp[:, K:] == -77.0).all() and (dXp[M] == -77.0).all()
+
+
+def test_parts_of_the_backward_pass_alone():
+    X, W, A, B, ids, scale = make(300, 264, 136, 16, 3, "bf16", 9)
+    dY = torch.randn(300, 136, device="cuda").to(X.dtype)
+    dX, dA, dB = sam.adapter_backward(dY, X, W, A, B, ids, scale)
+    only = sam.adapter_backward(dY, X, W, A, B, ids, scale, need_dab=False)
+    assert torch.equal(only[0], dX) and only[1] is None and only[2] is None
+    only = sam.adapter_backward(dY, X, W, A, B, ids, scale, need_dx=False)
+    assert only[0] is None and torch.equal(only[1], dA) and torch.equal(only[2], dB)
+
+
+@pytest.mark.parametrize("M", [6, 700])
+def test_gradients_are_the_differences_of_the_forward_pass(M):
+    """Small integers make every product and sum exact, and Y is linear in
+    each of X, A and B: central differences are exact too."""
+    K, N, r, n = 96, 80, 8, 3
+    g = torch.Generator().manual_seed(1)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    X, W, A, B, dY = ints(M, K), ints(K, N), ints(n, r, K), ints(n, r, N), ints(M, N)
+    ids = torch.randint(-1, n, (M,), generator=g, dtype=torch.int32).cuda()
+    scale = torch.tensor([1.0, 2.0, -1.0], device="cuda")
+    grads = sam.adapter_backward(dY, X, W, A, B, ids, scale)
+    for i, grad in enumerate(grads):
+        d = ints(*grad.shape)
+        ends = []
+        for sign in (1, -1):
+            args = [X, A, B]
+            args[i] = (args[i] + sign * d).to(torch.bfloat16)
+            Y = sam.adapter_gemm(args[0], W, args[1], args[2], ids, scale)
+            ends.append(float((Y.double() * dY.double()).sum()))
+        assert (ends[0] - ends[1]) / 2 == float((grad.double() * d.double()).sum()), ("X", "A", "B")[i]
+
+
+@pytest.mark.parametrize("shape", [(24, 2048, 512, 16, 5), (2049, 256, 4096, 16, 5)], ids=str)
+def test_streams_graphs_and_repeats(shape):
+    X, W, A, B, ids, scale = make(*shape, "bf16", 12)
+    dY = torch.randn(shape[0], shape[2], device="cuda").to(X.dtype)
+    call = lambda s=None: (sam.adapter_gemm(X, W, A, B, ids, scale, stream=s),  # noqa: E731
+                           *sam.adapter_backward(dY, X, W, A, B, ids, scale, stream=s))
+    first = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = call(side)
+    side.synchronize()
+    for a, b in zip(first, other):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = call()
+    for k in range(3):
+        X.add_(0.25)                     # eager work between the replays
+        eager = call()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(eager, captured):
+            assert torch.equal(a, b), k
+
+
+def test_far_rows():
+    """Rows past 2^31 bytes of X, Y and dX."""
+    M, K, N = 140000, 8192, 64
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    some = torch.tensor([0, 1, 70001, 131071, 131072, 139999], device="cuda")
+    g = torch.Generator().manual_seed(2)
+    t = lambda *s, by=1.0: (torch.randn(*s, generator=g) * by).to(torch.bfloat16).cuda()  # noqa: E731
+    X[some] = t(len(some), K)
+    W, A, B = t(K, N, by=K ** -0.5), t(2, 16, K, by=K ** -0.5), t(2, 16, N, by=0.25)
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    ids[100000:] = 1
+    Y = sam.adapter_gemm(X, W, A, B, ids, None, out_dtype=torch.bfloat16)
+    ref.close(Y[some], *ref.forward(X[some], W, A, B, ids[some], None, False))
+    left = torch.ones(M, dtype=torch.bool, device="cuda")
+    left[some] = False
+    assert not Y[left].any()
+    dY = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    dY[some] = t(len(some), N)
+    dX, dA, dB = sam.adapter_backward(dY, X, W, A, B, ids, None, out_dtype=torch.bfloat16)
+    want = ref.backward(dY[some], X[some], W, A, B, ids[some], None, False)
+    ref.close(dX[some], *want[0])
+    assert not dX[left].any()
+    ref.close(dA, *want[1])
+    ref.close(dB, *want[2])
