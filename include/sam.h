@@ -340,6 +340,56 @@ sam_status sam_adapter_backward_workspace(sam_dtype dtype, sam_op trans_w,
                                           int64_t ldw, int32_t want_dx,
                                           int32_t want_dab, uint64_t* bytes);
 
+/* Distillation from a teacher's top logits: the student's logits z of a row
+ * against the teacher's `top` largest ones t at the vocabulary entries
+ * `index`, at temperature T:
+ *   p = softmax(t / T) over the row's valid entries, q = softmax(z / T)
+ *   loss = weight T^2 sum_j p_j (log p_j - log q_j)
+ *   grad = weight T (q - p)      (its derivative with respect to z)
+ *   dtype    SAM_F32, SAM_BF16 or SAM_F16: the type of logits and grad.
+ *   logits   device, `rows` rows of V values, row stride ldz >= V, aligned to
+ *            one value (rows that start on 16 bytes cost nothing extra).
+ *   t_dtype, teacher  device, rows x top values, compact, any of the three types.
+ *   index    device, rows x top int32, compact; a value outside 0 .. V - 1
+ *            marks an empty entry. Entries with the same index each have
+ *            their own term in the loss and add up in the gradient.
+ *   weight   device, `rows` floats (the loss's own gradient and any mean's
+ *            1 / n belong here), or NULL for 1.
+ *   loss, lse  device, `rows` floats; lse = log sum exp(z / T) (-inf for a
+ *            row of -inf).
+ *   grad     device, `rows` rows of V, row stride ldg >= V; the logits
+ *            themselves (same pointer and stride) or no part of them.
+ * Logits of -inf are masked vocabulary entries: probability and gradient
+ * contribution 0, loss +inf where the teacher's p is not 0. A row whose
+ * weight is 0, whose entries are all empty or -inf, or whose logits are all
+ * -inf has loss 0 and gradient 0 (with weight 0 also where its logits are
+ * NaN). NaN elsewhere stays in its row. top 1 .. 1024, V up to 2^31 - 65536,
+ * T positive and finite; rows == 0 is a no-op. Sums are FP32; no atomics, a
+ * fixed order. No workspace. Asynchronous on `stream`. */
+sam_status sam_distill_loss(sam_dtype dtype, int64_t rows, int64_t V,
+                            int64_t top, const void* logits, int64_t ldz,
+                            sam_dtype t_dtype, const void* teacher,
+                            const int32_t* index, const float* weight,
+                            float temperature, float* loss, float* lse,
+                            void* stream);
+
+/* The gradient from the lse that sam_distill_loss wrote. q is as exact as
+ * lse's rounding lets it be (2^-24 |lse|): a row whose logits all lie next to
+ * a type's lowest value has lost its sum there; sam_distill has not. */
+sam_status sam_distill_grad(sam_dtype dtype, int64_t rows, int64_t V,
+                            int64_t top, const void* logits, int64_t ldz,
+                            const float* lse, sam_dtype t_dtype,
+                            const void* teacher, const int32_t* index,
+                            const float* weight, float temperature, void* grad,
+                            int64_t ldg, void* stream);
+
+/* Loss and gradient together: the logits are read once. */
+sam_status sam_distill(sam_dtype dtype, int64_t rows, int64_t V, int64_t top,
+                       const void* logits, int64_t ldz, sam_dtype t_dtype,
+                       const void* teacher, const int32_t* index,
+                       const float* weight, float temperature, float* loss,
+                       void* grad, int64_t ldg, void* stream);
+
 /* Number of entries in the variant table (ids 0 .. count-1). */
 int32_t sam_variant_count(void);
 

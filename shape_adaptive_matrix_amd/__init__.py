@@ -117,6 +117,12 @@ def lib() -> ctypes.CDLL:
                                   vp, vp, vp, ctypes.c_int, vp, i64, vp, vp, vp, u64, vp], ctypes.c_int),
         "sam_adapter_backward_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64, i64, i64, i64, i32,
                                             i32, ctypes.POINTER(u64)], ctypes.c_int),
+        "sam_distill_loss": ([ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int, vp, vp, vp, ctypes.c_float, vp, vp,
+                              vp], ctypes.c_int),
+        "sam_distill_grad": ([ctypes.c_int, i64, i64, i64, vp, i64, vp, ctypes.c_int, vp, vp, vp, ctypes.c_float, vp,
+                              i64, vp], ctypes.c_int),
+        "sam_distill": ([ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int, vp, vp, vp, ctypes.c_float, vp, vp, i64,
+                         vp], ctypes.c_int),
         "sam_device_check": ([], ctypes.c_int),
         "sam_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "sam_last_error": ([], ctypes.c_char_p),
@@ -581,3 +587,85 @@ def adapter_backward(dY, X, W, A, B, ids, scale=None, dX=None, dA=None, dB=None,
                                       _ptr(A), _ptr(B), _ptr(ids), _ptr(scale), out, _ptr(dX), lddx, _ptr(dA),
                                       _ptr(dB), _ptr(workspace), _workspace_bytes(workspace), _stream_ptr(stream)))
     return dX, dA, dB
+
+
+# -- distillation from a teacher's top logits --------------------------------------
+def _distill_operands(logits, teacher, index, weight):
+    """Checks of the tensors that the distillation calls share; (rows, V, top, ldz)."""
+    import torch
+    if logits.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise TypeError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
+    ldz = _rows(logits, "logits")
+    rows, V = logits.shape
+    if teacher.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise TypeError(f"teacher must be float32, bfloat16 or float16 (got {teacher.dtype})")
+    if teacher.dim() != 2 or teacher.shape[0] != rows or not teacher.is_contiguous():
+        raise ValueError(f"teacher must be a contiguous [{rows}, top] tensor (got {tuple(teacher.shape)})")
+    if index.dtype != torch.int32 or index.shape != teacher.shape or not index.is_contiguous():
+        raise ValueError(f"index must be a contiguous int32 {tuple(teacher.shape)} tensor")
+    if weight is not None and (weight.dtype != torch.float32 or tuple(weight.shape) != (rows,)
+                               or not weight.is_contiguous()):
+        raise ValueError(f"weight must be a contiguous float32 tensor of {rows}")
+    return rows, V, int(teacher.shape[1]), ldz
+
+
+def _per_row(t, rows, dev, name):
+    import torch
+    if t is None:
+        return torch.empty(rows, dtype=torch.float32, device=dev)
+    if t.dtype != torch.float32 or tuple(t.shape) != (rows,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {rows}")
+    return t
+
+
+def _distill_result(grad, logits):
+    import torch
+    if grad is None:
+        grad = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+    if grad.dtype != logits.dtype or grad.shape != logits.shape:
+        raise ValueError(f"grad must be {logits.dtype} {tuple(logits.shape)}")
+    return grad, _rows(grad, "grad")
+
+
+def distill_loss(logits, teacher, index, weight=None, temperature=1.0, loss=None, lse=None, stream=None):
+    """Distillation loss of every row, and log-sum-exp of logits / temperature
+    (sam_distill_loss): (loss, lse), float32 [rows].
+
+    logits [rows, V] float32, bfloat16 or float16 (a view with padded rows is
+    fine), teacher [rows, top] logits of the same or another of these types
+    at the vocabulary entries index (int32; outside 0 .. V-1: empty), weight
+    float32 [rows]."""
+    rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
+    dev = _on_device((logits, teacher, index, weight, loss, lse), ("logits", "teacher", "index", "weight", "loss", "lse"))
+    loss, lse = _per_row(loss, rows, dev, "loss"), _per_row(lse, rows, dev, "lse")
+    _check(lib().sam_distill_loss(_torch_dtype_code(logits, None), rows, V, top, _ptr(logits), ldz,
+                                  _torch_dtype_code(teacher, None), _ptr(teacher), _ptr(index), _ptr(weight),
+                                  float(temperature), _ptr(loss), _ptr(lse), _stream_ptr(stream)))
+    return loss, lse
+
+
+def distill_grad(logits, lse, teacher, index, weight=None, temperature=1.0, grad=None, stream=None):
+    """Gradient of the distillation loss with respect to the logits, from the
+    lse of distill_loss (sam_distill_grad). grad may be logits itself."""
+    rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
+    dev = _on_device((logits, lse, teacher, index, weight, grad), ("logits", "lse", "teacher", "index", "weight", "grad"))
+    lse = _per_row(lse, rows, dev, "lse")
+    grad, ldg = _distill_result(grad, logits)
+    _check(lib().sam_distill_grad(_torch_dtype_code(logits, None), rows, V, top, _ptr(logits), ldz, _ptr(lse),
+                                  _torch_dtype_code(teacher, None), _ptr(teacher), _ptr(index), _ptr(weight),
+                                  float(temperature), _ptr(grad), ldg, _stream_ptr(stream)))
+    return grad
+
+
+def distill(logits, teacher, index, weight=None, temperature=1.0, loss=None, grad=None, stream=None):
+    """Distillation loss of every row and its gradient with respect to the
+    logits, which are read once (sam_distill): (loss, grad). grad may be
+    logits itself."""
+    rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
+    dev = _on_device((logits, teacher, index, weight, loss, grad), ("logits", "teacher", "index", "weight", "loss", "grad"))
+    loss = _per_row(loss, rows, dev, "loss")
+    grad, ldg = _distill_result(grad, logits)
+    _check(lib().sam_distill(_torch_dtype_code(logits, None), rows, V, top, _ptr(logits), ldz,
+                             _torch_dtype_code(teacher, None), _ptr(teacher), _ptr(index), _ptr(weight),
+                             float(temperature), _ptr(loss), _ptr(grad), ldg, _stream_ptr(stream)))
+    return loss, grad
