@@ -286,8 +286,8 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  *   Y       device, M rows of N values, row stride ldy >= N; write-only.
  * rank 1 .. 128 (adapters of lower rank: zero rows); n_adapters 0 is the
  * plain projection; N, K >= 1; M == 0 is a no-op. Sums are FP32; the rank-r
- * intermediate is kept to 16 (SAM_BF16) or 22 (SAM_F16) bits relative to its
- * row's largest value. Other base addresses must be 16-byte aligned; rows
+ * intermediate is FP32 too, or kept to 22 bits (SAM_F16; 16 for SAM_BF16 with
+ * a SAM_BF16 result) relative to its row's largest value. Other base addresses must be 16-byte aligned; rows
  * that are no whole 16-byte pieces (K or N not a multiple of 8, or such a
  * stride) are copied into the workspace first. Y must not overlap anything
  * else. Workspace: sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when
@@ -319,7 +319,7 @@ sam_status sam_adapter_gemm_workspace(sam_dtype dtype, sam_op trans_w,
  * rows. dX (type `out`: SAM_F32 or dtype, row stride lddx >= K) may be NULL,
  * and so may dA and dB together; what is not wanted is not computed. Rows
  * are added up in row order in chunks of a fixed size: the same bits every
- * time. Everything else as for sam_adapter_gemm. With M == 0 dA and dB are
+ * time. dA and dB take the intermediate whole (SAM_BF16) or to 22 bits. Everything else as for sam_adapter_gemm. With M == 0 dA and dB are
  * zeros. */
 sam_status sam_adapter_backward(sam_dtype dtype, sam_op trans_w, int64_t M,
                                 int64_t N, int64_t K, int64_t n_adapters,

@@ -70,7 +70,9 @@ struct Call {
 struct Layout {
     int rp;
     Product prod;
-    int ksplit, slots;             // shrink
+    int np;                        // 16-bit values that a T in t16 is made of
+    int wide, ksplit, slots;       // shrink
+    int merged;                    // ... in the split product's own launch
     bool pad_x, pad_w, pad_a, pad_b, pad_dy;
     long long lx, lw, la, lb, ldy; // row strides that the kernels see
     Region x, w, a, b, dy;         // padded copies
@@ -106,7 +108,7 @@ sam_status check_sizes(const Call& c)
 Layout layout(const Call& c)
 {
     Layout L{};
-    L.rp = c.n == 0 ? 0 : (c.r > 64 ? 128 : (int)((c.r + 15) / 16 * 16));
+    L.rp = c.n == 0 ? 0 : (c.r > 64 ? 128 : (c.r > 32 ? 64 : (c.r > 16 ? 32 : 16)));
     const long long rows = c.M, cols = c.back ? c.K : c.N, k = c.back ? c.N : c.K;
     L.prod = choose(rows, cols, k);
     unsigned long long at = 0;
@@ -135,32 +137,41 @@ Layout layout(const Call& c)
     if (L.pad_b) take(L.b, 2ull * c.n * c.r * L.lb);
     if (L.pad_dy) take(L.dy, 2ull * c.M * L.ldy);
 
-    // Shrink: 16 rows a workgroup. Few row blocks: K ranges and the distinct
-    // adapters of a block (up to 16) get workgroups of their own.
-    const long long blocks = (c.M + 15) / 16;
-    L.slots = blocks <= 8 ? (int)(c.n < 16 ? (c.n < 1 ? 1 : c.n) : 16) : 1;
-    L.ksplit = 1;
-    if (!c.back && L.prod.split > 0) {
-        const long long kk = c.K;
-        long long s = 128 / (blocks < 1 ? 1 : blocks);
-        const long long most = (kk + 511) / 512;   // each of the eight waves one piece of 64
-        s = s > most ? most : s;
-        L.ksplit = (int)(s < 1 ? 1 : s);
+    // Shrink. Many rows: 64 a workgroup, K cut such that two workgroups a CU
+    // share the work (at least 256 values of K each). Up to 128 rows: 16 a
+    // workgroup, the distinct adapters of a block (up to 16) and K ranges of
+    // what a workgroup loads at once on workgroups of their own.
+    const int sides = c.back && c.want_ad ? 2 : 1;
+    const long long blocks = (c.M + 15) / 16, longest = c.back && c.N > c.K ? c.N : c.K;
+    L.wide = blocks > 8;
+    L.merged = !c.back && L.prod.split > 0 && L.prod.tile >= 3;
+    L.slots = L.wide ? 1 : (int)(c.n < 16 ? (c.n < 1 ? 1 : c.n) : 16);
+    long long s, most;
+    if (L.wide) {
+        s = 2 * kCUs / ((c.M + 63) / 64 * sides);
+        most = (longest + 255) / 256;
+    } else {
+        s = (longest + 1023) / 1024 * (L.merged && L.prod.tile == 5 ? 2 : 1);   // waves: four, or the narrowest tile's two
+        most = 16;
     }
+    L.ksplit = (int)(s < 1 ? 1 : (s > most ? most : s));
+    // T inside a tile as two values of the operands' type (16 or 22 bits); an
+    // FP32 result of bfloat16 gets three, all 24.
+    L.np = c.dtype == SAM_BF16 && c.out == SAM_F32 ? 3 : 2;
     if (c.n) {
         const bool fused = L.prod.split == 0;
+        const unsigned long long t = 4ull * c.M * L.rp;
         if (!c.back) {
+            take(L.t32, t * L.ksplit);
             if (fused) {
-                take(L.t16, 4ull * c.M * L.rp);
+                take(L.t16, t / 2 * L.np);
                 take(L.factor, 4ull * c.M);
-            } else {
-                take(L.t32, 4ull * L.ksplit * c.M * L.rp);
             }
         } else {
             // T of X (for dB), T of dY (for dA and, rounded, for dX).
-            take(L.t32, 4ull * c.M * L.rp);
-            take(L.t32b, 4ull * c.M * L.rp);
-            take(L.t16, 4ull * c.M * L.rp);
+            take(L.t32, t * L.ksplit);
+            take(L.t32b, t * L.ksplit);
+            take(L.t16, t / 2 * L.np);
             take(L.factor, 4ull * c.M);
             take(L.factor2, 4ull * c.M);
             take(L.order, 4ull * (c.M + 1));
@@ -218,8 +229,8 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
 {
     char* wsb = static_cast<char*>(ws);
     auto at = [&](const Region& r) -> void* { return r.bytes ? wsb + r.off : nullptr; };
-    // Padded copies, two a launch.
-    PadCopy pads[5];
+    // Padded copies, one launch.
+    PadCopy pads[kMaxPads];
     int np = 0;
     auto pad = [&](bool on, const void*& src, long long ld, const Region& r, long long ldd, long long rows, long long cols) {
         if (!on || rows == 0) return;
@@ -232,33 +243,35 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
     pad(L.pad_a, p.A, c.K, L.a, L.la, c.n * c.r, c.K);
     pad(L.pad_b, p.B, c.N, L.b, L.lb, c.n * c.r, c.N);
     pad(L.pad_dy, p.dY, c.lddy, L.dy, L.ldy, c.M, c.N);
-    hipError_t e = hipSuccess;
-    for (int i = 0; i < np && e == hipSuccess; i += 2) e = launch_pad(pads[i], i + 1 < np ? pads[i + 1] : PadCopy{}, 2, s);
+    hipError_t e = np ? launch_adapter_pad(pads, np, s) : hipSuccess;
 
     const bool fused = L.prod.split == 0;
     const bool term = c.n > 0;
     const int out16 = c.out != SAM_F32;
-    if (e == hipSuccess && term && (c.M > 0 || c.want_ad)) {
-        ShrinkArgs a{};
+    // T's sums are added by the pass that takes them, if that is the finish of
+    // the forward pass; otherwise they are added and rounded first.
+    ShrinkArgs a{};
+    if (term) {
         a.M = (int)c.M;
         a.n = (int)c.n;
         a.r = (int)c.r;
         a.rp = L.rp;
         a.ids = p.ids;
         a.scale = p.scale;
+        a.np = L.np;
+        a.wide = L.wide;
+        a.round = c.back || fused || L.wide;
         a.ksplit = L.ksplit;
         a.slots = L.slots;
-        const ShrinkSide x = {p.X, L.lx, p.A, L.la, (int)c.K, static_cast<float*>(at(L.t32)), nullptr, nullptr};
+        a.sides = 1;
+        const ShrinkSide x = {p.X, L.lx, p.A, L.la, (int)c.K, static_cast<float*>(at(L.t32)), c.back || !fused, nullptr, nullptr};
         if (!c.back) {
-            a.sides = 1;
             a.side[0] = x;
             a.side[0].t16 = at(L.t16);
             a.side[0].factor = static_cast<float*>(at(L.factor));
         } else {
-            const ShrinkSide y = {p.dY, L.ldy, p.B, L.lb, (int)c.N, static_cast<float*>(at(L.t32b)), at(L.t16),
-                                  static_cast<float*>(at(L.factor))};
-            a.side[0] = y;
-            a.sides = 1;
+            a.side[0] = {p.dY, L.ldy, p.B, L.lb, (int)c.N, static_cast<float*>(at(L.t32b)), 1, at(L.t16),
+                         static_cast<float*>(at(L.factor))};
             if (c.want_ad) {
                 a.sides = 2;
                 a.side[1] = x;
@@ -267,7 +280,7 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
                 a.seg = static_cast<int*>(at(L.seg));
             }
         }
-        e = launch_adapter_shrink(c.dtype, a, s);
+        if (e == hipSuccess && !L.merged && (c.M > 0 || c.want_ad)) e = launch_adapter_shrink(c.dtype, a, s);
     }
     if (e == hipSuccess && c.M > 0 && (!c.back || c.want_dx)) {
         const long long cols = c.back ? c.K : c.N, k = c.back ? c.N : c.K;
@@ -292,20 +305,22 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
             x.N = (int)cols;
             x.ids = p.ids;
             x.t16 = at(L.t16);
+            x.np = L.np;
             x.factor = static_cast<const float*>(at(L.factor));
             x.Y = p.Y;
             x.ldy = ldo;
             x.out16 = out16;
-            e = launch_adapter_ring(L.prod.tile, c.dtype, bt, g, (int)cols, &x, s);
+            e = launch_adapter_ring(L.prod.tile, c.dtype, bt, g, (int)cols, &x, nullptr, s);
         } else {
-            e = launch_adapter_ring(L.prod.tile, c.dtype, bt, g, (int)cols, nullptr, s);
+            const ShrinkArgs none{};
+            e = launch_adapter_ring(L.prod.tile, c.dtype, bt, g, (int)cols, nullptr, L.merged && term ? &a : &none, s);
             if (e == hipSuccess) {
                 FinishArgs f{};
                 f.part = g.out;
                 f.ldp = g.N;
                 f.split = L.prod.split;
                 f.t32 = static_cast<const float*>(c.back ? at(L.t32b) : at(L.t32));
-                f.tsplit = L.ksplit;
+                f.tsplit = a.round ? 1 : L.ksplit;
                 f.B = B;
                 f.ldb = lb;
                 f.ids = p.ids;
@@ -396,7 +411,8 @@ sam_status sam_adapter_gemm_workspace(sam_dtype dtype, sam_op trans_w, int64_t M
                                       int64_t rank, int64_t ldx, int64_t ldw, uint64_t* bytes)
 {
     if (!bytes) return api_fail(SAM_ERR_INVALID_ARG, "bytes is null");
-    const Call c = forward_call(dtype, trans_w, M, N, K, n_adapters, rank, ldx, ldw, dtype, N);
+    // FP32 results need the most.
+    const Call c = forward_call(dtype, trans_w, M, N, K, n_adapters, rank, ldx, ldw, SAM_F32, N);
     const sam_status st = check_sizes(c);
     if (st != SAM_OK) return st;
     *bytes = M == 0 ? 0 : layout(c).total;
@@ -459,7 +475,7 @@ sam_status sam_adapter_backward_workspace(sam_dtype dtype, sam_op trans_w, int64
                                           int32_t want_dx, int32_t want_dab, uint64_t* bytes)
 {
     if (!bytes) return api_fail(SAM_ERR_INVALID_ARG, "bytes is null");
-    const Call c = backward_call(dtype, trans_w, M, N, K, n_adapters, rank, lddy, ldx, ldw, dtype, want_dx != 0, K,
+    const Call c = backward_call(dtype, trans_w, M, N, K, n_adapters, rank, lddy, ldx, ldw, SAM_F32, want_dx != 0, K,
                                  want_dab != 0);
     const sam_status st = check_sizes(c);
     if (st != SAM_OK) return st;

@@ -25,18 +25,23 @@ struct ShrinkSide {
     const void* A;       // [n][r] rows, row stride lda
     long long lda;
     int K;
-    float* t32;          // [ksplit][M][rp]: scaled T (partial sums over K when ksplit > 1), or null
-    void* t16;           // [M][2 rp]: T / factor, rounded (first rp) and the rest (last rp), or null
-    float* factor;       // [M]: the power of two that t16 was divided by, or null (with ksplit > 1 too)
+    float* t32;          // [ksplit][M][rp]: partial sums over K of the scaled T
+    // What a second kernel makes of them (with `round`):
+    int keep;            // their sum goes to the first of them
+    void* t16;           // [M][np][rp]: T / factor as np values of the operands' type that add up to it, or null
+    float* factor;       // [M]: the power of two that t16 was divided by, or null
 };
 
 struct ShrinkArgs {
     ShrinkSide side[2];
     int sides;
-    int M, n, r, rp;     // rp = r rounded up to 16
+    int M, n, r, rp;     // rp = r rounded up to 16, 32, 64 or 128
     const int* ids;
     const float* scale;  // [n] or null (1)
-    int ksplit;          // K ranges, a workgroup each (t16 only with 1)
+    int np;              // 2, or 3 (bfloat16: then the values are exactly T)
+    int wide;            // 64 rows a workgroup, else 16 rows x 16 ranks
+    int round;
+    int ksplit;          // K ranges, a workgroup each
     int slots;           // workgroups sharing the distinct adapters of a row block
     // Grouping of rows by adapter, done by n further workgroups (backward):
     int* order;          // [M] rows sorted by adapter, in row order inside one; null: no grouping
@@ -67,6 +72,7 @@ struct AdapterRing {
     int n, r, rp, M, N;
     const int* ids;
     const void* t16;
+    int np;              // values that a T is made of (ShrinkArgs)
     const float* factor;
     void* Y;
     long long ldy;
@@ -99,18 +105,23 @@ struct OuterArgs {
     int max_chunks;      // ceil(M / chunk) + min(n, M)
 };
 
+constexpr int kMaxPads = 5;
+// Up to kMaxPads copies of 16-bit operands in one launch.
+hipError_t launch_adapter_pad(const PadCopy* c, int n, hipStream_t s);
 hipError_t launch_adapter_shrink(int dtype, const ShrinkArgs& a, hipStream_t s);
 hipError_t launch_adapter_finish(int dtype, const FinishArgs& a, hipStream_t s);
 hipError_t launch_adapter_outer(int dtype, const OuterArgs& a, hipStream_t s);
 // Tiles of the ring kernels used here. `tile` 0: 256 x 256, 1: 192 x 256, 2:
 // 128 x 128 (with the adapters' term, or split-K partials with `x` null), 3:
 // 64 x 128, 4: 32 x 128, 5: 16 x 128 (partials only). bt: W given as n rows of
-// K; g.N is n, the product's columns, rounded up to 8.
+// K; g.N is n, the product's columns, rounded up to 8. `shrink`, with tiles 3
+// to 5: workgroups of the same launch that make T's partial sums (not null; no
+// rows: none).
 struct AdapterTile {
     int bm, bn;
 };
 AdapterTile adapter_tile(int tile);
 hipError_t launch_adapter_ring(int tile, int dtype, int bt, const GemmArgs& g, int n, const AdapterRing* x,
-                               hipStream_t s);
+                               const ShrinkArgs* shrink, hipStream_t s);
 
 }  // namespace sam

@@ -3,6 +3,7 @@
 // partials with the adapters' term (finish), and the gradients of the
 // adapters (outer). sam_adapter.h has the formulas.
 #include "sam_adapter.h"
+#include "sam_adapter_shrink.h"
 #include "sam_ring16.h"
 
 namespace sam {
@@ -35,14 +36,28 @@ __device__ __forceinline__ void split_bits(float v, unsigned short& hi, unsigned
     lo = fabsf(v) < INFINITY ? to_bits<DT>(rest) : (unsigned short)0;
 }
 
-constexpr int kShrinkWaves = 8;
+// v as three bfloat16 values that add up to it exactly: 8 of its 24 bits each
+// (those under 2^-133 vanish). Inf and NaN leave nothing.
+__device__ __forceinline__ void split3_bits(float v, unsigned short (&o)[3])
+{
+    const bool fine = fabsf(v) < INFINITY;
+    const unsigned h = __float_as_uint(v) & 0xFFFF0000u;
+    const float r1 = v - __uint_as_float(h);
+    const unsigned m = __float_as_uint(r1) & 0xFFFF0000u;
+    const float r2 = r1 - __uint_as_float(m);
+    o[0] = fine ? (unsigned short)(h >> 16) : to_bits<DT_BF16>(v);
+    o[1] = fine ? (unsigned short)(m >> 16) : (unsigned short)0;
+    o[2] = fine ? (unsigned short)(__float_as_uint(r2) >> 16) : (unsigned short)0;
+}
+
+constexpr int kShrinkWaves = 4, kWideRows = 64;
 
 // Rows sorted by adapter, one workgroup per adapter: it counts the valid ids
 // below its own (where its rows start) and writes its rows in row order.
-__device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad)
+template <int NW>
+__device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad, int (&sums)[NW])
 {
-    constexpr int NT = kShrinkWaves * 64;
-    __shared__ int sums[kShrinkWaves];
+    constexpr int NT = NW * 64;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int below = 0;
     for (int m = tid; m < a.M; m += NT) below += (unsigned)a.ids[m] < (unsigned)ad;
@@ -52,7 +67,7 @@ __device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad)
     __syncthreads();
     int at = 0;
 #pragma unroll
-    for (int w = 0; w < kShrinkWaves; ++w) at += sums[w];
+    for (int w = 0; w < NW; ++w) at += sums[w];
     if (tid == 0) a.seg[ad] = at;
     for (int m0 = 0; m0 < a.M; m0 += NT) {
         const int m = m0 + tid;
@@ -63,7 +78,7 @@ __device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad)
         __syncthreads();
         int before = at;
 #pragma unroll
-        for (int w = 0; w < kShrinkWaves; ++w) {
+        for (int w = 0; w < NW; ++w) {
             before += w < wave ? sums[w] : 0;
             at += sums[w];
         }
@@ -72,252 +87,315 @@ __device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad)
     if (tid == 0 && ad == a.n - 1) a.seg[a.n] = at;
 }
 
-// T of 16 rows: for each distinct adapter among them (a slot), X A[ad]^T on
-// 16x16x32 blocks, the workgroup's eight waves taking pieces of 64 values of
-// K in turn and adding up through LDS in wave order. Both operands are
-// K-contiguous, so fragments come straight from memory: a lane holds 16
-// consecutive values of K of one row (32 bytes), the first eight for one MFMA
-// and the others for the next, the same for both operands. Rows of other
-// adapters read zeros and are not written.
-// Bound by reading X once; A[ad] comes from L2.
-template <int DT, int NR>
+// Rounds a row of T, held by 32 threads (column c0 + 32 q): divides by the
+// power of two below the row's largest value. A row of zeros gets the
+// smallest one (it then never sets the scale of rows that are added up with
+// it), one with Inf or NaN gets 1.
+template <int DT, int NQ>
+__device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide& sd, const float (&t)[NQ], float big,
+                                          bool odd, long long m, int c0, bool mine)
+{
+#pragma unroll
+    for (int s = 16; s; s >>= 1) {
+        big = fmaxf(big, __shfl_xor(big, s));
+        odd |= __shfl_xor((int)odd, s) != 0;
+    }
+    int e = big > 0.0f ? ilogbf(big) : -126;
+    e = odd ? 0 : (e < -126 ? -126 : e);
+    if (mine && c0 == 0) sd.factor[m] = ldexpf(1.0f, e);
+    if (!mine || !sd.t16) return;
+    unsigned short* o = static_cast<unsigned short*>(sd.t16) + m * a.np * a.rp;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+        const int c = c0 + 32 * q;
+        if (c >= a.rp) continue;
+        const float v = ldexpf(t[q], -e);
+        if (DT == DT_BF16 && a.np == 3) {
+            unsigned short p[3];
+            split3_bits(v, p);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) o[i * a.rp + c] = p[i];
+        } else {
+            unsigned short hi, lo;
+            split_bits<DT>(v, hi, lo);
+            o[c] = hi;
+            o[a.rp + c] = lo;
+        }
+    }
+}
+
+// T of up to 128 rows.
+template <int DT>
 __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_kernel(ShrinkArgs a)
+{
+    __shared__ int sums[kShrinkWaves];
+    const int wgs = shrink_wgs(a);
+    if ((int)blockIdx.x >= wgs)
+        group_rows(a, blockIdx.x - wgs, sums);
+    else
+        shrink_part<DT, kShrinkWaves>(a, blockIdx.x);
+}
+
+// T of 64 rows over one range of K, for calls with many rows: for each
+// distinct adapter among them a product of 64 rows and RP ranks. Both operands
+// go straight into LDS, rows of 128 bytes or 256 a wave instruction (loads
+// into fragments would touch 64 lines per KB: measured at 4096 x 11008, rank
+// 64, 54 us, this 39 us), through a ring of NBUF stages; wave w has rows
+// 16 w .. + 15. The partial sums of the K ranges are added, and rounded, by
+// adapter_round_kernel.
+// Bound by reading X once: A's traffic from L2 is r / 64 of X's.
+template <int DT, int NR>
+__global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_wide_kernel(ShrinkArgs a)
 {
     using namespace dma;
     constexpr int NW = kShrinkWaves;
     constexpr int RP = 16 * NR;
-    constexpr int BATCH = NR <= 2 ? 4 : (NR <= 4 ? 2 : 1);   // pieces of K loaded ahead of their MFMAs
-    __shared__ float part[NW][16][RP + 4];
+    constexpr int BK = NR == 1 ? 128 : 64;                 // the waves' loads of A must come out even
+    constexpr int ROW = BK * 2, CP = ROW / 16, RPL = 64 / CP, RSW = 16 / CP;   // as in the ring kernels
+    constexpr int XB = kWideRows * ROW, STAGE = XB + RP * ROW;
+    constexpr int X_PW = XB / 1024 / NW, A_PW = RP * ROW / 1024 / NW, LPS = X_PW + A_PW;
+    constexpr int NBUF = 80 * 1024 / STAGE;                // two workgroups a CU
+    static_assert(A_PW * 1024 * NW == RP * ROW && NBUF >= 3 && (NBUF - 1) * LPS < 64, "ring");
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[NBUF * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int blocks = (a.M + 15) / 16;
+    const int blocks = (a.M + kWideRows - 1) / kWideRows;
     int wg = blockIdx.x;
-    const int per_side = blocks * a.slots * a.ksplit;
+    const int per_side = blocks * a.ksplit;
     if (wg >= per_side * a.sides) {
-        group_rows(a, wg - per_side * a.sides);
+        group_rows(a, wg - per_side * a.sides, *reinterpret_cast<int(*)[NW]>(lds));
         return;
     }
     const ShrinkSide& sd = a.side[wg >= per_side];
     if (wg >= per_side) wg -= per_side;
-    const int split = wg / (blocks * a.slots);
-    wg -= split * blocks * a.slots;
-    const int m0 = (wg / a.slots) * 16;
-    const int slot = wg % a.slots;
-    const int K = sd.K;
-    const int pieces = (K + 63) / 64;
-    const int p0 = (int)((long long)pieces * split / a.ksplit), p1 = (int)((long long)pieces * (split + 1) / a.ksplit);
+    const int split = wg / blocks;
+    const int m0 = (wg - split * blocks) * kWideRows;
+    const int stages = (sd.K + BK - 1) / BK;
+    const int st0 = (int)((long long)stages * split / a.ksplit);
+    const int nk = (int)((long long)stages * (split + 1) / a.ksplit) - st0;
 
-    const int row = lane & 15, grp = lane >> 4;
-    int id = m0 + row < a.M ? a.ids[m0 + row] : -1;
+    int id = m0 + lane < a.M ? a.ids[m0 + lane] : -1;
     if ((unsigned)id >= (unsigned)a.n) id = -1;
-    unsigned left = (unsigned)(__ballot(id >= 0) & 0xFFFFull);
-    const __amdgpu_buffer_rsrc_t rX =
-        make_rsrc(static_cast<const char*>(sd.X) + (long long)m0 * sd.ldx * 2, (long long)(a.M - m0) * sd.ldx * 2);
+    unsigned long long left = __ballot(id >= 0);
+    const i4 rX = rsrc_words(static_cast<const char*>(sd.X) + (long long)m0 * sd.ldx * 2, (long long)(a.M - m0) * sd.ldx * 2);
+    const int lrow = lane & 15, grp = lane >> 4;
 
-    for (int d = 0; left; ++d) {
-        const int ad = __builtin_amdgcn_readlane(id, __ffs((int)left) - 1);
-        const unsigned same = (unsigned)(__ballot(id == ad) & 0xFFFFull);
+    while (left) {
+        const int ad = __builtin_amdgcn_readlane(id, __ffsll((long long)left) - 1);
+        const unsigned long long same = __ballot(id == ad);
         left &= ~same;
-        if (d % a.slots != slot) continue;
-        const __amdgpu_buffer_rsrc_t rA = make_rsrc(static_cast<const char*>(sd.A) + (long long)ad * a.r * sd.lda * 2,
-                                                    (long long)a.r * sd.lda * 2);
-        const int xrow = (same >> row) & 1 ? (int)(row * sd.ldx * 2) : kOOB;
+        const i4 rA = rsrc_words(static_cast<const char*>(sd.A) + (long long)ad * a.r * sd.lda * 2,
+                                 (long long)a.r * sd.lda * 2);
+        // Stages past the last one read zeros: the waits count on every load.
+        auto load = [&](int st) {
+            unsigned char* buf = lds + st % NBUF * STAGE;
+#pragma unroll
+            for (int q = 0; q < LPS; ++q) {
+                const bool x = q < X_PW;
+                const int I = wave + (x ? q : q - X_PW) * NW;
+                const int row = I * RPL + lane / CP;
+                const int k = (st0 + st) * BK + (lane % CP ^ row / RSW % CP) * 8;
+                const bool ok = st < nk && k < sd.K && (x ? (same >> row) & 1 : row < a.r);
+                const int off = ok ? (int)((row * (x ? sd.ldx : sd.lda) + k) * 2) : kOOB;
+                lds_load16(x ? rX : rA, lds_addr(buf + (x ? 0 : XB) + I * 1024), off);
+            }
+        };
         v4f acc[NR];
 #pragma unroll
         for (int q = 0; q < NR; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int p = p0 + wave; p < p1; p += NW * BATCH) {
-            u4 fx[BATCH][2], fa[BATCH][NR][2];
+        wait_cnt<0, 15>();   // the counts below are of the ring's loads alone
 #pragma unroll
-            for (int b = 0; b < BATCH; ++b) {
-                const int k = (p + b * NW) * 64 + 16 * grp;
-                const bool in = p + b * NW < p1;
+        for (int st = 0; st < NBUF - 1; ++st) load(st);
+        for (int st = 0; st < nk; ++st) {
+            wait_cnt<(NBUF - 2) * LPS, 0>();   // this wave's part of the stage is there; its reads of the last one are done
+            barrier();
+            load(st + NBUF - 1);               // into the stage that all waves have left
+            const unsigned char* buf = lds + st % NBUF * STAGE;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const bool ok = in && k + 8 * h < K;
-                    fx[b][h] = __builtin_amdgcn_raw_buffer_load_b128(rX, ok && xrow != kOOB ? xrow + (k + 8 * h) * 2 : kOOB, 0, 0);
+            for (int t = 0; t < BK / 32; ++t) {
+                auto piece = [&](const unsigned char* base, int row) {
+                    return *reinterpret_cast<const u4*>(base + row * ROW + (4 * t + grp ^ row / RSW % CP) * 16);
+                };
+                const u4 fx = piece(buf, 16 * wave + lrow);
 #pragma unroll
-                    for (int q = 0; q < NR; ++q)
-                        fa[b][q][h] = __builtin_amdgcn_raw_buffer_load_b128(
-                            rA, ok && 16 * q + row < a.r ? (int)(((16 * q + row) * sd.lda + k + 8 * h) * 2) : kOOB, 0, 0);
-                }
+                for (int q = 0; q < NR; ++q) Mf<DT, 16>::mfma(acc[q], fx, piece(buf + XB, 16 * q + lrow));
             }
-#pragma unroll
-            for (int b = 0; b < BATCH; ++b)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int q = 0; q < NR; ++q) Mf<DT, 16>::mfma(acc[q], fx[b][h], fa[b][q][h]);
         }
-        __syncthreads();   // the last slot's sums are read
-#pragma unroll
-        for (int q = 0; q < NR; ++q)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) part[wave][4 * grp + v][16 * q + row] = acc[q][v];
-        __syncthreads();
-        // 32 threads per row.
-        const int orow = tid >> 5, c0 = tid & 31;
-        const bool mine = (same >> orow) & 1;
+        // Nothing in flight, nothing unread, before the ring is filled again.
+        wait_cnt<0, 0>();
+        barrier();
         const float f = a.scale ? a.scale[ad] : 1.0f;
-        float t[(RP + 31) / 32], big = 0.0f;
-        bool odd = false;   // an Inf or a NaN in the row
 #pragma unroll
-        for (int q = 0; q < (RP + 31) / 32; ++q) {
-            const int c = c0 + 32 * q;
-            float v = 0.0f;
-            if (c < RP)
+        for (int v = 0; v < 4; ++v) {
+            const int row = 16 * wave + 4 * grp + v;
+            if (!((same >> row) & 1)) continue;
+            float* o = sd.t32 + ((long long)split * a.M + m0 + row) * RP + lrow;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) v += part[w][orow][c];
-            t[q] = c < a.r ? v * f : 0.0f;   // ranks past r: zeros also where X holds Inf
-            big = fmaxf(big, fabsf(t[q]));
-            odd |= !(fabsf(t[q]) < INFINITY);
-        }
-        const long long m = m0 + orow;
-        if (sd.t32 && mine)
-#pragma unroll
-            for (int q = 0; q < (RP + 31) / 32; ++q)
-                if (c0 + 32 * q < RP) sd.t32[((long long)split * a.M + m) * RP + c0 + 32 * q] = t[q];
-        if (sd.factor) {
-#pragma unroll
-            for (int s = 16; s; s >>= 1) {
-                big = fmaxf(big, __shfl_xor(big, s));
-                odd |= __shfl_xor((int)odd, s) != 0;
-            }
-            // Divide by the power of two below the row's largest value. A row
-            // of zeros gets the smallest one (it then never sets the scale of
-            // rows that are added up with it), one with Inf or NaN gets 1.
-            int e = big > 0.0f ? ilogbf(big) : -126;
-            e = odd ? 0 : (e < -126 ? -126 : e);
-            if (mine && c0 == 0) sd.factor[m] = ldexpf(1.0f, e);
-            if (mine && sd.t16) {
-                unsigned short* o = static_cast<unsigned short*>(sd.t16) + m * 2 * RP;
-#pragma unroll
-                for (int q = 0; q < (RP + 31) / 32; ++q) {
-                    const int c = c0 + 32 * q;
-                    unsigned short hi, lo;
-                    split_bits<DT>(ldexpf(t[q], -e), hi, lo);
-                    if (c < RP) {
-                        o[c] = hi;
-                        o[RP + c] = lo;
-                    }
-                }
-            }
+            for (int q = 0; q < NR; ++q)   // ranks past r: zeros also where X holds Inf
+                o[16 * q] = 16 * q + lrow < a.r ? acc[q][v] * f : 0.0f;
         }
     }
+}
+
+// The sum of a row's partials in K order, into the first of them, and its
+// rounded form. 32 threads per row, rows without an adapter left out.
+template <int DT, int NQ>
+__global__ void __launch_bounds__(256) adapter_round_kernel(ShrinkArgs a)
+{
+    const int c0 = threadIdx.x & 31;
+    const int m = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const ShrinkSide& sd = a.side[blockIdx.y];
+    const int id = m < a.M ? a.ids[m] : -1;
+    const bool mine = (unsigned)id < (unsigned)a.n;
+    float t[NQ], big = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+        const int c = c0 + 32 * q;
+        float v = 0.0f;
+        const float* p = sd.t32 + (long long)m * a.rp + c;
+        const long long step = (long long)a.M * a.rp;
+        for (int s0 = 0; s0 < a.ksplit; s0 += 8) {
+            float w[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) w[u] = mine && c < a.rp && s0 + u < a.ksplit ? p[(s0 + u) * step] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += w[u];
+        }
+        t[q] = v;
+        big = fmaxf(big, fabsf(v));
+        odd |= !(fabsf(v) < INFINITY);
+        if (sd.keep && a.ksplit > 1 && mine && c < a.rp) sd.t32[(long long)m * a.rp + c] = v;
+    }
+    if (sd.factor) round_row<DT, NQ>(a, sd, t, big, odd, m, c0, mine);
+}
+
+// 4 values of B as floats.
+template <int DT>
+__device__ __forceinline__ void floats_of(const uint2& w, float (&o)[4])
+{
+    o[0] = from_bits<DT>((unsigned short)w.x);
+    o[1] = from_bits<DT>((unsigned short)(w.x >> 16));
+    o[2] = from_bits<DT>((unsigned short)w.y);
+    o[3] = from_bits<DT>((unsigned short)(w.y >> 16));
 }
 
 // Y[m][c] = sum over splits of part, in split order, + sum_i T[m][i] B[a][i][c].
-// One wave per 256 columns of four rows; rows of one adapter share its loads.
-template <int DT>
-__device__ __forceinline__ void load_h4(const unsigned short* p, bool vec, int left, float (&o)[4])
+// A wave has 256 columns of a row. WS 4: the four waves of a workgroup share
+// one row's sums, a quarter of the partials and of the ranks each, and add up
+// in wave order; WS 1: a row each, four rows a workgroup (B of one adapter
+// then comes from L1 for three of them).
+// Bound by latency: nothing that is loaded depends on anything but the row's
+// id, so all first loads go out before the first is used. Measured at 64 rows
+// x 11008, rank 16, 5 partials: 11 us (one load at a time 39).
+template <int DT, int WS>
+__global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
 {
-    unsigned short b[4] = {0, 0, 0, 0};
-    if (vec) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        b[0] = (unsigned short)w.x; b[1] = (unsigned short)(w.x >> 16);
-        b[2] = (unsigned short)w.y; b[3] = (unsigned short)(w.y >> 16);
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (q < left) b[q] = p[q];
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] = from_bits<DT>(b[q]);
-}
-
-template <int DT, int ROWS>
-__global__ void __launch_bounds__(64) adapter_finish_kernel(FinishArgs a)
-{
-    __shared__ float t[ROWS][kMaxRank];
-    const int lane = threadIdx.x;
+    constexpr int U = 8;   // loads of a kind under way at once
+    __shared__ float4 red[3][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int strips = (a.N + 255) / 256;
-    const int m0 = (blockIdx.x / strips) * ROWS, c = (blockIdx.x % strips) * 256 + 4 * lane;
-    const int rows = min(ROWS, a.M - m0);
-    int id[ROWS];
-    bool same = true;
+    const int m = WS == 4 ? blockIdx.x / strips : blockIdx.x / strips * 4 + wave;
+    if (WS == 1 && m >= a.M) return;
+    const int c = (blockIdx.x % strips) * 256 + 4 * lane;
+    const int left = a.N - c, cc = left > 0 ? c : 0;   // lanes past N read the first columns
+    const int p = WS == 4 ? wave : 0;
+    const int s0 = a.split * p / WS, s1 = a.split * (p + 1) / WS;
+    const int i0 = a.r * p / WS, i1 = a.r * (p + 1) / WS;
+    int id = a.ids[m];
+    if ((unsigned)id >= (unsigned)a.n || i0 == i1) id = -1;
+
+    float4 w[U];
+    auto load_parts = [&](int s) {
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        id[q] = q < rows ? a.ids[m0 + q] : -1;
-        if ((unsigned)id[q] >= (unsigned)a.n) id[q] = -1;
-        same &= id[q] == id[0];
-    }
+        for (int u = 0; u < U; ++u)
+            w[u] = *reinterpret_cast<const float4*>(a.part + ((long long)min(s + u, a.split - 1) * a.M + m) * a.ldp + cc);
+    };
+    // T of the wave's ranks, a lane each (two with more than 64), summed over its own partials.
+    float t[2] = {0.0f, 0.0f};
+    uint2 wb[U];
+    const unsigned short* B = static_cast<const unsigned short*>(a.B) + (long long)max(id, 0) * a.r * a.ldb + cc;
+    auto load_b = [&](int i) {
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q)
-        for (int i = lane; i < a.r; i += 64) {
-            float v = 0.0f;
-            if (id[q] >= 0)
-                for (int s = 0; s < a.tsplit; ++s) v += a.t32[((long long)s * a.M + m0 + q) * a.rp + i];
-            t[q][i] = v;
-        }
-    __syncthreads();
-    if (c >= a.N) return;
-    const int left = a.N - c;
-    float y[ROWS][4];
+        for (int u = 0; u < U; ++u) wb[u] = *reinterpret_cast<const uint2*>(B + min(i + u, i1 - 1) * a.ldb);
+    };
+    load_parts(s0);
+    if (id >= 0) {
+        load_b(i0);
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
+        for (int q = 0; q < (WS == 4 ? 1 : 2); ++q) {
+            const int i = i0 + 64 * q + lane;
+            const float* tp = a.t32 + (long long)m * a.rp + min(i, i1 - 1);
+            const long long step = (long long)a.M * a.rp;
+            for (int s = 0; s < a.tsplit; s += U) {
+                float x[U];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) y[q][v] = 0.0f;
-        if (q >= rows) continue;
-        for (int s = 0; s < a.split; ++s) {
-            const float4 w = *reinterpret_cast<const float4*>(a.part + ((long long)s * a.M + m0 + q) * a.ldp + c);
-            y[q][0] += w.x; y[q][1] += w.y; y[q][2] += w.z; y[q][3] += w.w;
-        }
-    }
-    const unsigned short* B = static_cast<const unsigned short*>(a.B);
-    const bool vb = a.ldb % 4 == 0 && left >= 4;
-    float z[ROWS][4];
+                for (int u = 0; u < U; ++u) x[u] = tp[min(s + u, a.tsplit - 1) * step];
 #pragma unroll
-    for (int q = 0; q < ROWS; ++q)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) z[q][v] = 0.0f;
-    if (same) {
-        if (id[0] >= 0)
-            for (int i = 0; i < a.r; ++i) {
-                float b[4];
-                load_h4<DT>(B + ((long long)id[0] * a.r + i) * a.ldb + c, vb, left, b);
-#pragma unroll
-                for (int q = 0; q < ROWS; ++q)
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) z[q][v] = fmaf(t[q][i], b[v], z[q][v]);
+                for (int u = 0; u < U; ++u) t[q] += s + u < a.tsplit ? x[u] : 0.0f;
             }
+        }
+    }
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = s0; s < s1;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s + u < s1) {
+                y.x += w[u].x; y.y += w[u].y; y.z += w[u].z; y.w += w[u].w;
+            }
+        s += U;
+        if (s < s1) load_parts(s);
+    }
+    if (id >= 0)
+        for (int i = i0; i < i1;) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u < i1) {
+                    const int j = i + u - i0;
+                    const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(t[WS == 4 ? 0 : j >> 6]), j & 63));
+                    y.x = fmaf(f, from_bits<DT>((unsigned short)wb[u].x), y.x);
+                    y.y = fmaf(f, from_bits<DT>((unsigned short)(wb[u].x >> 16)), y.y);
+                    y.z = fmaf(f, from_bits<DT>((unsigned short)wb[u].y), y.z);
+                    y.w = fmaf(f, from_bits<DT>((unsigned short)(wb[u].y >> 16)), y.w);
+                }
+            i += U;
+            if (i < i1) load_b(i);
+        }
+    if constexpr (WS == 4) {
+        if (wave) red[wave - 1][lane] = y;
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const float4 x = red[q][lane];
+            y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+        }
+    }
+    if (left <= 0) return;
+    // Four values at a time also where the row does not start on 8 or 16
+    // bytes: the hardware's unaligned stores.
+    const float v[4] = {y.x, y.y, y.z, y.w};
+    const long long off = (long long)m * a.ldy + c;
+    if (a.out16) {
+        unsigned short h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = to_bits<DT>(v[q]);
+        unsigned short* o = static_cast<unsigned short*>(a.Y) + off;
+        if (left >= 4)
+            __builtin_memcpy(o, h, 8);
+        else
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+                if (q < left) o[q] = h[q];
     } else {
+        float* o = static_cast<float*>(a.Y) + off;
+        if (left >= 4)
+            __builtin_memcpy(o, v, 16);
+        else
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-            if (id[q] < 0) continue;
-            for (int i = 0; i < a.r; ++i) {
-                float b[4];
-                load_h4<DT>(B + ((long long)id[q] * a.r + i) * a.ldb + c, vb, left, b);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) z[q][v] = fmaf(t[q][i], b[v], z[q][v]);
-            }
-        }
-    }
-    const bool vy = a.N % 4 == 0 && a.ldy % 4 == 0;
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-        if (q >= rows) continue;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) y[q][v] += z[q][v];
-        const long long off = (long long)(m0 + q) * a.ldy + c;
-        if (a.out16) {
-            unsigned short h[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) h[v] = to_bits<DT>(y[q][v]);
-            unsigned short* o = static_cast<unsigned short*>(a.Y) + off;
-            if (vy)
-                *reinterpret_cast<uint2*>(o) = make_uint2(h[0] | (unsigned)h[1] << 16, h[2] | (unsigned)h[3] << 16);
-            else
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (v < left) o[v] = h[v];
-        } else {
-            float* o = static_cast<float*>(a.Y) + off;
-            if (vy)
-                *reinterpret_cast<float4*>(o) = make_float4(y[q][0], y[q][1], y[q][2], y[q][3]);
-            else
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (v < left) o[v] = y[q][v];
-        }
+            for (int q = 0; q < 3; ++q)
+                if (q < left) o[q] = v[q];
     }
 }
 
@@ -373,18 +451,25 @@ constexpr int kOuterCols = 256;
 // out[ad][i][c] = sum over a chunk's rows m of T[m][i] X[m][c], for 256
 // columns c: MFMA with the rows as its K, 32 a step. X rows come through
 // registers into LDS (their order is the grouping's, so each lane has its own
-// address) and are read with the transposing LDS read; T is divided by a
-// power of two common to the chunk (from the rows' factors, so that binary16
-// keeps it), split into a 16-bit value and its 16-bit remainder and read the
-// same way: two MFMAs a block, the sum right to 2^-17 (bf16) or 2^-22.
-// Bound by reading X once. Chunks of adapters with one chunk go to `out`,
-// others to `part`, which outer_sum adds in order.
+// address) and are read with the transposing LDS read; T is split into 16-bit
+// values, an MFMA each, and read the same way. bfloat16: three values, exactly
+// T. binary16: T divided by a power of two common to the chunk (from the rows'
+// factors, so that the type's range keeps it), a value and its remainder, the
+// sum right to 2^-22 of the chunk's largest.
+// Bound by reading X once. Measured at X, dY 4096 x 4096, rank 16, 8
+// adapters in runs: 24 us (with the look-up of every row's place in
+// front of its load 26 us; loads two steps ahead spill).
+// Chunks of adapters with one chunk go to `out`, others to `part`, which
+// outer_sum adds in order.
 template <int DT, int NR>
 __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
 {
     using namespace dma;
     constexpr int RP = 16 * NR;
-    constexpr int TROW = 2 * RP < 64 ? 64 : 2 * RP;           // values per T row in LDS
+    constexpr int NP = DT == DT_BF16 ? 3 : 2;
+    // Values per T row in LDS; not a multiple of 128 bytes, so that the four
+    // rows of a transposing read fall on different banks.
+    constexpr int TROW = NP * RP + (NP * RP % 64 == 0 ? 8 : 0);
     constexpr int XB = 32 * kOuterCols * 2, TB = 32 * TROW * 2;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[2][XB + TB];
     __shared__ float fmax_s[4];
@@ -402,16 +487,22 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
     const int begin = a.seg[ad] + (ch - w.first) * a.chunk;
     const int rows = min(a.chunk, a.seg[ad + 1] - begin);
     const int* order = a.order + begin;
+    // Rows of one run need no look-up: a load less in front of X's.
+    const int row0 = order[0];
+    const bool run = order[rows - 1] - row0 == rows - 1;
 
     // The chunk's scale: the largest of its rows' factors.
-    float big = 0.0f;
-    for (int m = tid; m < rows; m += 256) big = fmaxf(big, sd.factor[order[m]]);
+    int e = 0;
+    if constexpr (DT == DT_F16) {
+        float big = 0.0f;
+        for (int m = tid; m < rows; m += 256) big = fmaxf(big, sd.factor[order[m]]);
 #pragma unroll
-    for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
-    if (lane == 0) fmax_s[wave] = big;
-    __syncthreads();
-    big = fmaxf(fmaxf(fmax_s[0], fmax_s[1]), fmaxf(fmax_s[2], fmax_s[3]));
-    const int e = ilogbf(big);   // factors are powers of two, at least 2^-126
+        for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
+        if (lane == 0) fmax_s[wave] = big;
+        __syncthreads();
+        big = fmaxf(fmaxf(fmax_s[0], fmax_s[1]), fmaxf(fmax_s[2], fmax_s[3]));
+        e = ilogbf(big);   // factors are powers of two, at least 2^-126
+    }
 
     // Loads of step s into registers: X 32 rows x 512 bytes, four 16-byte
     // pieces a thread; T 32 rows x RP floats, RP / 8 a thread.
@@ -424,14 +515,17 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
         for (int q = 0; q < 4; ++q) {
             const int i = s * 32 + q * 8 + (tid >> 5), c = c0 + (tid & 31) * 8;
             rx[q] = u4{0u, 0u, 0u, 0u};
-            if (i < rows && c < sd.cols)
-                rx[q] = *reinterpret_cast<const u4*>(static_cast<const unsigned short*>(sd.X) + (long long)order[i] * sd.ldx + c);
+            if (i < rows && c < sd.cols) {
+                const long long m = run ? row0 + i : order[i];
+                rx[q] = *reinterpret_cast<const u4*>(static_cast<const unsigned short*>(sd.X) + m * sd.ldx + c);
+            }
         }
         const int i = s * 32 + trow;
 #pragma unroll
         for (int q = 0; q < TP; ++q) rt[q] = 0.0f;
         if (i < rows) {
-            const float* p = sd.t32 + (long long)order[i] * RP + tc;
+            const long long m = run ? row0 + i : order[i];
+            const float* p = sd.t32 + m * RP + tc;
 #pragma unroll
             for (int q = 0; q < TP; q += 2) {
                 const float2 v = *reinterpret_cast<const float2*>(p + q);
@@ -450,11 +544,17 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
         }
 #pragma unroll
         for (int q = 0; q < TP; q += 2) {
-            unsigned short h0, l0, h1, l1;
-            split_bits<DT>(ldexpf(rt[q], -e), h0, l0);
-            split_bits<DT>(ldexpf(rt[q + 1], -e), h1, l1);
-            *reinterpret_cast<unsigned*>(tb + (trow * TROW + tc + q) * 2) = h0 | (unsigned)h1 << 16;
-            *reinterpret_cast<unsigned*>(tb + (trow * TROW + RP + tc + q) * 2) = l0 | (unsigned)l1 << 16;
+            unsigned short h[2][NP];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if constexpr (NP == 3)
+                    split3_bits(rt[q + k], h[k]);
+                else
+                    split_bits<DT>(ldexpf(rt[q + k], -e), h[k][0], h[k][1]);
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                *reinterpret_cast<unsigned*>(tb + (trow * TROW + k * RP + tc + q) * 2) = h[0][k] | (unsigned)h[1][k] << 16;
         }
     };
     const int grp = lane >> 4, s16 = lane & 15;
@@ -463,12 +563,7 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const int steps = (rows + 31) / 32;
-    load(0);
-    for (int s = 0; s < steps; ++s) {
-        put(s);
-        if (s + 1 < steps) load(s + 1);
-        __syncthreads();
+    auto multiply = [&](int s) {
         const unsigned char* xb = lds[s & 1];
         const unsigned char* tb = xb + XB;
         u4 fx[4];
@@ -486,7 +581,7 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
             fx[j] = u4{h[0][0], h[0][1], h[1][0], h[1][1]};
         }
 #pragma unroll
-        for (int i = 0; i < 2 * NR; ++i) {
+        for (int i = 0; i < NP * NR; ++i) {
             u2 h[2];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -499,6 +594,16 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
 #pragma unroll
             for (int j = 0; j < 4; ++j) Mf<DT, 16>::mfma(acc[i % NR][j], ft, fx[j]);
         }
+    };
+    // A step's values are in LDS from its `put` to the barrier after the next
+    // one's: two buffers, one barrier a step.
+    const int steps = (rows + 31) / 32;
+    load(0);
+    for (int s = 0; s < steps; ++s) {
+        put(s);
+        load(s + 1);   // past the last step: nothing is read
+        __syncthreads();
+        multiply(s);
     }
     const bool direct = w.count == 1;
     float* o = direct ? sd.out + (long long)ad * a.r * sd.cols : sd.part + (long long)ch * a.r * sd.cols;
@@ -537,24 +642,83 @@ __global__ void __launch_bounds__(256) adapter_outer_sum_kernel(OuterArgs a)
         const long long i = at + 256 * q;
         if (i >= vals) continue;
         float v = 0.0f;
-        for (int c = 0; c < w.count; ++c) v += part[(long long)c * vals + i];
+        for (int c = 0; c < w.count; c += 8) {
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = part[(long long)min(c + u, w.count - 1) * vals + i];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += c + u < w.count ? x[u] : 0.0f;
+        }
         out[i] = v;
     }
+}
+
+// Copies of operands whose rows are no whole 16-byte pieces, into rows that
+// are, zeros in the gap. A wave has up to 256 pieces of a row; source pieces
+// start on any value (the hardware's unaligned loads).
+struct PadArgs {
+    PadCopy c[kMaxPads];
+    long long first[kMaxPads];  // each copy's first wave
+    int strips[kMaxPads];       // waves per row
+    int n;
+};
+
+__global__ void __launch_bounds__(256) adapter_pad_kernel(PadArgs a)
+{
+    const long long unit = (long long)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int at = 0;
+    for (int q = 1; q < a.n; ++q)
+        if (unit >= a.first[q]) at = q;
+    const PadCopy& p = a.c[at];
+    const unsigned u = (unsigned)(unit - a.first[at]), n = (unsigned)a.strips[at];
+    const long long row = u / n;
+    if (row >= p.rows) return;
+    const unsigned short* s = static_cast<const unsigned short*>(p.src) + row * p.lds;
+    u4* d = reinterpret_cast<u4*>(static_cast<unsigned short*>(p.dst) + row * p.ldd);
+    const int cols = (int)p.cols, pieces = (int)(p.ldd / 8);
+    const int i0 = (int)(u % n) * 256 + (threadIdx.x & 63);
+    u4 v[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int i = i0 + 64 * b;
+        v[b] = u4{0u, 0u, 0u, 0u};
+        if (8 * i + 8 <= cols) {
+            __builtin_memcpy(&v[b], s + 8 * i, 16);
+        } else if (8 * i < cols) {
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (8 * i + k < cols) v[b][k >> 1] |= (unsigned)s[8 * i + k] << (16 * (k & 1));
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (i0 + 64 * b < pieces) d[i0 + 64 * b] = v[b];
 }
 
 template <int DT>
 hipError_t shrink_dt(const ShrinkArgs& a, hipStream_t s)
 {
-    const int blocks = (a.M + 15) / 16;
-    const dim3 grid((unsigned)(blocks * a.slots * a.ksplit * a.sides + (a.order ? a.n : 0)));
+    const int more = a.order ? a.n : 0;
     const dim3 block(kShrinkWaves * 64);
-    switch (a.rp / 16) {
-    case 1: hipLaunchKernelGGL((adapter_shrink_kernel<DT, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((adapter_shrink_kernel<DT, 2>), grid, block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((adapter_shrink_kernel<DT, 3>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((adapter_shrink_kernel<DT, 4>), grid, block, 0, s, a); break;
-    case 8: hipLaunchKernelGGL((adapter_shrink_kernel<DT, 8>), grid, block, 0, s, a); break;
-    default: return hipErrorInvalidValue;
+    if (a.wide) {
+        const dim3 grid((unsigned)((a.M + kWideRows - 1) / kWideRows * a.ksplit * a.sides + more));
+        switch (a.rp) {
+        case 16: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 1>), grid, block, 0, s, a); break;
+        case 32: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 2>), grid, block, 0, s, a); break;
+        case 64: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 4>), grid, block, 0, s, a); break;
+        case 128: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 8>), grid, block, 0, s, a); break;
+        default: return hipErrorInvalidValue;
+        }
+    } else {
+        hipLaunchKernelGGL((adapter_shrink_kernel<DT>), dim3((unsigned)(shrink_wgs(a) + more)), block, 0, s, a);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.round || a.M == 0) return e;
+    const dim3 rgrid((unsigned)((a.M + 7) / 8), (unsigned)a.sides), rblock(256);
+    switch ((a.rp + 31) / 32) {
+    case 1: hipLaunchKernelGGL((adapter_round_kernel<DT, 1>), rgrid, rblock, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((adapter_round_kernel<DT, 2>), rgrid, rblock, 0, s, a); break;
+    default: hipLaunchKernelGGL((adapter_round_kernel<DT, 4>), rgrid, rblock, 0, s, a); break;
     }
     return hipGetLastError();
 }
@@ -567,7 +731,6 @@ hipError_t outer_dt(const OuterArgs& a, hipStream_t s)
     if (grid.x) switch (a.rp / 16) {
     case 1: hipLaunchKernelGGL((adapter_outer_kernel<DT, 1>), grid, block, 0, s, a); break;
     case 2: hipLaunchKernelGGL((adapter_outer_kernel<DT, 2>), grid, block, 0, s, a); break;
-    case 3: hipLaunchKernelGGL((adapter_outer_kernel<DT, 3>), grid, block, 0, s, a); break;
     case 4: hipLaunchKernelGGL((adapter_outer_kernel<DT, 4>), grid, block, 0, s, a); break;
     case 8: hipLaunchKernelGGL((adapter_outer_kernel<DT, 8>), grid, block, 0, s, a); break;
     default: return hipErrorInvalidValue;
@@ -588,20 +751,37 @@ hipError_t launch_adapter_shrink(int dtype, const ShrinkArgs& a, hipStream_t s)
 
 hipError_t launch_adapter_finish(int dtype, const FinishArgs& a, hipStream_t s)
 {
+    // Four waves a row while that fills the CUs no more than four times over.
     const long long strips = (a.N + 255) / 256;
-    const int rows = a.M >= 16 ? 4 : 1;
-    const dim3 grid((unsigned)(strips * ((a.M + rows - 1) / rows)));
-    if (rows == 4) {
-        if (dtype == DT_BF16)
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_BF16, 4>), grid, dim3(64), 0, s, a);
+    const bool share = strips * a.M <= 4 * 256 * 8;
+    const dim3 grid((unsigned)(strips * (share ? a.M : (a.M + 3) / 4))), block(256);
+    if (dtype == DT_BF16) {
+        if (share)
+            hipLaunchKernelGGL((adapter_finish_kernel<DT_BF16, 4>), grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_F16, 4>), grid, dim3(64), 0, s, a);
+            hipLaunchKernelGGL((adapter_finish_kernel<DT_BF16, 1>), grid, block, 0, s, a);
     } else {
-        if (dtype == DT_BF16)
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_BF16, 1>), grid, dim3(64), 0, s, a);
+        if (share)
+            hipLaunchKernelGGL((adapter_finish_kernel<DT_F16, 4>), grid, block, 0, s, a);
         else
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_F16, 1>), grid, dim3(64), 0, s, a);
+            hipLaunchKernelGGL((adapter_finish_kernel<DT_F16, 1>), grid, block, 0, s, a);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_adapter_pad(const PadCopy* c, int n, hipStream_t s)
+{
+    PadArgs a{};
+    long long waves = 0;
+    for (int i = 0; i < n; ++i) {
+        a.c[i] = c[i];
+        a.first[i] = waves;
+        a.strips[i] = (int)((c[i].ldd / 8 + 255) / 256);
+        waves += c[i].rows * a.strips[i];
+        if (c[i].rows * a.strips[i] >= 1ll << 32) return hipErrorInvalidValue;
+    }
+    a.n = n;
+    if (waves) hipLaunchKernelGGL(adapter_pad_kernel, dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -12,6 +12,7 @@
 // neither overflows nor loses small rows; the accumulators are multiplied by
 // it before the K loop starts.
 #include "sam_adapter.h"
+#include "sam_adapter_shrink.h"
 #include "sam_ring16.h"
 
 namespace sam {
@@ -96,8 +97,8 @@ struct AdapterHook {
         constexpr int CPR = BN / 8, RPI = 64 / CPR;   // 16-byte chunks per row of B, rows per 1 KB load
         constexpr int INS = RC * BN * 2 / 1024;       // loads per chunk of ranks
         static_assert(INS % NW == 0, "loads must split evenly over waves");
-        const __amdgpu_buffer_rsrc_t rT = make_rsrc(static_cast<const char*>(x.t16) + (long long)m0 * x.rp * 4,
-                                                    (long long)(x.M - m0) * x.rp * 4);
+        const __amdgpu_buffer_rsrc_t rT = make_rsrc(static_cast<const char*>(x.t16) + (long long)m0 * x.rp * x.np * 2,
+                                                    (long long)(x.M - m0) * x.rp * x.np * 2);
         __builtin_amdgcn_sched_barrier(0);
         bool first = true;
 #pragma clang loop unroll(disable)
@@ -123,17 +124,19 @@ struct AdapterHook {
                     lds_load16(rB, lds_addr(bl + I * 1024), ok ? (int)((row * x.ldb + c * 8) * 2) : kOOB);
                 }
                 asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-                const int steps = min(RC, x.rp - r0) / 16;
+                const int steps = min(RC, x.rp - r0) / 16 * (x.np - 1);
 #pragma clang loop unroll(disable)
-                for (int t = 0; t < steps; ++t) {
+                for (int st = 0; st < steps; ++st) {
                     // T of the wave's rows: lane groups 0 and 1 hold 8 ranks
-                    // each, groups 2 and 3 the same ranks' remainders.
+                    // each, groups 2 and 3 the same ranks' remainders. Third
+                    // values take a step of their own, groups 0 and 1 alone.
+                    const int t = x.np == 3 ? st >> 1 : st, piece = x.np == 3 && (st & 1) ? 2 : 0;
                     u4 ft[TM], fb[TN];
 #pragma unroll
                     for (int i = 0; i < TM; ++i) {
                         const int row = wm0 + 16 * i + lrow;
-                        const int off = (row * 2 * x.rp + (lgrp >> 1) * x.rp + r0 + 16 * t + 8 * (lgrp & 1)) * 2;
-                        ft[i] = __builtin_amdgcn_raw_buffer_load_b128(rT, off, 0, 0);
+                        const int off = ((row * x.np + piece + (lgrp >> 1)) * x.rp + r0 + 16 * t + 8 * (lgrp & 1)) * 2;
+                        ft[i] = __builtin_amdgcn_raw_buffer_load_b128(rT, piece && lgrp > 1 ? kOOB : off, 0, 0);
                     }
 #pragma unroll
                     for (int j = 0; j < TN; ++j) {
@@ -194,41 +197,52 @@ struct AdapterHook {
             make_rsrc(static_cast<char*>(x.Y) + ((long long)m0 * x.ldy + n0) * es,
                       ((long long)(rows - 1) * x.ldy + cols) * es);
         const bool vec = x.N % 4 == 0 && x.ldy % 4 == 0;   // four columns: all inside Y, aligned to 4 values
+        auto each = [&](auto put) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int row = wm0 + 16 * i + (lane & 15);
-                const int col = wn0 + 16 * j + 4 * (lane >> 4);
-                const v4f v = acc[i][j];
-                if (x.out16) {
-                    typedef H h4 __attribute__((ext_vector_type(4)));
-                    const h4 h = {(H)v[0], (H)v[1], (H)v[2], (H)v[3]};
-                    const u2 w = __builtin_bit_cast(u2, h);
-                    if (vec) {
-                        const bool ok = row < rows && col < cols;
-                        __builtin_amdgcn_raw_buffer_store_b64(w, rY, ok ? (row * ldy + col) * 2 : kOOB, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const bool ok = row < rows && col + q < cols;
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(w[q >> 1] >> (16 * (q & 1))), rY,
-                                                                  ok ? (row * ldy + col + q) * 2 : kOOB, 0, 0);
-                        }
-                    }
-                } else if (vec) {
-                    const bool ok = row < rows && col < cols;
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), rY,
-                                                           ok ? (row * ldy + col) * 4 : kOOB, 0, 0);
+                for (int j = 0; j < TN; ++j) put(acc[i][j], wm0 + 16 * i + (lane & 15), wn0 + 16 * j + 4 * (lane >> 4));
+        };
+        auto half4 = [](const v4f& v) {
+            typedef H h4 __attribute__((ext_vector_type(4)));
+            const h4 h = {(H)v[0], (H)v[1], (H)v[2], (H)v[3]};
+            return __builtin_bit_cast(u2, h);
+        };
+        if (vec && x.out16) {
+            each([&](const v4f& v, int row, int col) {
+                const bool ok = row < rows && col < cols;
+                __builtin_amdgcn_raw_buffer_store_b64(half4(v), rY, ok ? (row * ldy + col) * 2 : kOOB, 0, 0);
+            });
+        } else if (vec) {
+            each([&](const v4f& v, int row, int col) {
+                const bool ok = row < rows && col < cols;
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), rY, ok ? (row * ldy + col) * 4 : kOOB, 0, 0);
+            });
+        } else {
+            // Rows that do not start on 8 or 16 bytes: the hardware's
+            // unaligned stores, single values at the end of a row.
+            char* Y = static_cast<char*>(x.Y) + ((long long)m0 * x.ldy + n0) * es;
+            each([&](const v4f& v, int row, int col) {
+                if (row >= rows || col >= cols) return;
+                const u4 w = x.out16 ? u4{half4(v)[0], half4(v)[1], 0u, 0u} : __builtin_bit_cast(u4, v);
+                char* o = Y + ((long long)row * ldy + col) * es;
+                if (col + 4 <= cols) {
+                    if (x.out16)
+                        __builtin_memcpy(o, &w, 8);
+                    else
+                        __builtin_memcpy(o, &w, 16);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const bool ok = row < rows && col + q < cols;
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[q]), rY,
-                                                              ok ? (row * ldy + col + q) * 4 : kOOB, 0, 0);
-                    }
+                    for (int q = 0; q < 3; ++q)
+                        if (col + q < cols) {
+                            if (x.out16)
+                                reinterpret_cast<unsigned short*>(o)[q] = (unsigned short)(w[q >> 1] >> (16 * (q & 1)));
+                            else
+                                reinterpret_cast<unsigned*>(o)[q] = w[q];
+                        }
                 }
-            }
+            });
+        }
     }
 };
 
@@ -265,13 +279,35 @@ adapter_part_kernel(GemmArgs g, int n)
                                                                               true, &n);
 }
 
+// The same for few rows, with `more` workgroups in front (a multiple of 8, so
+// that the tiles keep their XCDs) for T's partial sums, which nothing here
+// needs: a launch less, and their loads are under way beside the tiles'.
+template <int DT, int BM, int BN, int WM, int WN, int NBUF, int MODE>
+__global__ void __launch_bounds__(WM * WN * 64)
+__attribute__((amdgpu_waves_per_eu(1, ring16_waves_per_eu<BM, BN, WM, WN, 64, NBUF>())))
+adapter_part_shrink_kernel(GemmArgs g, int n, ShrinkArgs a, int more)
+{
+    if ((int)blockIdx.x < more) {
+        if ((int)blockIdx.x < shrink_wgs(a)) shrink_part<DT, WM * WN>(a, blockIdx.x);
+        return;
+    }
+    int tm, tn, s;
+    dma::tile_coords(blockIdx.x - more, g, tm, tn, s);
+    const int kbeg = s * g.k_chunk;
+    const int kend = min(g.K, kbeg + g.k_chunk);
+    ring16_segment<DT, BM, BN, WM, WN, 64, NBUF, MODE, 16, 1, false, PartHook>(g, tm, tn, kbeg, kend, nullptr, s, 0, 0,
+                                                                              true, &n);
+}
+
 typedef void (*AdapterKernelFn)(AdapterRingArgs);
 typedef void (*AdapterPartFn)(GemmArgs, int);
+typedef void (*AdapterPartShrinkFn)(GemmArgs, int, ShrinkArgs, int);
 
 struct TileKernels {
     int bm, bn, threads;
     AdapterKernelFn fused[2][2];   // [dtype - 1][bt]
     AdapterPartFn part[2][2];
+    AdapterPartShrinkFn shrink[2][2];
 };
 
 #define SAM_AD_FUSED(BM, BN, WM, WN, NBUF)                                                         \
@@ -280,15 +316,20 @@ struct TileKernels {
 #define SAM_AD_PART(BM, BN, WM, WN, NBUF)                                                          \
     {{adapter_part_kernel<DT_BF16, BM, BN, WM, WN, NBUF, 0>, adapter_part_kernel<DT_BF16, BM, BN, WM, WN, NBUF, 3>}, \
      {adapter_part_kernel<DT_F16, BM, BN, WM, WN, NBUF, 0>, adapter_part_kernel<DT_F16, BM, BN, WM, WN, NBUF, 3>}}
+#define SAM_AD_SHRINK(BM, BN, WM, WN, NBUF)                                                        \
+    {{adapter_part_shrink_kernel<DT_BF16, BM, BN, WM, WN, NBUF, 0>,                                 \
+      adapter_part_shrink_kernel<DT_BF16, BM, BN, WM, WN, NBUF, 3>},                                \
+     {adapter_part_shrink_kernel<DT_F16, BM, BN, WM, WN, NBUF, 0>,                                  \
+      adapter_part_shrink_kernel<DT_F16, BM, BN, WM, WN, NBUF, 3>}}
 #define SAM_AD_NONE {{nullptr, nullptr}, {nullptr, nullptr}}
 
 const TileKernels kTiles[] = {
-    {256, 256, 512, SAM_AD_FUSED(256, 256, 2, 4, 2), SAM_AD_NONE},
-    {192, 256, 512, SAM_AD_FUSED(192, 256, 2, 4, 2), SAM_AD_NONE},
-    {128, 128, 512, SAM_AD_FUSED(128, 128, 2, 4, 4), SAM_AD_PART(128, 128, 2, 4, 4)},
-    {64, 128, 256, SAM_AD_NONE, SAM_AD_PART(64, 128, 1, 4, 3)},
-    {32, 128, 256, SAM_AD_NONE, SAM_AD_PART(32, 128, 1, 4, 4)},
-    {16, 128, 128, SAM_AD_NONE, SAM_AD_PART(16, 128, 1, 2, 4)},
+    {256, 256, 512, SAM_AD_FUSED(256, 256, 2, 4, 2), SAM_AD_NONE, SAM_AD_NONE},
+    {192, 256, 512, SAM_AD_FUSED(192, 256, 2, 4, 2), SAM_AD_NONE, SAM_AD_NONE},
+    {128, 128, 512, SAM_AD_FUSED(128, 128, 2, 4, 4), SAM_AD_PART(128, 128, 2, 4, 4), SAM_AD_NONE},
+    {64, 128, 256, SAM_AD_NONE, SAM_AD_NONE, SAM_AD_SHRINK(64, 128, 1, 4, 3)},
+    {32, 128, 256, SAM_AD_NONE, SAM_AD_NONE, SAM_AD_SHRINK(32, 128, 1, 4, 3)},
+    {16, 128, 128, SAM_AD_NONE, SAM_AD_NONE, SAM_AD_SHRINK(16, 128, 1, 2, 4)},
 };
 
 }  // namespace
@@ -296,7 +337,7 @@ const TileKernels kTiles[] = {
 AdapterTile adapter_tile(int tile) { return {kTiles[tile].bm, kTiles[tile].bn}; }
 
 hipError_t launch_adapter_ring(int tile, int dtype, int bt, const GemmArgs& g, int n, const AdapterRing* x,
-                               hipStream_t s)
+                               const ShrinkArgs* shrink, hipStream_t s)
 {
     const TileKernels& k = kTiles[tile];
     const dim3 grid((unsigned)((long long)g.tiles_m * g.tiles_n * g.split));
@@ -304,6 +345,9 @@ hipError_t launch_adapter_ring(int tile, int dtype, int bt, const GemmArgs& g, i
         const AdapterKernelFn fn = k.fused[dtype - 1][bt];
         if (!fn) return hipErrorInvalidDeviceFunction;
         hipLaunchKernelGGL(fn, grid, dim3(k.threads), 0, s, AdapterRingArgs{g, *x});
+    } else if (const AdapterPartShrinkFn beside = k.shrink[dtype - 1][bt]) {
+        const int more = (shrink_wgs(*shrink) + 7) / 8 * 8;
+        hipLaunchKernelGGL(beside, dim3(grid.x + more), dim3(k.threads), 0, s, g, n, *shrink, more);
     } else {
         const AdapterPartFn fn = k.part[dtype - 1][bt];
         if (!fn) return hipErrorInvalidDeviceFunction;
