@@ -287,9 +287,10 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  * rank 1 .. 128 (adapters of lower rank: zero rows); n_adapters 0 is the
  * plain projection; N, K >= 1; M == 0 is a no-op. Sums are FP32; the rank-r
  * intermediate is FP32 too, or kept to 22 bits (SAM_F16; 16 for SAM_BF16 with
- * a SAM_BF16 result) relative to its row's largest value. Other base addresses must be 16-byte aligned; rows
- * that are no whole 16-byte pieces (K or N not a multiple of 8, or such a
- * stride) are copied into the workspace first. Y must not overlap anything
+ * a SAM_BF16 result) relative to its row's largest value. Other base
+ * addresses must be 16-byte aligned; rows that are no whole 16-byte pieces (K
+ * or N not a multiple of 8, or such a stride) are copied into the workspace
+ * first. Y must not overlap anything
  * else. Workspace: sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when
  * short. N, K and strides up to 2.08 M values. Asynchronous on `stream`, no
  * atomics on results, fixed summation order. */
@@ -364,7 +365,7 @@ sam_status sam_adapter_backward_workspace(sam_dtype dtype, sam_op trans_w,
  * weight is 0, whose entries are all empty or -inf, or whose logits are all
  * -inf has loss 0 and gradient 0 (with weight 0 also where its logits are
  * NaN). NaN elsewhere stays in its row. top 1 .. 1024, V up to 2^31 - 65536,
- * T positive and finite; rows == 0 is a no-op. Sums are FP32; no atomics, a
+ * T from 2^-40 to 2^40; rows == 0 is a no-op. Sums are FP32; no atomics, a
  * fixed order. No workspace. Asynchronous on `stream`. */
 sam_status sam_distill_loss(sam_dtype dtype, int64_t rows, int64_t V,
                             int64_t top, const void* logits, int64_t ldz,

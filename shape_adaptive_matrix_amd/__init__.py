@@ -11,6 +11,7 @@ the ``sam_`` prefix.
 from __future__ import annotations
 
 import ctypes
+import functools
 import re
 from pathlib import Path
 
@@ -483,46 +484,102 @@ def gemm_mxfp4_variant(vid: int, A, SA, Bt, SB, C=None, split_k: int = 0, worksp
 
 
 # -- low-rank adapters beside a shared projection --------------------------------
+# A call of few rows takes as long on the host as on the GPU, so these checks
+# read each property of a tensor once.
+def _matrix(t, name):
+    """(rows, columns, row stride) of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    return rows, cols, max(ld, cols, 1)
+
+
+def _one_gpu(names, tensors):
+    """_on_device, for tensors that are in order by comparing device numbers."""
+    d = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (d < 0 or t.get_device() != d):
+            _on_device(tensors, names)
+    return d
+
+
+def _address(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream_address(stream):
+    import torch
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
 def _adapter_operands(X, W, A, B, ids, scale, trans_w):
     """Checks of the tensors that the adapter calls share; (code, M, N, K, n, rank, ldx, ldw)."""
     import torch
-    if X.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"X must be bfloat16 or float16 (got {X.dtype})")
+    dt = X.dtype
+    if dt != torch.bfloat16 and dt != torch.float16:
+        raise TypeError(f"X must be bfloat16 or float16 (got {dt})")
     for t, name in ((W, "W"), (A, "A"), (B, "B")):
-        if t.dtype != X.dtype:
-            raise TypeError(f"{name} is {t.dtype}, X is {X.dtype}")
-    ldx, ldw = _rows(X, "X"), _rows(W, "W")
-    M, K = X.shape
-    Kw, N = (W.shape[1], W.shape[0]) if trans_w else (W.shape[0], W.shape[1])
+        if t.dtype != dt:
+            raise TypeError(f"{name} is {t.dtype}, X is {dt}")
+    M, K, ldx = _matrix(X, "X")
+    Kw, N, ldw = _matrix(W, "W")
+    if trans_w:
+        Kw, N = N, Kw
     if Kw != K:
         raise ValueError(f"X has rows of {K}, W {tuple(W.shape)} (trans_w={bool(trans_w)}) takes {Kw}")
-    if A.dim() != 3 or B.dim() != 3 or A.shape[:2] != B.shape[:2] or A.shape[2] != K or B.shape[2] != N:
-        raise ValueError(f"A must be [n, rank, {K}] and B [n, rank, {N}] (got {tuple(A.shape)}, {tuple(B.shape)})")
+    sa, sb = A.shape, B.shape
+    if len(sa) != 3 or len(sb) != 3 or sa[:2] != sb[:2] or sa[2] != K or sb[2] != N:
+        raise ValueError(f"A must be [n, rank, {K}] and B [n, rank, {N}] (got {tuple(sa)}, {tuple(sb)})")
     if not (A.is_contiguous() and B.is_contiguous()):
         raise ValueError("A and B must be contiguous")
-    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,) or not ids.is_contiguous():
+    if ids.dtype != torch.int32 or ids.dim() != 1 or ids.numel() != M or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous int32 tensor of {M} (got {ids.dtype} {tuple(ids.shape)})")
-    n, rank = int(A.shape[0]), int(A.shape[1])
-    if scale is not None and (scale.dtype != torch.float32 or tuple(scale.shape) != (n,) or not scale.is_contiguous()):
+    n, rank = sa[0], sa[1]
+    if scale is not None and (scale.dtype != torch.float32 or scale.dim() != 1 or scale.numel() != n
+                              or not scale.is_contiguous()):
         raise ValueError(f"scale must be a contiguous float32 tensor of {n}")
-    return _torch_dtype_code(X, None), M, N, K, n, rank, ldx, ldw
+    return BF16 if dt == torch.bfloat16 else F16, M, N, K, n, rank, ldx, ldw
 
 
-def _adapter_result(Y, rows, cols, out_dtype, like, name):
-    """The result tensor (given or new) and its type code."""
+def _adapter_result(Y, rows, cols, out_dtype, like, code, name):
+    """The result tensor (given or new), its type code and row stride."""
     import torch
     if Y is not None:
         if out_dtype is not None and Y.dtype != out_dtype:
             raise TypeError(f"{name} is {Y.dtype}, out_dtype {out_dtype}")
         out_dtype = Y.dtype
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
-    if out_dtype not in (torch.float32, like.dtype):
+    elif out_dtype is None:
+        out_dtype = torch.float32
+    if out_dtype != like.dtype and out_dtype != torch.float32:
         raise TypeError(f"{name} must be float32 or {like.dtype} (got {out_dtype})")
+    out = F32 if out_dtype == torch.float32 else code
     if Y is None:
-        Y = torch.empty((rows, cols), dtype=out_dtype, device=like.device)
-    elif tuple(Y.shape) != (rows, cols):
+        shape = (rows, cols)
+        Y = like.new_empty(shape) if out == code else torch.empty(shape, dtype=torch.float32, device=like.device)
+        return Y, out, max(cols, 1)
+    r, c, ld = _matrix(Y, name)
+    if r != rows or c != cols:
         raise ValueError(f"{name} must have shape ({rows}, {cols}) (got {tuple(Y.shape)})")
-    return Y, _torch_dtype_code(Y, None)
+    return Y, out, ld
+
+
+@functools.lru_cache(maxsize=4096)
+def _adapter_workspace_bytes(name, *args):
+    """Workspace bytes of a call: a function of its sizes and strides alone."""
+    b = ctypes.c_uint64()
+    _check(getattr(lib(), name)(*args, ctypes.byref(b)))
+    return b.value
+
+
+def _adapter_workspace(nbytes, like, stream):
+    """nbytes of `like`'s GPU, allocated on `stream` (see workspace_for)."""
+    if not nbytes:
+        return None
+    if stream is not None:
+        return workspace_for({"workspace_bytes": nbytes}, like.device, stream)
+    return like.new_empty((nbytes + 1) // 2)   # 16-bit values
 
 
 def adapter_gemm(X, W, A, B, ids, scale=None, Y=None, trans_w=False, out_dtype=None, workspace=None, stream=None):
@@ -536,16 +593,17 @@ def adapter_gemm(X, W, A, B, ids, scale=None, Y=None, trans_w=False, out_dtype=N
     code, M, N, K, n, rank, ldx, ldw = _adapter_operands(X, W, A, B, ids, scale, trans_w)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    dev = _on_device((X, W, A, B, ids, scale, Y, workspace), ("X", "W", "A", "B", "ids", "scale", "Y", "workspace"))
-    Y, out = _adapter_result(Y, M, N, out_dtype, X, "Y")
-    ldy = _rows(Y, "Y")
+    _one_gpu(("X", "W", "A", "B", "ids", "scale", "Y", "workspace"), (X, W, A, B, ids, scale, Y, workspace))
+    Y, out, ldy = _adapter_result(Y, M, N, out_dtype, X, code, "Y")
+    t = int(trans_w)
     if workspace is None:
-        b = ctypes.c_uint64()
-        _check(lib().sam_adapter_gemm_workspace(code, int(trans_w), M, N, K, n, rank, ldx, ldw, ctypes.byref(b)))
-        workspace = workspace_for({"workspace_bytes": b.value}, dev, stream)
-    _check(lib().sam_adapter_gemm(code, int(trans_w), M, N, K, n, rank, _ptr(X), ldx, _ptr(W), ldw, _ptr(A), _ptr(B),
-                                  _ptr(ids), _ptr(scale), out, _ptr(Y), ldy, _ptr(workspace),
-                                  _workspace_bytes(workspace), _stream_ptr(stream)))
+        need = _adapter_workspace_bytes("sam_adapter_gemm_workspace", code, t, M, N, K, n, rank, ldx, ldw)
+        workspace = _adapter_workspace(need, X, stream)
+    else:
+        need = _workspace_bytes(workspace)
+    _check(lib().sam_adapter_gemm(code, t, M, N, K, n, rank, _address(X), ldx, _address(W), ldw, _address(A),
+                                  _address(B), _address(ids), _address(scale), out, _address(Y), ldy,
+                                  _address(workspace), need, _stream_address(stream)))
     return Y
 
 
@@ -559,72 +617,76 @@ def adapter_backward(dY, X, W, A, B, ids, scale=None, dX=None, dA=None, dB=None,
     code, M, N, K, n, rank, ldx, ldw = _adapter_operands(X, W, A, B, ids, scale, trans_w)
     if dY.dtype != X.dtype or tuple(dY.shape) != (M, N):
         raise ValueError(f"dY must be {X.dtype} [{M}, {N}] (got {dY.dtype} {tuple(dY.shape)})")
-    lddy = _rows(dY, "dY")
+    lddy = _matrix(dY, "dY")[2]
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    dev = _on_device((dY, X, W, A, B, ids, scale, dX, dA, dB, workspace),
-                     ("dY", "X", "W", "A", "B", "ids", "scale", "dX", "dA", "dB", "workspace"))
+    _one_gpu(("dY", "X", "W", "A", "B", "ids", "scale", "dX", "dA", "dB", "workspace"),
+             (dY, X, W, A, B, ids, scale, dX, dA, dB, workspace))
     out, lddx = F32, max(K, 1)
     if need_dx:
-        dX, out = _adapter_result(dX, M, K, out_dtype, X, "dX")
-        lddx = _rows(dX, "dX")
+        dX, out, lddx = _adapter_result(dX, M, K, out_dtype, X, code, "dX")
     else:
         dX = None
     if need_dab:
-        dA, dB = (torch.empty(s, dtype=torch.float32, device=dev) if t is None else t
+        dA, dB = (torch.empty(s, dtype=torch.float32, device=X.device) if t is None else t
                   for t, s in ((dA, A.shape), (dB, B.shape)))
         for t, like, name in ((dA, A, "dA"), (dB, B, "dB")):
             if t.dtype != torch.float32 or t.shape != like.shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous float32 {tuple(like.shape)}")
     else:
         dA = dB = None
+    t = int(trans_w)
     if workspace is None:
-        b = ctypes.c_uint64()
-        _check(lib().sam_adapter_backward_workspace(code, int(trans_w), M, N, K, n, rank, lddy, ldx, ldw, int(need_dx),
-                                                    int(need_dab), ctypes.byref(b)))
-        workspace = workspace_for({"workspace_bytes": b.value}, dev, stream)
-    _check(lib().sam_adapter_backward(code, int(trans_w), M, N, K, n, rank, _ptr(dY), lddy, _ptr(X), ldx, _ptr(W), ldw,
-                                      _ptr(A), _ptr(B), _ptr(ids), _ptr(scale), out, _ptr(dX), lddx, _ptr(dA),
-                                      _ptr(dB), _ptr(workspace), _workspace_bytes(workspace), _stream_ptr(stream)))
+        need = _adapter_workspace_bytes("sam_adapter_backward_workspace", code, t, M, N, K, n, rank, lddy, ldx, ldw,
+                                        int(need_dx), int(need_dab))
+        workspace = _adapter_workspace(need, X, stream)
+    else:
+        need = _workspace_bytes(workspace)
+    _check(lib().sam_adapter_backward(code, t, M, N, K, n, rank, _address(dY), lddy, _address(X), ldx, _address(W),
+                                      ldw, _address(A), _address(B), _address(ids), _address(scale), out, _address(dX),
+                                      lddx, _address(dA), _address(dB), _address(workspace), need,
+                                      _stream_address(stream)))
     return dX, dA, dB
 
 
 # -- distillation from a teacher's top logits --------------------------------------
 def _distill_operands(logits, teacher, index, weight):
-    """Checks of the tensors that the distillation calls share; (rows, V, top, ldz)."""
+    """Checks of the tensors that the distillation calls share; (code, teacher's code, rows, V, top, ldz)."""
     import torch
-    if logits.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    codes = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    code, t_code = codes.get(logits.dtype), codes.get(teacher.dtype)
+    if code is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16 (got {logits.dtype})")
-    ldz = _rows(logits, "logits")
-    rows, V = logits.shape
-    if teacher.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+    if t_code is None:
         raise TypeError(f"teacher must be float32, bfloat16 or float16 (got {teacher.dtype})")
-    if teacher.dim() != 2 or teacher.shape[0] != rows or not teacher.is_contiguous():
-        raise ValueError(f"teacher must be a contiguous [{rows}, top] tensor (got {tuple(teacher.shape)})")
-    if index.dtype != torch.int32 or index.shape != teacher.shape or not index.is_contiguous():
-        raise ValueError(f"index must be a contiguous int32 {tuple(teacher.shape)} tensor")
-    if weight is not None and (weight.dtype != torch.float32 or tuple(weight.shape) != (rows,)
-                               or not weight.is_contiguous()):
-        raise ValueError(f"weight must be a contiguous float32 tensor of {rows}")
-    return rows, V, int(teacher.shape[1]), ldz
+    rows, V, ldz = _matrix(logits, "logits")
+    shape = teacher.shape
+    if len(shape) != 2 or shape[0] != rows or not teacher.is_contiguous():
+        raise ValueError(f"teacher must be a contiguous [{rows}, top] tensor (got {tuple(shape)})")
+    if index.dtype != torch.int32 or index.shape != shape or not index.is_contiguous():
+        raise ValueError(f"index must be a contiguous int32 {tuple(shape)} tensor")
+    if weight is not None:
+        _per_row(weight, rows, None, "weight")
+    return code, t_code, rows, V, shape[1], ldz
 
 
-def _per_row(t, rows, dev, name):
+def _per_row(t, rows, like, name):
+    """t, checked, or (None) a new float32 tensor of `rows` beside `like`."""
     import torch
     if t is None:
-        return torch.empty(rows, dtype=torch.float32, device=dev)
-    if t.dtype != torch.float32 or tuple(t.shape) != (rows,) or not t.is_contiguous():
+        return torch.empty(rows, dtype=torch.float32, device=like.device)
+    if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != rows or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {rows}")
     return t
 
 
-def _distill_result(grad, logits):
-    import torch
+def _distill_result(grad, logits, V):
+    """The gradient (given or new) and its row stride."""
     if grad is None:
-        grad = torch.empty(tuple(logits.shape), dtype=logits.dtype, device=logits.device)
+        return logits.new_empty(logits.shape), max(V, 1)
     if grad.dtype != logits.dtype or grad.shape != logits.shape:
         raise ValueError(f"grad must be {logits.dtype} {tuple(logits.shape)}")
-    return grad, _rows(grad, "grad")
+    return grad, _matrix(grad, "grad")[2]
 
 
 def distill_loss(logits, teacher, index, weight=None, temperature=1.0, loss=None, lse=None, stream=None):
@@ -635,25 +697,25 @@ def distill_loss(logits, teacher, index, weight=None, temperature=1.0, loss=None
     fine), teacher [rows, top] logits of the same or another of these types
     at the vocabulary entries index (int32; outside 0 .. V-1: empty), weight
     float32 [rows]."""
-    rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
-    dev = _on_device((logits, teacher, index, weight, loss, lse), ("logits", "teacher", "index", "weight", "loss", "lse"))
-    loss, lse = _per_row(loss, rows, dev, "loss"), _per_row(lse, rows, dev, "lse")
-    _check(lib().sam_distill_loss(_torch_dtype_code(logits, None), rows, V, top, _ptr(logits), ldz,
-                                  _torch_dtype_code(teacher, None), _ptr(teacher), _ptr(index), _ptr(weight),
-                                  float(temperature), _ptr(loss), _ptr(lse), _stream_ptr(stream)))
+    code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
+    _one_gpu(("logits", "teacher", "index", "weight", "loss", "lse"), (logits, teacher, index, weight, loss, lse))
+    loss, lse = _per_row(loss, rows, logits, "loss"), _per_row(lse, rows, logits, "lse")
+    _check(lib().sam_distill_loss(code, rows, V, top, _address(logits), ldz, t_code, _address(teacher),
+                                  _address(index), _address(weight), float(temperature), _address(loss),
+                                  _address(lse), _stream_address(stream)))
     return loss, lse
 
 
 def distill_grad(logits, lse, teacher, index, weight=None, temperature=1.0, grad=None, stream=None):
     """Gradient of the distillation loss with respect to the logits, from the
     lse of distill_loss (sam_distill_grad). grad may be logits itself."""
-    rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
-    dev = _on_device((logits, lse, teacher, index, weight, grad), ("logits", "lse", "teacher", "index", "weight", "grad"))
-    lse = _per_row(lse, rows, dev, "lse")
-    grad, ldg = _distill_result(grad, logits)
-    _check(lib().sam_distill_grad(_torch_dtype_code(logits, None), rows, V, top, _ptr(logits), ldz, _ptr(lse),
-                                  _torch_dtype_code(teacher, None), _ptr(teacher), _ptr(index), _ptr(weight),
-                                  float(temperature), _ptr(grad), ldg, _stream_ptr(stream)))
+    code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
+    _one_gpu(("logits", "lse", "teacher", "index", "weight", "grad"), (logits, lse, teacher, index, weight, grad))
+    lse = _per_row(lse, rows, logits, "lse")
+    grad, ldg = _distill_result(grad, logits, V)
+    _check(lib().sam_distill_grad(code, rows, V, top, _address(logits), ldz, _address(lse), t_code, _address(teacher),
+                                  _address(index), _address(weight), float(temperature), _address(grad), ldg,
+                                  _stream_address(stream)))
     return grad
 
 
@@ -661,11 +723,11 @@ def distill(logits, teacher, index, weight=None, temperature=1.0, loss=None, gra
     """Distillation loss of every row and its gradient with respect to the
     logits, which are read once (sam_distill): (loss, grad). grad may be
     logits itself."""
-    rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
-    dev = _on_device((logits, teacher, index, weight, loss, grad), ("logits", "teacher", "index", "weight", "loss", "grad"))
-    loss = _per_row(loss, rows, dev, "loss")
-    grad, ldg = _distill_result(grad, logits)
-    _check(lib().sam_distill(_torch_dtype_code(logits, None), rows, V, top, _ptr(logits), ldz,
-                             _torch_dtype_code(teacher, None), _ptr(teacher), _ptr(index), _ptr(weight),
-                             float(temperature), _ptr(loss), _ptr(grad), ldg, _stream_ptr(stream)))
+    code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
+    _one_gpu(("logits", "teacher", "index", "weight", "loss", "grad"), (logits, teacher, index, weight, loss, grad))
+    loss = _per_row(loss, rows, logits, "loss")
+    grad, ldg = _distill_result(grad, logits, V)
+    _check(lib().sam_distill(code, rows, V, top, _address(logits), ldz, t_code, _address(teacher), _address(index),
+                             _address(weight), float(temperature), _address(loss), _address(grad), ldg,
+                             _stream_address(stream)))
     return loss, grad

@@ -30,7 +30,9 @@ sam_status check(int dtype, int64_t rows, int64_t V, int64_t top, int64_t ldz, i
                         (long long)V, (long long)top, kMaxTop, (long long)ldz);
     const long long strips = (V + 16383) / 16384;
     if (rows > ((1ll << 31) - 1) / strips) return api_fail(SAM_ERR_INVALID_ARG, "rows=%lld too many", (long long)rows);
-    if (!(T > 0.0f) || !(T < INFINITY)) return api_fail(SAM_ERR_INVALID_ARG, "temperature must be positive and finite");
+    // Within these 1 / T, T^2 and their products with the other factors are ordinary numbers.
+    if (!(T >= 0x1p-40f) || !(T <= 0x1p40f))
+        return api_fail(SAM_ERR_INVALID_ARG, "temperature must be positive, between 2^-40 and 2^40");
     for (int i = 0; i < n; ++i) {
         if (b[i].bytes && !b[i].p) return api_fail(SAM_ERR_INVALID_ARG, "%s is null", b[i].name);
         if (b[i].bytes && !aligned_to(b[i].p, b[i].align))

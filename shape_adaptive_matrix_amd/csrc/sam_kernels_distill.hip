@@ -5,6 +5,7 @@
 // registers between the softmax's sum and the gradient; of a row too long for
 // registers and LDS the rest is read again.
 #include "sam_distill.h"
+#include "sam_dma.h"
 
 namespace sam {
 
@@ -62,11 +63,22 @@ struct Piece {
 // The registers as they are, not what an earlier use made of them: without it
 // the compiler keeps 16-bit rows as floats from one use to the next, twice
 // the registers.
-template <int P>
-__device__ __forceinline__ void as_read(u4 (&r)[P])
+__device__ __forceinline__ void as_read(u4& a, u4& b, u4& c, u4& d)
 {
-#pragma unroll
-    for (int q = 0; q < P; ++q) asm volatile("" : "+v"(r[q]));
+    asm volatile("" : "+v"(a), "+v"(b), "+v"(c), "+v"(d));
+}
+
+// Rows are read once and written once: past the caches (a buffer access's
+// non-temporal bit). Measured without it, loss and gradient: 4096 x 32768
+// bf16 124 us, not 110; 1024 x 131072 FP32 234, not 219.
+constexpr int kOnce = 2;
+
+// Stores take their whole offset in the vector register. With part of it in
+// the scalar one the compiler lets the next instruction overwrite the data's
+// registers, and some of the 16 bytes came out as what was written there.
+__device__ __forceinline__ void store_once(const u4& v, __amdgpu_buffer_rsrc_t r, int off)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, kOnce);
 }
 
 // 2^x with the hardware's instruction (x <= 0 here but for a pivot that is
@@ -74,11 +86,19 @@ __device__ __forceinline__ void as_read(u4 (&r)[P])
 // under 2^-126 become zero.
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-__device__ __forceinline__ float teacher_at(const DistillArgs& a, long long i)
+// A teacher's or a student's value as it is stored, and as a float: loads
+// that are not waited for where they are issued.
+__device__ __forceinline__ unsigned raw_at(const void* p, int dtype, long long i)
 {
-    if (a.t_dtype == DT_F32) return static_cast<const float*>(a.t)[i];
-    if (a.t_dtype == DT_BF16) return (float)static_cast<const __bf16*>(a.t)[i];
-    return (float)static_cast<const _Float16*>(a.t)[i];
+    if (dtype == DT_F32) return static_cast<const unsigned*>(p)[i];
+    return static_cast<const unsigned short*>(p)[i];
+}
+
+__device__ __forceinline__ float value_of(unsigned raw, int dtype)
+{
+    if (dtype == DT_F32) return __uint_as_float(raw);
+    if (dtype == DT_BF16) return __uint_as_float(raw << 16);
+    return (float)__builtin_bit_cast(_Float16, (unsigned short)raw);
 }
 
 template <int NT, class F>
@@ -107,7 +127,7 @@ __device__ __forceinline__ float teacher_row(const DistillArgs& a, long long row
     for (int j = threadIdx.x; j < a.top; j += NT) {
         const int i = a.index[row * a.top + j];
         const bool ok = (unsigned)i < (unsigned)a.V;
-        const float t = ok ? teacher_at(a, row * a.top + j) : -INFINITY;
+        const float t = ok ? value_of(raw_at(a.t, a.t_dtype, row * a.top + j), a.t_dtype) : -INFINITY;
         idx[j] = ok ? i : -1;
         p[j] = t;
         m = fmaxf(m, t);
@@ -155,200 +175,350 @@ __device__ __forceinline__ Span span_of(const void* p, int V)
     return {head, pieces, head + pieces * E};
 }
 
+// A reduction over the wave: rows of 16 lanes by shifts, then across them;
+// lane 63's result, held by the wave. id: the operation's neutral value.
+template <int CTRL, int ROWS, class F>
+__device__ __forceinline__ float dpp_step(float v, float id, F op)
+{
+    return op(v, __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(id), __float_as_uint(v), CTRL, ROWS, 0xF, false)));
+}
+
+template <class F>
+__device__ __forceinline__ float wave_reduce(float v, float id, F op)
+{
+    v = dpp_step<0x111, 0xF>(v, id, op);   // from 1, 2, 4, 8 lanes below
+    v = dpp_step<0x112, 0xF>(v, id, op);
+    v = dpp_step<0x114, 0xF>(v, id, op);
+    v = dpp_step<0x118, 0xF>(v, id, op);
+    v = dpp_step<0x142, 0xA>(v, id, op);   // lane 15 of the row below
+    v = dpp_step<0x143, 0xC>(v, id, op);   // lane 31
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+}
+
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, -INFINITY, [](float x, float y) { return fmaxf(x, y); }); }
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, 0.0f, [](float x, float y) { return x + y; }); }
+
+// A value that no kernel call in flight writes, by a scalar load (a vector
+// load would queue behind the row's).
+__device__ __forceinline__ float constant(const float* p, long long i)
+{
+    return reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<unsigned long long>(p))[i];
+}
+
+// A row's part of the arguments. `read`: its logits are wanted; otherwise its
+// pieces read zeros, which costs nothing.
+template <int DT>
+struct Row {
+    typedef typename Ty<DT>::T T;
+    long long at;
+    const T* z;
+    float w;
+    Span sp;
+    const u4* zb;
+    long long bytes;
+    __device__ __forceinline__ Row(const DistillArgs& a, long long row, bool grad, bool read)
+        : at(row), z(static_cast<const T*>(a.z) + row * a.ldz), w(a.weight ? constant(a.weight, row) : 1.0f), sp(span_of<DT>(z, a.V)),
+          zb(reinterpret_cast<const u4*>(z + sp.head)), bytes(read && !(grad && w == 0.0f) ? 16ll * sp.pieces : 0) {}
+    // Values outside the pieces: at most E - 1 at either end, a thread each.
+    __device__ __forceinline__ int edge_at(int V) const
+    {
+        const int tid = threadIdx.x;
+        if (tid < sp.head) return tid;
+        return tid >= 32 && tid - 32 < V - sp.tail0 ? sp.tail0 + tid - 32 : -1;
+    }
+};
+
 // P pieces of a row stay in each thread's registers and L more in its own
-// place in LDS; what is left of a longer row is read again for the gradient.
-template <int DT, int NT, int P, int L, bool GRAD>
-__global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a)
+// place in LDS; what is left of a longer row (REST) is read again for the
+// gradient. With the gradient a workgroup takes row after row: as soon as a
+// piece of one row's gradient is stored its registers take the next row's
+// logits, so that loads and stores are under way together all the time, and
+// the sums run on pieces as they arrive. For that no load may sit behind a
+// condition (the compiler could not count how many follow it, and would wait
+// for all): pieces past a row's end read zeros, entries past the last read
+// the last, and what they hold is dropped when it is used.
+// A row has one barrier, between its sums and what follows from them: the
+// teacher's entries go 64 to a wave, and what is to be written behind the
+// whole row (the loss, the entries' own gradients) goes out behind the next
+// row's barrier.
+// Measured, loss and gradient: 4096 x 32768 bf16 110 us (rows on
+// workgroups of their own, everything between barriers: 123), 1024 x 131072
+// FP32 219 us (274).
+// Waves a SIMD that the registers have to leave room for: with the gradient
+// as many as `run` puts on a CU.
+constexpr int distill_waves(int nt, int p, bool grad) { return !grad ? 1 : (nt == 512 && p == 8 ? 6 : 4); }
+
+template <int DT, int NT, int P, int L, bool REST, bool GRAD>
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(distill_waves(NT, P, GRAD))))
+distill_kernel(DistillArgs a)
 {
     typedef Piece<DT> Pc;
     typedef typename Pc::T T;
-    constexpr int E = Pc::E;
-    __shared__ u4 hold[L > 0 ? L * NT : 1];
-    __shared__ float p[kMaxTop];
-    __shared__ int idx[kMaxTop];
-    __shared__ float red[2][NT / 64];
-    const int tid = threadIdx.x;
-    const long long row = blockIdx.x;
-    const T* z = static_cast<const T*>(a.z) + row * a.ldz;
-    T* g = static_cast<T*>(a.grad) + row * a.ldg;
-    const float w = a.weight ? a.weight[row] : 1.0f;
-    const Span sp = span_of<DT>(z, a.V);
-    const u4* zb = reinterpret_cast<const u4*>(z + sp.head);
-    u4* gb = reinterpret_cast<u4*>(g + sp.head);
-    const bool whole = (((unsigned long long)gb) & 15) == 0;
-    auto write = [&](int i, const u4& x) {
-        if (whole) {
-            gb[i] = x;
-        } else {
-            const T* h = reinterpret_cast<const T*>(&x);
-#pragma unroll
-            for (int k = 0; k < E; ++k) g[sp.head + (long long)i * E + k] = h[k];
-        }
-    };
-    // Values outside the pieces: at most E - 1 at either end, a thread each.
-    int edge_at = -1;
-    if (tid < sp.head) edge_at = tid;
-    if (tid >= 32 && tid - 32 < a.V - sp.tail0) edge_at = sp.tail0 + tid - 32;
-    if (GRAD && w == 0.0f) {
-        // A row that is not trained on: its logits are not read.
-        for (int i = tid; i < sp.pieces; i += NT) write(i, u4{0u, 0u, 0u, 0u});
-        if (edge_at >= 0) g[edge_at] = (T)0.0f;
-        if (a.loss && tid == 0) a.loss[row] = 0.0f;
-        return;
-    }
+    constexpr int E = Pc::E, NW = NT / 64;
+    static_assert(P % 4 == 0 && L % 4 == 0, "pieces are summed four at a time");
+    __shared__ __attribute__((aligned(16))) u4 hold[L > 0 ? L * NT : 1];
+    __shared__ float val[2][kMaxTop];    // by row parity: the teacher's value
+    __shared__ int idx[2][kMaxTop];      // its index, -1: empty
+    __shared__ float gval[2][kMaxTop];      // an entry's own gradient
+    __shared__ unsigned long long gset[2][kMaxTop / 64];   // and whether it is written, a bit each
+    __shared__ float4 part[2][NW];       // a wave's largest logit and sum, its entries' largest and sum
+    __shared__ float lsum[2][NW];        // its part of the loss
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int chunks = (a.top + 63) / 64;
 
-    // The row's loads first; the teacher's part runs while they are under way.
+    // What is loaded ahead of a row's turn: the wave's first entries, its edge value, its pieces.
     u4 r[P];
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        const int i = tid + q * NT;
-        r[q] = Pc::masked();
-        if (i < sp.pieces) r[q] = zb[i];
-    }
-    float edge = -INFINITY;
-    if (edge_at >= 0) edge = (float)z[edge_at];
-
-    float best;
-    const float psum = teacher_row<NT>(a, row, p, idx, red[0], best);
-
-    // This thread's largest value, then the row's, and the row's sum of
-    // 2^((z - m) scale). Values not in registers: a running maximum and sum,
-    // four pieces at a time.
-    float m = edge;
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        float v[E];
-        Pc::get(r[q], v);
-#pragma unroll
-        for (int i = 0; i < E; ++i) m = fmaxf(m, v[i]);
-    }
-    float mx = -INFINITY, sx = 0.0f;
-    auto running = [&](const u4 (&x)[4]) {
-        float n = mx;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            float v[E];
-            Pc::get(x[b], v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) n = fmaxf(n, v[i]);
-        }
-        const float pv = n > -INFINITY ? n : 0.0f;
-        if (mx > -INFINITY) sx *= pow2((mx - pv) * a.scale);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            float v[E];
-            Pc::get(x[b], v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) sx += pow2((v[i] - pv) * a.scale);
-        }
-        mx = n;
+    unsigned t, edge;
+    int ix;
+    auto entry_at = [&](const Row<DT>& c, int o) { return c.at * a.top + min(lane + 64 * o, a.top - 1); };
+    auto fetch_entries = [&](const Row<DT>& c) {
+        ix = a.index[entry_at(c, wave)];
+        t = raw_at(a.t, a.t_dtype, entry_at(c, wave));
+        edge = raw_at(c.z, DT, max(c.edge_at(a.V), 0));
     };
+    auto fetch = [&](const Row<DT>& c, int q) {
+        r[q] = __builtin_amdgcn_raw_buffer_load_b128(dma::make_rsrc(c.zb, c.bytes), tid * 16, q * NT * 16, kOnce);
+    };
+    auto fetch_hold = [&](const Row<DT>& c, int o) {   // straight into LDS; no registers for it
+        dma::lds_load16(dma::rsrc_words(c.zb, c.bytes), dma::lds_addr(hold + o * NT + wave * 64), (tid + (P + o) * NT) * 16);
+    };
+    auto fetch_rest = [&](const Row<DT>& c, u4 (&x)[4], int at) {
+        const __amdgpu_buffer_rsrc_t rs = dma::make_rsrc(c.zb + at, c.bytes - 16ll * at);
 #pragma unroll
-    for (int o = 0; o < L; o += 4) {
-        u4 x[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int i = tid + (P + o + b) * NT;
-            x[b] = Pc::masked();
-            if (i < sp.pieces) x[b] = zb[i];
+        for (int b = 0; b < 4; ++b) x[b] = __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, b * NT * 16, 0);
+    };
+    // -inf in pieces past the row's end, of four that start at piece `at`, NT
+    // apart. A branch, not selects, for whole groups pass it by.
+    auto trim = [&](const Row<DT>& c, u4& x0, u4& x1, u4& x2, u4& x3, int at) {
+        if (at + 4 * NT > c.sp.pieces) {
+            as_read(x0, x1, x2, x3);
+            const int left = c.sp.pieces - at - tid;
+            if (left <= 0) x0 = Pc::masked();
+            if (left <= NT) x1 = Pc::masked();
+            if (left <= 2 * NT) x2 = Pc::masked();
+            if (left <= 3 * NT) x3 = Pc::masked();
         }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) hold[(o + b) * NT + tid] = x[b];
-        running(x);
-    }
-    for (int i0 = tid + (P + L) * NT; i0 < sp.pieces; i0 += 4 * NT) {
-        u4 x[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            x[b] = Pc::masked();
-            if (i0 + b * NT < sp.pieces) x[b] = zb[i0 + b * NT];
+    };
+    // What follows a row that all waves have stored: each wave's entries, the loss.
+    auto finish_row = [&](long long row, int par) {
+        if (GRAD)
+            for (int j = lane + 64 * wave; j < a.top; j += NT)
+                if (gset[par][j / 64] >> lane & 1) static_cast<T*>(a.grad)[row * a.ldg + idx[par][j]] = (T)gval[par][j];
+        if (tid == 0) {
+            float sum = 0.0f;
+            for (int w = 0; w < min(chunks, NW); ++w) sum += lsum[par][w];
+            if (a.loss) a.loss[row] = sum;
         }
-        running(x);
-    }
-    as_read(r);
-    m = block_reduce<NT>(fmaxf(m, mx), red[1], [](float x, float y) { return fmaxf(x, y); });
-    const float pivot = m > -INFINITY ? m : 0.0f;
-    // mx = -inf with a sum: NaN values, which stay.
-    float s = pow2((edge - pivot) * a.scale) + (mx > -INFINITY ? sx * pow2((mx - pivot) * a.scale) : sx);
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-        float v[E];
-        Pc::get(r[q], v);
-#pragma unroll
-        for (int i = 0; i < E; ++i) s += pow2((v[i] - pivot) * a.scale);
-    }
-    as_read(r);
-    s = block_reduce<NT>(s, red[0], [](float x, float y) { return x + y; });
+    };
 
-    // The loss, entry by entry; p[j] becomes the probability. A row takes
-    // part if the teacher has an entry and the student a logit above -inf.
-    const bool on = w != 0.0f && !(psum == 0.0f) && !(s == 0.0f);
-    const float ls = logf(s), lp = logf(psum);
-    const float tp = best > -INFINITY ? best : 0.0f;
-    float sum = 0.0f;
-    for (int j = tid; j < a.top; j += NT) {
-        const float lt = (p[j] - tp) / a.T;
-        const float pj = idx[j] >= 0 ? expf(lt) / psum : 0.0f;
-        if (on && !(pj == 0.0f)) sum += pj * (lt - lp - (((float)z[idx[j]] - pivot) / a.T - ls));
-        p[j] = pj;
-    }
-    sum = block_reduce<NT>(sum, red[1], [](float x, float y) { return x + y; });
-    if (tid == 0) {
-        if (a.loss) a.loss[row] = on ? w * a.T * a.T * sum : 0.0f;
-        if (a.lse) a.lse[row] = s == 0.0f ? -INFINITY : (float)((double)pivot / a.T + (double)ls);
-    }
-    if constexpr (GRAD) {
-        const float wt = w * a.T, f = on ? wt / s : 0.0f;
-        // The entries' own logits are read before any of the row is written
-        // (the gradient may take the logits' place). Every index is written
-        // once more after the row, by its first entry.
-        constexpr int MORE = (kMaxTop + NT - 1) / NT;
-        float gv[MORE];
-        int gat[MORE];
+    long long row = blockIdx.x, before = -1;
+    Row<DT> c(a, row, GRAD, true);
+    fetch_entries(c);
 #pragma unroll
-        for (int o = 0; o < MORE; ++o) {
-            const int j = tid + o * NT;
-            gat[o] = -1;
-            if (on && j < a.top) {
-                const float pt = total_p(a, p, idx, j);
-                if (!(pt < 0.0f)) {
-                    gat[o] = idx[j];
-                    gv[o] = wt * (pow2(((float)z[idx[j]] - pivot) * a.scale) / s - pt);
+    for (int o = 0; o < L; ++o) fetch_hold(c, o);
+#pragma unroll
+    for (int q = 0; q < P; ++q) fetch(c, q);
+    for (int par = 0;; par ^= 1) {
+        const bool last = !GRAD || row + gridDim.x >= a.rows;
+        const Row<DT> n(a, last ? row : row + gridDim.x, GRAD, !last);
+        const int edge_at = c.edge_at(a.V);
+        const float edge_v = edge_at >= 0 ? value_of(edge, DT) : -INFINITY;
+
+        const bool look = !GRAD || c.w != 0.0f;   // a row that is not trained on: its logits are not looked at
+        float z_own = 0.0f;                       // of the wave's first entries
+        bool twice = chunks > 1;                  // an index may come more than once
+        if (look) {
+            // The entries' own logits arrive behind the row's.
+            if (lane + 64 * wave >= a.top || (unsigned)ix >= (unsigned)a.V) ix = -1;
+            const unsigned zr = raw_at(c.z, DT, max(ix, 0));
+            float best = -INFINITY, psum = 0.0f;
+            if (wave < chunks) {
+                auto take = [&](int o, int i, unsigned raw) {
+                    const int j = lane + 64 * o;
+                    const float v = i >= 0 ? value_of(raw, a.t_dtype) : -INFINITY;
+                    best = fmaxf(best, v);
+                    if (j < a.top) {
+                        idx[par][j] = i;
+                        val[par][j] = v;
+                    }
+                };
+                take(wave, ix, t);
+                for (int o = wave + NW; o < chunks; o += NW) {
+                    const int i = a.index[entry_at(c, o)];
+                    take(o, lane + 64 * o >= a.top || (unsigned)i >= (unsigned)a.V ? -1 : i, raw_at(a.t, a.t_dtype, entry_at(c, o)));
+                }
+                best = wave_max(best);
+                for (int j = lane + 64 * wave; j < a.top; j += NT)
+                    if (idx[par][j] >= 0) psum += expf((val[par][j] - (best > -INFINITY ? best : 0.0f)) / a.T);
+                psum = wave_sum(psum);
+                if (GRAD && chunks == 1) {   // the wave's own entries are all there are
+                    for (int k = 0; k < a.top; ++k) twice |= ix >= 0 && idx[par][k] == ix && k != lane;
+                    twice = __ballot(twice) != 0;
                 }
             }
+
+            // A running maximum and sum of 2^((z - mx) scale), 16 values at a time.
+            constexpr int GR = 16 / E;
+            float mx = -INFINITY, sx = 0.0f;
+            auto running = [&](const u4 (&x)[GR]) {
+                float m = mx;
+#pragma unroll
+                for (int b = 0; b < GR; ++b) {
+                    float v[E];
+                    Pc::get(x[b], v);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) m = fmaxf(m, v[i]);
+                }
+                const float pv = m > -INFINITY ? m : 0.0f;
+                sx *= mx > -INFINITY ? pow2((mx - pv) * a.scale) : 1.0f;
+#pragma unroll
+                for (int b = 0; b < GR; ++b) {
+                    float v[E];
+                    Pc::get(x[b], v);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) sx += pow2((v[i] - pv) * a.scale);
+                }
+                mx = m;
+                asm volatile("" : "+v"(sx), "+v"(mx));   // here, not where the sum is used: registers
+            };
+            auto running4 = [&](const u4& x0, const u4& x1, const u4& x2, const u4& x3) {
+                if constexpr (GR == 4) {
+                    running({x0, x1, x2, x3});
+                } else {
+                    running({x0, x1});
+                    running({x2, x3});
+                }
+            };
+#pragma unroll
+            for (int q = 0; q < P; q += 4) {
+                trim(c, r[q], r[q + 1], r[q + 2], r[q + 3], q * NT);
+                running4(r[q], r[q + 1], r[q + 2], r[q + 3]);
+                as_read(r[q], r[q + 1], r[q + 2], r[q + 3]);
+            }
+            if constexpr (L > 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int o = 0; o < L; o += 4) {
+                u4 x[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) x[b] = hold[(o + b) * NT + tid];
+                trim(c, x[0], x[1], x[2], x[3], (P + o) * NT);
+                running4(x[0], x[1], x[2], x[3]);
+            }
+            if constexpr (REST)
+                for (int at = (P + L) * NT; at < c.sp.pieces; at += 4 * NT) {
+                    u4 x[4];
+                    fetch_rest(c, x, at);
+                    trim(c, x[0], x[1], x[2], x[3], at);
+                    running4(x[0], x[1], x[2], x[3]);
+                }
+            // The wave's. mx = -inf with a sum: NaN values, which stay.
+            const float m = wave_max(fmaxf(mx, edge_v)), pv = m > -INFINITY ? m : 0.0f;
+            const float s = wave_sum(pow2((edge_v - pv) * a.scale) + (mx > -INFINITY ? sx * pow2((mx - pv) * a.scale) : sx));
+            if (lane == 0) part[par][wave] = make_float4(m, s, best, psum);
+            z_own = value_of(zr, DT);
+            asm volatile("" : "+v"(z_own));   // it is there; later it would be waited for behind stores
         }
         __syncthreads();
-        auto grad_of = [&](const u4& x) {
-            float v[E];
-            Pc::get(x, v);
-#pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = on ? f * pow2((v[i] - pivot) * a.scale) : 0.0f;
-            return Pc::put(v);
-        };
-#pragma unroll
-        for (int q = 0; q < P; ++q) {
-            const int i = tid + q * NT;
-            if (i < sp.pieces) write(i, grad_of(r[q]));
+
+        float pivot = 0.0f, s = 1.0f;
+        bool on = look;   // a row takes part if the teacher has an entry and the student a logit above -inf
+        if (look) {
+            const float4 w = part[par][lane & (NW - 1)];
+            const bool mine = lane < NW;
+            const float m = wave_max(w.x), best = wave_max(w.z), tp = best > -INFINITY ? best : 0.0f;
+            pivot = m > -INFINITY ? m : 0.0f;
+            s = wave_sum(!mine ? 0.0f : w.x > -INFINITY ? w.y * pow2((w.x - pivot) * a.scale) : w.y);
+            const float psum = wave_sum(!mine ? 0.0f : w.z > -INFINITY ? w.w * expf((w.z - tp) / a.T) : w.w);
+            on = __builtin_amdgcn_readfirstlane(c.w != 0.0f && !(psum == 0.0f) && !(s == 0.0f));
+            const float ls = logf(s);
+            if (tid == 0 && a.lse) a.lse[row] = s == 0.0f ? -INFINITY : (float)((double)pivot / a.T + (double)ls);
+            if (on && wave < chunks) {
+                // The loss, entry by entry, and the entries' gradients: an
+                // index is written by its first entry, for all of them.
+                const float lp = logf(psum);
+                float sum = 0.0f;
+                auto entry = [&](int o, float zj) {
+                    const int j = lane + 64 * o;
+                    const int i = j < a.top ? idx[par][j] : -1;
+                    const float lt = i >= 0 ? (val[par][j] - tp) / a.T : -INFINITY;
+                    const float pj = i >= 0 ? expf(lt) / psum : 0.0f;
+                    if (!(pj == 0.0f)) sum += pj * (lt - lp - ((zj - pivot) / a.T - ls));
+                    if constexpr (GRAD) {
+                        float pt = pj;
+                        bool first = i >= 0;
+                        if (twice && first)
+                            for (int k = 0; k < a.top; ++k)
+                                if (idx[par][k] == i && k != j) {
+                                    first &= k > j;
+                                    pt += expf((val[par][k] - tp) / a.T) / psum;
+                                }
+                        const unsigned long long set = __ballot(first);
+                        if (lane == 0) gset[par][o] = set;
+                        if (first) gval[par][j] = c.w * a.T * (pow2((zj - pivot) * a.scale) / s - pt);
+                    }
+                };
+                entry(wave, z_own);
+                for (int o = wave + NW; o < chunks; o += NW)
+                    entry(o, value_of(raw_at(c.z, DT, max(idx[par][min(lane + 64 * o, a.top - 1)], 0)), DT));
+                sum = wave_sum(sum);
+                if (lane == 0) lsum[par][wave] = c.w * a.T * a.T * sum;
+            }
         }
+        if (!on && tid == 0 && a.loss) a.loss[row] = 0.0f;
+        if constexpr (!GRAD) {
+            __syncthreads();
+            if (on) finish_row(row, par);
+            return;
+        }
+
+        T* g = static_cast<T*>(a.grad) + row * a.ldg;
+        const T* gb = g + c.sp.head;   // aligned to a value: the hardware's unaligned stores
+        const __amdgpu_buffer_rsrc_t rg = dma::make_rsrc(gb, 16ll * c.sp.pieces);
+        const float f = c.w * a.T / s;
+        auto grad_of = [&](const u4& x) {
+            u4 o = {0u, 0u, 0u, 0u};
+            if (on) {
+                float v[E];
+                Pc::get(x, v);
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[i] = f * pow2((v[i] - pivot) * a.scale);
+                o = Pc::put(v);
+                asm volatile("" : "+v"(o));
+            }
+            return o;
+        };
+        if constexpr (REST)
+            for (int at = (P + L) * NT; at < c.sp.pieces; at += 4 * NT) {
+                u4 x[4];
+                fetch_rest(c, x, at);
+                const __amdgpu_buffer_rsrc_t rs = dma::make_rsrc(gb + (long long)at * E, 16ll * (c.sp.pieces - at));
+#pragma unroll
+                for (int b = 0; b < 4; ++b) store_once(grad_of(x[b]), rs, (tid + b * NT) * 16);
+            }
+        fetch_entries(n);
+        if (before >= 0) finish_row(before, par ^ 1);   // behind the loads: its stores need not be waited for
+        before = on ? row : -1;
 #pragma unroll
         for (int o = 0; o < L; ++o) {
-            const int i = tid + (P + o) * NT;
-            if (i < sp.pieces) write(i, grad_of(hold[o * NT + tid]));
+            store_once(grad_of(hold[o * NT + tid]), rg, (tid + (P + o) * NT) * 16);
+            fetch_hold(n, o);
         }
-        for (int i0 = tid + (P + L) * NT; i0 < sp.pieces; i0 += 4 * NT) {
-            u4 x[4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (i0 + b * NT < sp.pieces) x[b] = zb[i0 + b * NT];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (i0 + b * NT < sp.pieces) write(i0 + b * NT, grad_of(x[b]));
+        for (int q = 0; q < P; ++q) {
+            store_once(grad_of(r[q]), rg, (tid + q * NT) * 16);
+            fetch(n, q);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (edge_at >= 0) g[edge_at] = (T)(on ? f * pow2((edge - pivot) * a.scale) : 0.0f);
-        __syncthreads();
-#pragma unroll
-        for (int o = 0; o < MORE; ++o)
-            if (gat[o] >= 0) g[gat[o]] = (T)gv[o];
+        if (edge_at >= 0) g[edge_at] = (T)(on ? f * pow2((edge_v - pivot) * a.scale) : 0.0f);
+        if (last) {
+            __syncthreads();
+            if (on) finish_row(row, par);
+            if constexpr (L > 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load into LDS outlives the workgroup
+            return;
+        }
+        row += gridDim.x;
+        c = n;
     }
 }
 
@@ -374,16 +544,13 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillArgs 
     const float lse = a.lse[row];
     const Span sp = span_of<DT>(z, a.V);
     const u4* zb = reinterpret_cast<const u4*>(z + sp.head);
-    u4* gb = reinterpret_cast<u4*>(g + sp.head);
-    const bool whole = (((unsigned long long)gb) & 15) == 0;
-    const int first = strip * NT * P;
+    const int first = strip * NT * P, here = sp.pieces - first;
+    const __amdgpu_buffer_rsrc_t rz = dma::make_rsrc(zb + first, 16ll * here);
+    // Aligned to a value: the hardware's unaligned stores.
+    const __amdgpu_buffer_rsrc_t rg = dma::make_rsrc(g + sp.head + (long long)first * E, 16ll * here);
     u4 r[P];
 #pragma unroll
-    for (int q = 0; q < P; ++q) {
-        const int i = first + tid + q * NT;
-        r[q] = Pc::masked();
-        if (i < sp.pieces) r[q] = zb[i];
-    }
+    for (int q = 0; q < P; ++q) r[q] = __builtin_amdgcn_raw_buffer_load_b128(rz, tid * 16, q * NT * 16, 0);
     // The first strip takes the values before the pieces, the last those behind.
     float edge = 0.0f;
     int edge_at = -1;
@@ -426,21 +593,11 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillArgs 
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < P; ++q) {
-        const int i = first + tid + q * NT;
-        if (i < sp.pieces) {
-            float v[E];
-            Pc::get(r[q], v);
+        float v[E];
+        Pc::get(r[q], v);
 #pragma unroll
-            for (int k = 0; k < E; ++k) v[k] = !on || v[k] == -INFINITY ? 0.0f : wt * q_of(v[k]);
-            const u4 x = Pc::put(v);
-            if (whole) {
-                gb[i] = x;
-            } else {
-                const T* h = reinterpret_cast<const T*>(&x);
-#pragma unroll
-                for (int k = 0; k < E; ++k) g[sp.head + (long long)i * E + k] = h[k];
-            }
-        }
+        for (int k = 0; k < E; ++k) v[k] = !on || v[k] == -INFINITY ? 0.0f : wt * q_of(v[k]);
+        store_once(Pc::put(v), rg, (tid + q * NT) * 16);
     }
     if (edge_at >= 0) g[edge_at] = (T)(!on || edge == -INFINITY ? 0.0f : wt * q_of(edge));
     __syncthreads();
@@ -449,32 +606,36 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillArgs 
         if (gat[o] >= 0) g[gat[o]] = (T)gv[o];
 }
 
-template <int DT, int NT, int P, int L>
-hipError_t run(const DistillArgs& a, hipStream_t s)
+// per: workgroups of a CU that take rows in turn.
+template <int DT, int NT, int P, int L, bool REST = false>
+hipError_t run(const DistillArgs& a, int per, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.rows), block(NT);
+    const dim3 block(NT);
     if (a.grad)
-        hipLaunchKernelGGL((distill_kernel<DT, NT, P, L, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((distill_kernel<DT, NT, P, L, REST, true>), dim3((unsigned)(a.rows < 256 * per ? a.rows : 256 * per)),
+                           block, 0, s, a);
     else   // the loss alone has no use for what it has read
-        hipLaunchKernelGGL((distill_kernel<DT, NT, P, 0, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((distill_kernel<DT, NT, P, 0, REST, false>), dim3((unsigned)a.rows), block, 0, s, a);
     return hipGetLastError();
 }
 
-// Threads and registers by the row's length; few rows: as many threads as
-// fit, for latency.
+// Threads and registers by the row's length, so that each holds a row and two
+// to four workgroups share a CU (4096 x 32768 bf16: three of 512 threads 110
+// us, two 114, three of 256 with twice the registers 122, one of 1024 138);
+// few rows: as many threads as fit, for latency.
 template <int DT>
 hipError_t pick(const DistillArgs& a, hipStream_t s)
 {
     const long long pieces = ((long long)a.V + Piece<DT>::E - 1) / Piece<DT>::E;
     const bool few = a.rows <= 256;
-    if (pieces <= 256 * 4) return run<DT, 256, 4, 0>(a, s);
-    if (few && pieces <= 1024 * 4) return run<DT, 1024, 4, 0>(a, s);
-    if (few && pieces <= 1024 * 8) return run<DT, 1024, 8, 0>(a, s);
-    if (pieces <= 256 * 8) return run<DT, 256, 8, 0>(a, s);
-    if (pieces <= 256 * 16) return run<DT, 256, 16, 0>(a, s);
-    if (pieces <= 512 * 16) return run<DT, 512, 16, 0>(a, s);
-    if (pieces <= 1024 * 16) return run<DT, 1024, 16, 0>(a, s);
-    return run<DT, 1024, 20, 8>(a, s);
+    if (pieces <= 256 * 4) return run<DT, 256, 4, 0>(a, 4, s);
+    if (few && pieces <= 1024 * 4) return run<DT, 1024, 4, 0>(a, 1, s);
+    if (few && pieces <= 1024 * 8) return run<DT, 1024, 8, 0>(a, 1, s);
+    if (pieces <= 256 * 8) return run<DT, 256, 8, 0>(a, 4, s);
+    if (pieces <= 512 * 8) return run<DT, 512, 8, 0>(a, 3, s);
+    if (pieces <= 512 * 16) return run<DT, 512, 16, 0>(a, 2, s);
+    if (pieces <= 1024 * 16) return run<DT, 1024, 16, 0>(a, 1, s);
+    return run<DT, 1024, 20, 8, true>(a, 1, s);
 }
 
 }  // namespace

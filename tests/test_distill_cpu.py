@@ -30,7 +30,7 @@ REFUSED = [
     (dict(dtype=sam.MXFP8), INVALID), (dict(dtype=-1), INVALID), (dict(td=7), INVALID), (dict(rows=-1), INVALID),
     (dict(V=0), INVALID), (dict(V=1 << 31), INVALID), (dict(top=0), INVALID), (dict(top=1025), INVALID),
     (dict(ldz=99), INVALID), (dict(rows=1 << 31), INVALID), (dict(T=0.0), INVALID), (dict(T=-1.0), INVALID),
-    (dict(T=math.nan), INVALID), (dict(T=math.inf), INVALID), (dict(z=None), INVALID), (dict(t=None), INVALID),
+    (dict(T=2.0 ** -41), INVALID), (dict(T=2.0 ** 41), INVALID), (dict(T=math.nan), INVALID), (dict(T=math.inf), INVALID), (dict(z=None), INVALID), (dict(t=None), INVALID),
     (dict(index=None), INVALID), (dict(z=P + 2), MISALIGNED), (dict(t=2 * P + 2), MISALIGNED),
     (dict(index=3 * P + 2), MISALIGNED), (dict(weight=4 * P + 1), MISALIGNED),
 ]

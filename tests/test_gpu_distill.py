@@ -128,6 +128,41 @@ def test_strides_places_and_alignment(V, pad, dtype):
     assert torch.equal(copy[:, 1:V + 1], apart_grad)
 
 
+@pytest.mark.parametrize("T", [2.0 ** -40, 2.0 ** 40])
+def test_outermost_temperatures(T):
+    """Nearest to an argmax, and nearest to equal probabilities: what the loss
+    and its gradient tend to there, and no overflow on the way."""
+    z, t, idx, w = make(5, 600, 4, "f32", 13)
+    loss, lse = sam.distill_loss(z, t, idx, w, T)
+    both, grad = sam.distill(z, t, idx, w, T)
+    assert all(torch.isfinite(x).all() for x in (loss, lse, both, grad))
+    if T < 1:
+        top, best = z.argmax(1), idx.gather(1, t.argmax(1, keepdim=True).long())[:, 0].long()
+        want = torch.zeros_like(z).scatter_add_(1, top[:, None], (w * T)[:, None])
+        want.scatter_add_(1, best[:, None], -(w * T)[:, None])
+    else:   # q = 1 / V, p = 1 / top, each off by its exponents' 8 / T and FP32 sums' steps
+        want = torch.full_like(z, 1 / 600).scatter_add_(1, idx.long(), torch.full_like(t, -0.25)) * (w * T)[:, None]
+    assert ((grad - want).abs() <= 2.0 ** -20 * (w * T)[:, None]).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_workgroups_take_many_rows(dtype):
+    """More rows than workgroups, so that each takes several: rows that are not
+    trained on, empty and masked ones between the others, odd lengths."""
+    for R, V in ((3500, 1001), (2300, 9001), (1100, 20011)):
+        z, t, idx, w = make(R, V, 70, dtype, 14)
+        w[::3] = 0.0
+        z[w == 0] = math.nan
+        idx[1::5] = -1
+        z[2::7] = torch.where(w[2::7, None] == 0, z[2::7], torch.full_like(z[2::7], -math.inf))
+        idx[4::9, 30:] = idx[4::9, :40]
+        zz = torch.where(w[:, None] == 0, torch.zeros_like(z), z)     # the reference has no such rows
+        want = ref.reference(zz, t, idx, w, 1.5)
+        loss, grad = sam.distill(z, t, idx, w, 1.5)
+        ref.close(loss, *want[0])
+        ref.close(grad, *want[2])
+
+
 def test_gradient_is_the_loss_difference():
     """Central differences of the loss in a random direction, step h: off by
     O(h^2) of the third derivative and by the loss's FP32 error over h."""
