@@ -49,8 +49,9 @@ Product choose(long long rows, long long cols, long long k)
     const AdapterTile t = adapter_tile(p.tile);
     p.tiles_m = (int)((rows + t.bm - 1) / t.bm);
     p.tiles_n = (int)((cols + t.bn - 1) / t.bn);
-    const long long target = p.tile == 2 ? kCUs : 2 * kCUs;
-    long long s = target / ((long long)p.tiles_m * p.tiles_n);
+    // One workgroup a CU: two read W no faster (one row x 4096 x 4096: 10.5 us
+    // with two, 9.2 with one) and leave twice the partials.
+    long long s = kCUs / ((long long)p.tiles_m * p.tiles_n);
     const long long most = (k + 4 * kBK - 1) / (4 * kBK);
     s = s < 1 ? 1 : (s > most ? most : s);
     p.k_chunk = (int)(((k + s - 1) / s + kBK - 1) / kBK * kBK);
@@ -76,7 +77,7 @@ struct Layout {
     bool pad_x, pad_w, pad_a, pad_b, pad_dy;
     long long lx, lw, la, lb, ldy; // row strides that the kernels see
     Region x, w, a, b, dy;         // padded copies
-    Region t32, t32b, t16, factor, factor2, part, order, seg, outer;
+    Region t32, t32b, t16, factor, factor2, part, order, seg, chunk_first, chunks, outer;
     int chunk, max_chunks;
     unsigned long long total;
 };
@@ -140,21 +141,27 @@ Layout layout(const Call& c)
     // Shrink. Many rows: 64 a workgroup, K cut such that two workgroups a CU
     // share the work (at least 256 values of K each). Up to 128 rows: 16 a
     // workgroup, the distinct adapters of a block (up to 16) and K ranges of
-    // what a workgroup loads at once on workgroups of their own.
+    // what a workgroup loads at once on workgroups of their own. In the first
+    // form a block's second adapter has a workgroup too, and the CUs room for
+    // 64 of them: few blocks have one in long runs, but two passes of one
+    // workgroup, or one that starts when another ends, last as long as two of
+    // all (4096 x 11008, rank 64, 4 adapters in runs: 39 us, so SLOT_US).
     const int sides = c.back && c.want_ad ? 2 : 1;
     const long long blocks = (c.M + 15) / 16, longest = c.back && c.N > c.K ? c.N : c.K;
     L.wide = blocks > 8;
     L.merged = !c.back && L.prod.split > 0 && L.prod.tile >= 3;
-    L.slots = L.wide ? 1 : (int)(c.n < 16 ? (c.n < 1 ? 1 : c.n) : 16);
     long long s, most;
     if (L.wide) {
-        s = 2 * kCUs / ((c.M + 63) / 64 * sides);
+        s = (2 * kCUs - 64) / ((c.M + 63) / 64 * sides);
         most = (longest + 255) / 256;
     } else {
         s = (longest + 1023) / 1024 * (L.merged && L.prod.tile == 5 ? 2 : 1);   // waves: four, or the narrowest tile's two
         most = 16;
     }
     L.ksplit = (int)(s < 1 ? 1 : (s > most ? most : s));
+    s = L.wide ? 4 * kCUs / ((c.M + 63) / 64 * sides * L.ksplit) : 16;
+    s = L.wide ? (s < 2 ? 2 : (s > 8 ? 8 : s)) : s;
+    L.slots = (int)(s > c.n ? (c.n ? c.n : 1) : s);
     // T inside a tile as two values of the operands' type (16 or 22 bits); an
     // FP32 result of bfloat16 gets three, all 24.
     L.np = c.dtype == SAM_BF16 && c.out == SAM_F32 ? 3 : 2;
@@ -187,6 +194,8 @@ Layout layout(const Call& c)
         L.chunk = (int)chunk;
         L.max_chunks = (int)((c.M + chunk - 1) / chunk + (c.n < c.M ? c.n : c.M));
         take(L.outer, 4ull * L.max_chunks * c.r * (c.K + c.N));
+        take(L.chunk_first, 4ull * (c.n + 1));
+        take(L.chunks, 16ull * (L.max_chunks + 1));
     }
     L.total = at;
     return L;
@@ -278,6 +287,10 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
                 a.side[1].factor = static_cast<float*>(at(L.factor2));
                 a.order = static_cast<int*>(at(L.order));
                 a.seg = static_cast<int*>(at(L.seg));
+                a.chunk = L.chunk;
+                a.max_chunks = L.max_chunks;
+                a.chunk_first = static_cast<int*>(at(L.chunk_first));
+                a.chunks = static_cast<int4*>(at(L.chunks));
             }
         }
         if (e == hipSuccess && !L.merged && (c.M > 0 || c.want_ad)) e = launch_adapter_shrink(c.dtype, a, s);
@@ -343,9 +356,9 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
         o.r = (int)c.r;
         o.rp = L.rp;
         o.order = static_cast<const int*>(at(L.order));
-        o.seg = static_cast<const int*>(at(L.seg));
-        o.chunk = L.chunk;
         o.max_chunks = L.max_chunks;
+        o.chunk_first = a.chunk_first;
+        o.chunks = a.chunks;
         float* part = static_cast<float*>(at(L.outer));
         o.side[0] = {static_cast<const float*>(at(L.t32b)), static_cast<const float*>(at(L.factor)), p.X, L.lx, (int)c.K,
                      p.dA, part};

@@ -46,6 +46,11 @@ struct ShrinkArgs {
     // Grouping of rows by adapter, done by n further workgroups (backward):
     int* order;          // [M] rows sorted by adapter, in row order inside one; null: no grouping
     int* seg;            // [n + 1] where each adapter's rows start in it
+    // ... and chunks of its rows, listed by the second kernel:
+    int chunk;           // rows per chunk
+    int max_chunks;      // ceil(M / chunk) + min(n, M)
+    int* chunk_first;    // [n + 1] each adapter's first chunk
+    int4* chunks;        // [max_chunks] adapter (-1: no such chunk), place in `order`, rows, first row of a run or -1
 };
 
 // Sum of the split partials of X W plus T B.
@@ -100,9 +105,9 @@ struct OuterArgs {
     OuterSide side[2];
     int M, n, r, rp;
     const int* order;
-    const int* seg;
-    int chunk;           // rows per chunk
-    int max_chunks;      // ceil(M / chunk) + min(n, M)
+    int max_chunks;      // as in ShrinkArgs
+    const int* chunk_first;
+    const int4* chunks;
 };
 
 constexpr int kMaxPads = 5;

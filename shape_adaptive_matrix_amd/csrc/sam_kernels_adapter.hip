@@ -53,38 +53,63 @@ __device__ __forceinline__ void split3_bits(float v, unsigned short (&o)[3])
 constexpr int kShrinkWaves = 4, kWideRows = 64;
 
 // Rows sorted by adapter, one workgroup per adapter: it counts the valid ids
-// below its own (where its rows start) and writes its rows in row order.
+// below its own (where its rows start) and writes its rows in row order. Each
+// wave has a range of the rows, eight loads under way at once.
 template <int NW>
-__device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad, int (&sums)[NW])
+__device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad, int (&sums)[2 * NW])
 {
-    constexpr int NT = NW * 64;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int below = 0;
-    for (int m = tid; m < a.M; m += NT) below += (unsigned)a.ids[m] < (unsigned)ad;
+    constexpr int U = 8;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int per = ((a.M + NW * 64 - 1) / (NW * 64)) * 64;
+    const int m0 = min(wave * per, a.M), m1 = min(m0 + per, a.M);
+    auto load = [&](int m, int (&id)[U]) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) below += __shfl_xor(below, d);
-    if (lane == 0) sums[wave] = below;
-    __syncthreads();
-    int at = 0;
+        for (int u = 0; u < U; ++u) id[u] = a.ids[min(m + 64 * u + lane, a.M - 1)];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) at += sums[w];
-    if (tid == 0) a.seg[ad] = at;
-    for (int m0 = 0; m0 < a.M; m0 += NT) {
-        const int m = m0 + tid;
-        const bool mine = m < a.M && a.ids[m] == ad;
-        const unsigned long long b = __ballot(mine);
-        __syncthreads();   // the last step's sums are read
-        if (lane == 0) sums[wave] = __popcll(b);
-        __syncthreads();
-        int before = at;
+        for (int u = 0; u < U; ++u)
+            if (m + 64 * u + lane >= m1) id[u] = -1;
+    };
+    int below = 0, mine = 0;
+    for (int m = m0; m < m1; m += 64 * U) {
+        int id[U];
+        load(m, id);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            before += w < wave ? sums[w] : 0;
-            at += sums[w];
+        for (int u = 0; u < U; ++u) {
+            below += (unsigned)id[u] < (unsigned)ad;
+            mine += id[u] == ad;
         }
-        if (mine) a.order[before + __popcll(b & ((1ull << lane) - 1))] = m;
     }
-    if (tid == 0 && ad == a.n - 1) a.seg[a.n] = at;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        below += __shfl_xor(below, d);
+        mine += __shfl_xor(mine, d);
+    }
+    if (lane == 0) {
+        sums[wave] = below;
+        sums[NW + wave] = mine;
+    }
+    __syncthreads();
+    int at = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        at += sums[w] + (w < wave ? sums[NW + w] : 0);
+        all += sums[w] + sums[NW + w];
+    }
+    if (tid == 0) {
+        a.seg[ad] = at;
+        if (ad == a.n - 1) a.seg[a.n] = all;
+    }
+    for (int m = m0; m < m1; m += 64 * U) {
+        int id[U];
+        load(m, id);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned long long b = __ballot(id[u] == ad);
+            if (id[u] == ad) a.order[at + __popcll(b & ((1ull << lane) - 1))] = m + 64 * u + lane;
+            at += __popcll(b);
+        }
+    }
 }
 
 // Rounds a row of T, held by 32 threads (column c0 + 32 q): divides by the
@@ -128,10 +153,10 @@ __device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide&
 template <int DT>
 __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_kernel(ShrinkArgs a)
 {
-    __shared__ int sums[kShrinkWaves];
+    __shared__ int sums[2 * kShrinkWaves];
     const int wgs = shrink_wgs(a);
     if ((int)blockIdx.x >= wgs)
-        group_rows(a, blockIdx.x - wgs, sums);
+        group_rows<kShrinkWaves>(a, blockIdx.x - wgs, sums);
     else
         shrink_part<DT, kShrinkWaves>(a, blockIdx.x);
 }
@@ -161,66 +186,105 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_wide_kernel(
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int blocks = (a.M + kWideRows - 1) / kWideRows;
     int wg = blockIdx.x;
-    const int per_side = blocks * a.ksplit;
-    if (wg >= per_side * a.sides) {
-        group_rows(a, wg - per_side * a.sides, *reinterpret_cast<int(*)[NW]>(lds));
-        return;
+    if (a.order) {   // first, for they take longest
+        if (wg < a.n) {
+            group_rows<NW>(a, wg, *reinterpret_cast<int(*)[2 * NW]>(lds));
+            return;
+        }
+        wg -= a.n;
     }
-    const ShrinkSide& sd = a.side[wg >= per_side];
-    if (wg >= per_side) wg -= per_side;
+    // A block's further adapters first, too: behind all others they would
+    // start when those end.
+    const int per_slot = blocks * a.ksplit * a.sides;
+    const int slot = a.slots - 1 - wg / per_slot;
+    wg %= per_slot;
+    const int second = wg >= blocks * a.ksplit;
+    const ShrinkSide& sd = a.side[second];
+    if (second) wg -= blocks * a.ksplit;
     const int split = wg / blocks;
     const int m0 = (wg - split * blocks) * kWideRows;
+    // The K ranges take stages in turn, so that a row's neighbouring pieces
+    // are read at the same time.
     const int stages = (sd.K + BK - 1) / BK;
-    const int st0 = (int)((long long)stages * split / a.ksplit);
-    const int nk = (int)((long long)stages * (split + 1) / a.ksplit) - st0;
+    const int nk = (stages - split + a.ksplit - 1) / a.ksplit;
 
     int id = m0 + lane < a.M ? a.ids[m0 + lane] : -1;
     if ((unsigned)id >= (unsigned)a.n) id = -1;
     unsigned long long left = __ballot(id >= 0);
-    const i4 rX = rsrc_words(static_cast<const char*>(sd.X) + (long long)m0 * sd.ldx * 2, (long long)(a.M - m0) * sd.ldx * 2);
+    const char* Xb = static_cast<const char*>(sd.X) + (long long)m0 * sd.ldx * 2;
     const int lrow = lane & 15, grp = lane >> 4;
 
-    while (left) {
+    for (int d = 0; left; ++d) {
         const int ad = __builtin_amdgcn_readlane(id, __ffsll((long long)left) - 1);
         const unsigned long long same = __ballot(id == ad);
         left &= ~same;
-        const i4 rA = rsrc_words(static_cast<const char*>(sd.A) + (long long)ad * a.r * sd.lda * 2,
-                                 (long long)a.r * sd.lda * 2);
-        // Stages past the last one read zeros: the waits count on every load.
-        auto load = [&](int st) {
-            unsigned char* buf = lds + st % NBUF * STAGE;
+        if (d % a.slots != slot) continue;
+        const char* Ab = static_cast<const char*>(sd.A) + (long long)ad * a.r * sd.lda * 2;
+        // A lane's places in the rows, kept; a stage moves the base. Stages
+        // past the last one read zeros: the waits count on every load.
+        int off[LPS];
+        const int tail = sd.K % BK;   // values of K in a last stage that is not whole
 #pragma unroll
-            for (int q = 0; q < LPS; ++q) {
-                const bool x = q < X_PW;
-                const int I = wave + (x ? q : q - X_PW) * NW;
-                const int row = I * RPL + lane / CP;
-                const int k = (st0 + st) * BK + (lane % CP ^ row / RSW % CP) * 8;
-                const bool ok = st < nk && k < sd.K && (x ? (same >> row) & 1 : row < a.r);
-                const int off = ok ? (int)((row * (x ? sd.ldx : sd.lda) + k) * 2) : kOOB;
-                lds_load16(x ? rX : rA, lds_addr(buf + (x ? 0 : XB) + I * 1024), off);
+        for (int q = 0; q < LPS; ++q) {
+            const int row = (wave + (q < X_PW ? q : q - X_PW) * NW) * RPL + lane / CP;
+            const bool ok = q < X_PW ? (same >> row) & 1 : row < a.r;
+            off[q] = ok ? (int)((row * (q < X_PW ? sd.ldx : sd.lda) + (lane % CP ^ row / RSW % CP) * 8) * 2) : kOOB;
+        }
+        const long long step = (long long)a.ksplit * BK * 2;
+        const char *xk = Xb + (long long)split * BK * 2, *ak = Ab + (long long)split * BK * 2;   // of the next stage to load
+        int next = 0;
+        const int x_lds = __builtin_amdgcn_readfirstlane(lds_addr(lds)) + wave * 1024;
+        auto load = [&](int b) {   // into stage b of the ring
+            const bool in = next < nk;
+            const i4 sX = rsrc_words(xk, in ? kOOB : 0), sA = rsrc_words(ak, in ? kOOB : 0);
+            auto one = [&](int q, int o) {
+                lds_load16(q < X_PW ? sX : sA, x_lds + b * STAGE + (q < X_PW ? q * NW * 1024 : XB + (q - X_PW) * NW * 1024), o);
+            };
+            if (tail && next * a.ksplit + split == stages - 1) {
+#pragma unroll
+                for (int q = 0; q < LPS; ++q) {
+                    const int row = (wave + (q < X_PW ? q : q - X_PW) * NW) * RPL + lane / CP;
+                    one(q, (lane % CP ^ row / RSW % CP) * 8 >= tail ? kOOB : off[q]);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < LPS; ++q) one(q, off[q]);
             }
+            ++next;
+            xk += step;
+            ak += step;
         };
         v4f acc[NR];
 #pragma unroll
         for (int q = 0; q < NR; ++q) acc[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
         wait_cnt<0, 15>();   // the counts below are of the ring's loads alone
 #pragma unroll
-        for (int st = 0; st < NBUF - 1; ++st) load(st);
-        for (int st = 0; st < nk; ++st) {
-            wait_cnt<(NBUF - 2) * LPS, 0>();   // this wave's part of the stage is there; its reads of the last one are done
-            barrier();
-            load(st + NBUF - 1);               // into the stage that all waves have left
-            const unsigned char* buf = lds + st % NBUF * STAGE;
+        for (int b = 0; b < NBUF - 1; ++b) load(b);
+        // The ring's stages unrolled: their places are constants.
+        for (int st = 0; st < nk; st += NBUF)
 #pragma unroll
-            for (int t = 0; t < BK / 32; ++t) {
-                auto piece = [&](const unsigned char* base, int row) {
-                    return *reinterpret_cast<const u4*>(base + row * ROW + (4 * t + grp ^ row / RSW % CP) * 16);
+            for (int b = 0; b < NBUF; ++b) {
+                if (st + b >= nk) break;
+                wait_cnt<(NBUF - 2) * LPS, 0>();   // this wave's part of the stage is there; its reads of the last one are done
+                barrier();
+                load((b + NBUF - 1) % NBUF);       // into the stage that all waves have left
+                // All fragments of the stage, then its MFMAs: one LDS latency a stage, not one each.
+                auto piece = [&](int place, int t, int row) {
+                    return *reinterpret_cast<const u4*>(lds + b * STAGE + place + row * ROW + ((4 * t + grp) ^ (row / RSW % CP)) * 16);
                 };
-                const u4 fx = piece(buf, 16 * wave + lrow);
+                u4 fx[BK / 32], fa[BK / 32][NR];
 #pragma unroll
-                for (int q = 0; q < NR; ++q) Mf<DT, 16>::mfma(acc[q], fx, piece(buf + XB, 16 * q + lrow));
+                for (int t = 0; t < BK / 32; ++t) {
+                    fx[t] = piece(0, t, 16 * wave + lrow);
+#pragma unroll
+                    for (int q = 0; q < NR; ++q) fa[t][q] = piece(XB, t, 16 * q + lrow);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int t = 0; t < BK / 32; ++t)
+#pragma unroll
+                    for (int q = 0; q < NR; ++q) Mf<DT, 16>::mfma(acc[q], fx[t], fa[t][q]);
             }
-        }
         // Nothing in flight, nothing unread, before the ring is filled again.
         wait_cnt<0, 0>();
         barrier();
@@ -237,11 +301,53 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_wide_kernel(
     }
 }
 
+// The adapters' rows cut into chunks of a.chunk, numbered in adapter order:
+// where each adapter's chunks start, and each chunk's place. One workgroup.
+__device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
+{
+    __shared__ int sums[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int base = 0;
+    for (int a0 = 0; a0 < a.n; a0 += 256) {
+        const int ad = a0 + tid;
+        const int begin = ad < a.n ? a.seg[ad] : 0, rows = ad < a.n ? a.seg[ad + 1] - begin : 0;
+        const int count = (rows + a.chunk - 1) / a.chunk;
+        int sum = count;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int o = __shfl_up(sum, d);
+            if (lane >= d) sum += o;
+        }
+        __syncthreads();   // the last step's sums are read
+        if (lane == 63) sums[wave] = sum;
+        __syncthreads();
+        int first = base + sum - count;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            first += w < wave ? sums[w] : 0;
+            base += sums[w];
+        }
+        if (ad < a.n) a.chunk_first[ad] = first;
+        for (int c = 0; c < count; ++c) {
+            const int at = begin + c * a.chunk, n = min(a.chunk, rows - c * a.chunk);
+            const int row0 = a.order[at];
+            // Rows of one run need no look-up.
+            a.chunks[first + c] = make_int4(ad, at, n, a.order[at + n - 1] - row0 == n - 1 ? row0 : -1);
+        }
+    }
+    if (tid == 0) a.chunk_first[a.n] = base;
+    for (int c = base + tid; c < a.max_chunks; c += 256) a.chunks[c] = make_int4(-1, 0, 0, -1);
+}
+
 // The sum of a row's partials in K order, into the first of them, and its
 // rounded form. 32 threads per row, rows without an adapter left out.
 template <int DT, int NQ>
 __global__ void __launch_bounds__(256) adapter_round_kernel(ShrinkArgs a)
 {
+    if ((int)blockIdx.x >= (a.M + 7) / 8) {
+        if (blockIdx.y == 0) list_chunks(a);
+        return;
+    }
     const int c0 = threadIdx.x & 31;
     const int m = blockIdx.x * 8 + (threadIdx.x >> 5);
     const ShrinkSide& sd = a.side[blockIdx.y];
@@ -287,11 +393,11 @@ __device__ __forceinline__ void floats_of(const uint2& w, float (&o)[4])
 // then comes from L1 for three of them).
 // Bound by latency: nothing that is loaded depends on anything but the row's
 // id, so all first loads go out before the first is used. Measured at 64 rows
-// x 11008, rank 16, 5 partials: 11 us (one load at a time 39).
+// x 11008, rank 16, 2 partials: 6.8 us (one load at a time, 5 partials: 39).
 template <int DT, int WS>
 __global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
 {
-    constexpr int U = 8;   // loads of a kind under way at once
+    constexpr int UP = WS == 4 ? 4 : 8, UB = 8;   // partials, rows of B under way at once; what is more than there are comes from L1
     __shared__ float4 red[3][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -306,19 +412,19 @@ __global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
     int id = a.ids[m];
     if ((unsigned)id >= (unsigned)a.n || i0 == i1) id = -1;
 
-    float4 w[U];
+    float4 w[UP];
     auto load_parts = [&](int s) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < UP; ++u)
             w[u] = *reinterpret_cast<const float4*>(a.part + ((long long)min(s + u, a.split - 1) * a.M + m) * a.ldp + cc);
     };
     // T of the wave's ranks, a lane each (two with more than 64), summed over its own partials.
     float t[2] = {0.0f, 0.0f};
-    uint2 wb[U];
+    uint2 wb[UB];
     const unsigned short* B = static_cast<const unsigned short*>(a.B) + (long long)max(id, 0) * a.r * a.ldb + cc;
     auto load_b = [&](int i) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) wb[u] = *reinterpret_cast<const uint2*>(B + min(i + u, i1 - 1) * a.ldb);
+        for (int u = 0; u < UB; ++u) wb[u] = *reinterpret_cast<const uint2*>(B + min(i + u, i1 - 1) * a.ldb);
     };
     load_parts(s0);
     if (id >= 0) {
@@ -328,29 +434,30 @@ __global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
             const int i = i0 + 64 * q + lane;
             const float* tp = a.t32 + (long long)m * a.rp + min(i, i1 - 1);
             const long long step = (long long)a.M * a.rp;
-            for (int s = 0; s < a.tsplit; s += U) {
-                float x[U];
+            t[q] = *tp;
+            for (int s = 1; s < a.tsplit; s += 8) {
+                float x[8];
 #pragma unroll
-                for (int u = 0; u < U; ++u) x[u] = tp[min(s + u, a.tsplit - 1) * step];
+                for (int u = 0; u < 8; ++u) x[u] = tp[min(s + u, a.tsplit - 1) * step];
 #pragma unroll
-                for (int u = 0; u < U; ++u) t[q] += s + u < a.tsplit ? x[u] : 0.0f;
+                for (int u = 0; u < 8; ++u) t[q] += s + u < a.tsplit ? x[u] : 0.0f;
             }
         }
     }
     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int s = s0; s < s1;) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < UP; ++u)
             if (s + u < s1) {
                 y.x += w[u].x; y.y += w[u].y; y.z += w[u].z; y.w += w[u].w;
             }
-        s += U;
+        s += UP;
         if (s < s1) load_parts(s);
     }
     if (id >= 0)
         for (int i = i0; i < i1;) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < UB; ++u)
                 if (i + u < i1) {
                     const int j = i + u - i0;
                     const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(t[WS == 4 ? 0 : j >> 6]), j & 63));
@@ -359,7 +466,7 @@ __global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
                     y.z = fmaf(f, from_bits<DT>((unsigned short)wb[u].y), y.z);
                     y.w = fmaf(f, from_bits<DT>((unsigned short)(wb[u].y >> 16)), y.w);
                 }
-            i += U;
+            i += UB;
             if (i < i1) load_b(i);
         }
     if constexpr (WS == 4) {
@@ -399,53 +506,6 @@ __global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
     }
 }
 
-// Which adapter's chunk `want` is, and which of its chunks: adapters' rows
-// are cut into chunks of `chunk` rows, numbered in adapter order. Every lane
-// of the wave gets the answer; ad = -1 past the last chunk.
-struct Chunk {
-    int ad, first, count;   // adapter, its first chunk's number, its chunks
-};
-
-__device__ __forceinline__ Chunk find_chunk(const int* seg, int n, int chunk, int want)
-{
-    const int lane = threadIdx.x & 63;
-    int base = 0;
-    for (int a0 = 0; a0 < n; a0 += 64) {
-        const int ad = a0 + lane;
-        const int c = ad < n ? (seg[ad + 1] - seg[ad] + chunk - 1) / chunk : 0;
-        int sum = c;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
-        }
-        const unsigned long long hit = __ballot(want < base + sum);
-        if (hit) {
-            const int l = __ffsll((long long)hit) - 1;
-            return {a0 + l, base + __shfl(sum - c, l), __shfl(c, l)};
-        }
-        base += __shfl(sum, 63);
-    }
-    return {-1, 0, 0};
-}
-
-// The adapter's chunks and the number of its first one.
-__device__ __forceinline__ Chunk chunks_of(const int* seg, int n, int chunk, int want_ad)
-{
-    const int lane = threadIdx.x & 63;
-    int first = 0, count = 0;
-    for (int a0 = 0; a0 <= want_ad; a0 += 64) {
-        const int ad = a0 + lane;
-        const int c = ad < n ? (seg[ad + 1] - seg[ad] + chunk - 1) / chunk : 0;
-        int s = ad < want_ad ? c : 0;
-#pragma unroll
-        for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-        first += s;
-        if (want_ad - a0 < 64) count = __shfl(c, want_ad - a0);
-    }
-    return {want_ad, first, count};
-}
-
 constexpr int kOuterCols = 256;
 
 // out[ad][i][c] = sum over a chunk's rows m of T[m][i] X[m][c], for 256
@@ -481,15 +541,11 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
     const OuterSide& sd = a.side[second];
     const int wg = second ? blockIdx.x - wgs0 : blockIdx.x;
     const int ch = wg % a.max_chunks, c0 = (wg / a.max_chunks) * kOuterCols;
-    const Chunk w = find_chunk(a.seg, a.n, a.chunk, ch);
-    const int ad = __builtin_amdgcn_readfirstlane(w.ad);
+    const int4 w = a.chunks[ch];
+    const int ad = w.x, rows = w.z, row0 = w.w;
     if (ad < 0) return;
-    const int begin = a.seg[ad] + (ch - w.first) * a.chunk;
-    const int rows = min(a.chunk, a.seg[ad + 1] - begin);
-    const int* order = a.order + begin;
-    // Rows of one run need no look-up: a load less in front of X's.
-    const int row0 = order[0];
-    const bool run = order[rows - 1] - row0 == rows - 1;
+    const int* order = a.order + w.y;
+    const bool run = row0 >= 0;
 
     // The chunk's scale: the largest of its rows' factors.
     int e = 0;
@@ -605,7 +661,7 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
         __syncthreads();
         multiply(s);
     }
-    const bool direct = w.count == 1;
+    const bool direct = a.chunk_first[ad + 1] - a.chunk_first[ad] == 1;
     float* o = direct ? sd.out + (long long)ad * a.r * sd.cols : sd.part + (long long)ch * a.r * sd.cols;
     const float back = ldexpf(1.0f, e);
 #pragma unroll
@@ -629,25 +685,25 @@ __global__ void __launch_bounds__(256) adapter_outer_sum_kernel(OuterArgs a)
     const long long v0 = (long long)a.r * a.side[0].cols, v1 = (long long)a.r * a.side[1].cols;
     const int b0 = (int)((v0 + 1023) / 1024), b1 = (int)((v1 + 1023) / 1024);
     const int ad = blockIdx.x / (b0 + b1), b = blockIdx.x % (b0 + b1);
-    const Chunk w = chunks_of(a.seg, a.n, a.chunk, ad);
-    if (w.count == 1) return;
+    const int first = a.chunk_first[ad], count = a.chunk_first[ad + 1] - first;
+    if (count == 1) return;
     const bool second = b >= b0;
     const OuterSide& sd = a.side[second];
     const long long vals = second ? v1 : v0;
     const long long at = (long long)(second ? b - b0 : b) * 1024 + threadIdx.x;
     float* out = sd.out + (long long)ad * vals;
-    const float* part = sd.part + (long long)w.first * vals;
+    const float* part = sd.part + (long long)first * vals;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const long long i = at + 256 * q;
         if (i >= vals) continue;
         float v = 0.0f;
-        for (int c = 0; c < w.count; c += 8) {
+        for (int c = 0; c < count; c += 8) {
             float x[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = part[(long long)min(c + u, w.count - 1) * vals + i];
+            for (int u = 0; u < 8; ++u) x[u] = part[(long long)min(c + u, count - 1) * vals + i];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v += c + u < w.count ? x[u] : 0.0f;
+            for (int u = 0; u < 8; ++u) v += c + u < count ? x[u] : 0.0f;
         }
         out[i] = v;
     }
@@ -701,7 +757,7 @@ hipError_t shrink_dt(const ShrinkArgs& a, hipStream_t s)
     const int more = a.order ? a.n : 0;
     const dim3 block(kShrinkWaves * 64);
     if (a.wide) {
-        const dim3 grid((unsigned)((a.M + kWideRows - 1) / kWideRows * a.ksplit * a.sides + more));
+        const dim3 grid((unsigned)((a.M + kWideRows - 1) / kWideRows * a.slots * a.ksplit * a.sides + more));
         switch (a.rp) {
         case 16: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 1>), grid, block, 0, s, a); break;
         case 32: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 2>), grid, block, 0, s, a); break;
@@ -713,8 +769,8 @@ hipError_t shrink_dt(const ShrinkArgs& a, hipStream_t s)
         hipLaunchKernelGGL((adapter_shrink_kernel<DT>), dim3((unsigned)(shrink_wgs(a) + more)), block, 0, s, a);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.round || a.M == 0) return e;
-    const dim3 rgrid((unsigned)((a.M + 7) / 8), (unsigned)a.sides), rblock(256);
+    if (e != hipSuccess || !a.round) return e;
+    const dim3 rgrid((unsigned)((a.M + 7) / 8 + (a.order ? 1 : 0)), (unsigned)a.sides), rblock(256);
     switch ((a.rp + 31) / 32) {
     case 1: hipLaunchKernelGGL((adapter_round_kernel<DT, 1>), rgrid, rblock, 0, s, a); break;
     case 2: hipLaunchKernelGGL((adapter_round_kernel<DT, 2>), rgrid, rblock, 0, s, a); break;
@@ -751,9 +807,10 @@ hipError_t launch_adapter_shrink(int dtype, const ShrinkArgs& a, hipStream_t s)
 
 hipError_t launch_adapter_finish(int dtype, const FinishArgs& a, hipStream_t s)
 {
-    // Four waves a row while that fills the CUs no more than four times over.
+    // Four waves a row while that leaves CUs free (64 rows x 11008: 9.2 us with
+    // four, 6.8 with one; one row x 4096: 3.6 and 8.1).
     const long long strips = (a.N + 255) / 256;
-    const bool share = strips * a.M <= 4 * 256 * 8;
+    const bool share = strips * a.M <= 1024;
     const dim3 grid((unsigned)(strips * (share ? a.M : (a.M + 3) / 4))), block(256);
     if (dtype == DT_BF16) {
         if (share)

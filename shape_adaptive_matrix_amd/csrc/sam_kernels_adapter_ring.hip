@@ -31,7 +31,7 @@ __device__ __forceinline__ void lds_sync()
 }
 
 struct AdapterHook {
-    static constexpr bool ON = true;
+    static constexpr bool ON = true, B_ONCE = false;
     typedef AdapterRing Args;
     static __device__ __forceinline__ int b_rows(const GemmArgs&, const AdapterRing* x) { return x->N; }
     static constexpr int RC = 32;   // ranks of one adapter in LDS at a time
@@ -218,29 +218,49 @@ struct AdapterHook {
                 const bool ok = row < rows && col < cols;
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), rY, ok ? (row * ldy + col) * 4 : kOOB, 0, 0);
             });
+        } else if (x.out16) {
+            // Rows that do not start on 8 bytes. Where they do not start on 4
+            // either, a lane stores the four values that do, one to the left
+            // of its own: the first is the last one of the lane (or block)
+            // beside it. Words that do not start on 4 bytes cost more: 2049 x
+            // 4097 over 1025 39 us, this way RAGGED_US.
+            const int hi = min(cols, wn0 + 16 * TN);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int row = wm0 + 16 * i + (lane & 15);
+                unsigned short* y = static_cast<unsigned short*>(x.Y) + (long long)(m0 + row) * x.ldy + n0;
+                const int odd = (int)(((long long)(m0 + row) * x.ldy + n0 + wn0) & 1);
+                unsigned beside = 0;
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const u2 h = half4(acc[i][j]);
+                    const unsigned last = h[1] >> 16;
+                    const unsigned left = __builtin_amdgcn_ds_bpermute(((lane + 48) & 63) * 4, lane >= 48 ? beside : last);
+                    beside = last;
+                    const u2 v = odd ? u2{left | h[0] << 16, h[0] >> 16 | h[1] << 16} : h;
+                    const int col = wn0 + 16 * j + 4 * (lane >> 4) - odd;
+                    if (row >= rows) continue;
+                    if (col >= wn0 && col + 4 <= hi)
+                        __builtin_memcpy(y + col, &v, 8);
+                    else
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (col + q >= wn0 && col + q < hi) y[col + q] = (unsigned short)(v[q >> 1] >> (16 * (q & 1)));
+                    if (odd && j == TN - 1 && lane >= 48 && col + 4 < hi) y[col + 4] = (unsigned short)last;
+                }
+            }
         } else {
-            // Rows that do not start on 8 or 16 bytes: the hardware's
-            // unaligned stores, single values at the end of a row.
-            char* Y = static_cast<char*>(x.Y) + ((long long)m0 * x.ldy + n0) * es;
+            // The hardware's unaligned stores, single values at the end of a row.
+            float* Y = static_cast<float*>(x.Y) + (long long)m0 * x.ldy + n0;
             each([&](const v4f& v, int row, int col) {
                 if (row >= rows || col >= cols) return;
-                const u4 w = x.out16 ? u4{half4(v)[0], half4(v)[1], 0u, 0u} : __builtin_bit_cast(u4, v);
-                char* o = Y + ((long long)row * ldy + col) * es;
-                if (col + 4 <= cols) {
-                    if (x.out16)
-                        __builtin_memcpy(o, &w, 8);
-                    else
-                        __builtin_memcpy(o, &w, 16);
-                } else {
+                float* o = Y + (long long)row * ldy + col;
+                if (col + 4 <= cols)
+                    __builtin_memcpy(o, &v, 16);
+                else
 #pragma unroll
                     for (int q = 0; q < 3; ++q)
-                        if (col + q < cols) {
-                            if (x.out16)
-                                reinterpret_cast<unsigned short*>(o)[q] = (unsigned short)(w[q >> 1] >> (16 * (q & 1)));
-                            else
-                                reinterpret_cast<unsigned*>(o)[q] = w[q];
-                        }
-                }
+                        if (col + q < cols) o[q] = v[q];
             });
         }
     }
@@ -260,8 +280,9 @@ adapter_ring_kernel(AdapterRingArgs a)
 
 // One workgroup per (tile, K range): partials with rows of N rounded up to 8
 // floats, of which the columns past n are not meant to be read.
+template <bool ONCE>
 struct PartHook {
-    static constexpr bool ON = false;
+    static constexpr bool ON = false, B_ONCE = ONCE;
     typedef int Args;
     static __device__ __forceinline__ int b_rows(const GemmArgs&, const int* n) { return *n; }
 };
@@ -275,7 +296,7 @@ adapter_part_kernel(GemmArgs g, int n)
     dma::tile_coords(blockIdx.x, g, tm, tn, s);
     const int kbeg = s * g.k_chunk;
     const int kend = min(g.K, kbeg + g.k_chunk);
-    ring16_segment<DT, BM, BN, WM, WN, 64, NBUF, MODE, 16, 1, false, PartHook>(g, tm, tn, kbeg, kend, nullptr, s, 0, 0,
+    ring16_segment<DT, BM, BN, WM, WN, 64, NBUF, MODE, 16, 1, false, PartHook<false>>(g, tm, tn, kbeg, kend, nullptr, s, 0, 0,
                                                                               true, &n);
 }
 
@@ -295,7 +316,7 @@ adapter_part_shrink_kernel(GemmArgs g, int n, ShrinkArgs a, int more)
     dma::tile_coords(blockIdx.x - more, g, tm, tn, s);
     const int kbeg = s * g.k_chunk;
     const int kend = min(g.K, kbeg + g.k_chunk);
-    ring16_segment<DT, BM, BN, WM, WN, 64, NBUF, MODE, 16, 1, false, PartHook>(g, tm, tn, kbeg, kend, nullptr, s, 0, 0,
+    ring16_segment<DT, BM, BN, WM, WN, 64, NBUF, MODE, 16, 1, false, PartHook<true>>(g, tm, tn, kbeg, kend, nullptr, s, 0, 0,
                                                                               true, &n);
 }
 

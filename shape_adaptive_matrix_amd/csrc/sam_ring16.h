@@ -132,9 +132,9 @@ __device__ __forceinline__ int nsw(int row) { return (4 * (row & 3)) ^ (2 * ((ro
 // three calls: `before` ahead of the ring's first loads, `start` behind them,
 // with the accumulators still zero, and `store` in place of the stores of C.
 // b_rows: how many rows B given transposed has (a hook may run with N, the
-// stored width, rounded up).
+// stored width, rounded up). B_ONCE: no other tile reads this one's B.
 struct RingPlain {
-    static constexpr bool ON = false;
+    static constexpr bool ON = false, B_ONCE = false;
     typedef int Args;
     static __device__ __forceinline__ int b_rows(const GemmArgs& a, const int*) { return a.N; }
 };
@@ -255,7 +255,11 @@ __device__ __forceinline__ void ring16_segment(const GemmArgs& args, int tm, int
             const bool ok = n0 + row < NB && gk < kend;
             const i4 rBt = rsrc_words(static_cast<const char*>(args.B) + (long long)n0 * ldb * 2,
                                       (long long)(NB - n0) * ldb * 2);
-            lds_load16(rBt, lds_addr(buf + A_BYTES + I * 1024), ok ? (row * ldb + gk) * 2 : kOOB);
+            const int off = ok ? (row * ldb + gk) * 2 : kOOB;
+            if constexpr (HOOK::B_ONCE)
+                lds_load16_once(rBt, lds_addr(buf + A_BYTES + I * 1024), off);
+            else
+                lds_load16(rBt, lds_addr(buf + A_BYTES + I * 1024), off);
         } else {
             const int I = wave + (q - A_PW) * NW;
             const int row = I * RPI + lane / CPR;
@@ -265,7 +269,10 @@ __device__ __forceinline__ void ring16_segment(const GemmArgs& args, int tm, int
             const int off = ok ? (row * ldb + c * 8) * 2 : kOOB;
             if constexpr (DIRECT) {
                 const i4 rB = rsrc_words(static_cast<const char*>(args.B) + bbase, b_bytes - bbase);
-                lds_load16(rB, lds_addr(buf + A_BYTES + I * 1024), off);
+                if constexpr (HOOK::B_ONCE)
+                    lds_load16_once(rB, lds_addr(buf + A_BYTES + I * 1024), off);
+                else
+                    lds_load16(rB, lds_addr(buf + A_BYTES + I * 1024), off);
             } else {
                 const __amdgpu_buffer_rsrc_t rB = make_rsrc(static_cast<const char*>(args.B) + bbase, b_bytes - bbase);
                 R[q] = __builtin_amdgcn_raw_buffer_load_b128(rB, off, 0, 0);
