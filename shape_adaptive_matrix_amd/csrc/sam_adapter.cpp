@@ -187,10 +187,12 @@ Layout layout(const Call& c)
     }
     if (L.prod.split > 0 && (!c.back || c.want_dx)) take(L.part, 4ull * L.prod.split * c.M * round8(cols));
     if (c.back && c.want_ad && c.n) {
-        // Chunks of rows such that about four workgroups a CU share the work.
+        // Chunks of rows such that two to four workgroups a CU share the work
+        // (4096 rows, 8192 columns: 256 rows 22 us, 128 the same and twice the
+        // partials; 1025 rows, 2817 columns: 256 rows 18 us, 64 9 us).
         const long long strips = (c.K + 255) / 256 + (c.N + 255) / 256;
-        long long chunk = 256;
-        while (chunk < (1 << 20) && (c.M / (2 * chunk)) * strips >= 4 * kCUs) chunk *= 2;
+        long long chunk = 64;
+        while (chunk < (1 << 20) && (c.M / (2 * chunk)) * strips >= 2 * kCUs) chunk *= 2;
         L.chunk = (int)chunk;
         L.max_chunks = (int)((c.M + chunk - 1) / chunk + (c.n < c.M ? c.n : c.M));
         take(L.outer, 4ull * L.max_chunks * c.r * (c.K + c.N));

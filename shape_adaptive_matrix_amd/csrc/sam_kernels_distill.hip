@@ -13,6 +13,8 @@ namespace {
 
 typedef unsigned int u4 __attribute__((ext_vector_type(4)));
 
+constexpr int kFewTop = 128;
+
 template <int DT> struct Ty;
 template <> struct Ty<DT_F32> { typedef float T; };
 template <> struct Ty<DT_BF16> { typedef __bf16 T; };
@@ -117,45 +119,15 @@ __device__ __forceinline__ float block_reduce(float v, float* s, F op)
     return v;
 }
 
-// A row's teacher distribution: p[j] and index[j] (-1: empty) in LDS. Returns
-// the sum of the unnormalised weights, 0 if no entry is valid; best: their
-// pivot.
-template <int NT>
-__device__ __forceinline__ float teacher_row(const DistillArgs& a, long long row, float* p, int* idx, float* red, float& best)
+// How many of a row's entries have index i. Their list is -1 up to a multiple of four.
+__device__ __forceinline__ int repeats(const int* idx, int top, int i)
 {
-    float m = -INFINITY;
-    for (int j = threadIdx.x; j < a.top; j += NT) {
-        const int i = a.index[row * a.top + j];
-        const bool ok = (unsigned)i < (unsigned)a.V;
-        const float t = ok ? value_of(raw_at(a.t, a.t_dtype, row * a.top + j), a.t_dtype) : -INFINITY;
-        idx[j] = ok ? i : -1;
-        p[j] = t;
-        m = fmaxf(m, t);
+    int n = 0;
+    for (int k = 0; k < top; k += 4) {
+        const int4 v = *reinterpret_cast<const int4*>(idx + k);
+        n += (v.x == i) + (v.y == i) + (v.z == i) + (v.w == i);
     }
-    best = block_reduce<NT>(m, red, [](float x, float y) { return fmaxf(x, y); });
-    const float pivot = best > -INFINITY ? best : 0.0f;
-    float sum = 0.0f;
-    for (int j = threadIdx.x; j < a.top; j += NT) {
-        const float e = expf((p[j] - pivot) / a.T);
-        sum += e;
-    }
-    return block_reduce<NT>(sum, red, [](float x, float y) { return x + y; });
-}
-
-// p of all entries with entry j's index, or a negative value unless j is the
-// first of them.
-__device__ __forceinline__ float total_p(const DistillArgs& a, const float* p, const int* idx, int j)
-{
-    const int i = idx[j];
-    if (i < 0) return -1.0f;
-    float sum = 0.0f;
-    bool first = true;
-    for (int o = 0; o < a.top; ++o)
-        if (idx[o] == i) {
-            first &= o >= j;
-            sum += p[o];
-        }
-    return first ? sum : -1.0f;
+    return n;
 }
 
 // The part of a row that is whole aligned 16-byte pieces, and the values
@@ -241,14 +213,14 @@ struct Row {
 // teacher's entries go 64 to a wave, and what is to be written behind the
 // whole row (the loss, the entries' own gradients) goes out behind the next
 // row's barrier.
-// Measured, loss and gradient: 4096 x 32768 bf16 110 us (rows on
+// Measured, loss and gradient: 4096 x 32768 bf16 100 us (rows on
 // workgroups of their own, everything between barriers: 123), 1024 x 131072
 // FP32 219 us (274).
 // Waves a SIMD that the registers have to leave room for: with the gradient
 // as many as `run` puts on a CU.
-constexpr int distill_waves(int nt, int p, bool grad) { return !grad ? 1 : (nt == 512 && p == 8 ? 6 : 4); }
+constexpr int distill_waves(int nt, int p, bool grad) { return !grad ? 1 : (nt == 512 && p == 8 ? 6 : nt == 64 && p <= 8 ? 5 : 4); }
 
-template <int DT, int NT, int P, int L, bool REST, bool GRAD>
+template <int DT, int NT, int P, int L, bool REST, bool GRAD, int TOP>
 __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(distill_waves(NT, P, GRAD))))
 distill_kernel(DistillArgs a)
 {
@@ -257,25 +229,36 @@ distill_kernel(DistillArgs a)
     constexpr int E = Pc::E, NW = NT / 64;
     static_assert(P % 4 == 0 && L % 4 == 0, "pieces are summed four at a time");
     __shared__ __attribute__((aligned(16))) u4 hold[L > 0 ? L * NT : 1];
-    __shared__ float val[2][kMaxTop];    // by row parity: the teacher's value
-    __shared__ int idx[2][kMaxTop];      // its index, -1: empty
-    __shared__ float gval[2][kMaxTop];      // an entry's own gradient
-    __shared__ unsigned long long gset[2][kMaxTop / 64];   // and whether it is written, a bit each
+    __shared__ float val[2][TOP];        // by row parity: the teacher's value
+    __shared__ __attribute__((aligned(16))) int idx[2][TOP];   // its index, -1: empty
+    __shared__ float gval[2][TOP];       // an entry's own gradient
+    __shared__ unsigned long long gset[2][TOP / 64];   // and whether it is written, a bit each
     __shared__ float4 part[2][NW];       // a wave's largest logit and sum, its entries' largest and sum
     __shared__ float lsum[2][NW];        // its part of the loss
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int chunks = (a.top + 63) / 64;
 
-    // What is loaded ahead of a row's turn: the wave's first entries, its edge value, its pieces.
+    // What is loaded ahead of a row's turn: its pieces, its edge value, the
+    // wave's first entries and their logits (for which the entries themselves
+    // come two rows ahead).
     u4 r[P];
-    unsigned t, edge;
-    int ix;
+    unsigned t, t_next, zr, edge;
+    int ix, ix_next;
     auto entry_at = [&](const Row<DT>& c, int o) { return c.at * a.top + min(lane + 64 * o, a.top - 1); };
-    auto fetch_entries = [&](const Row<DT>& c) {
-        ix = a.index[entry_at(c, wave)];
-        t = raw_at(a.t, a.t_dtype, entry_at(c, wave));
+    auto entry_of = [&](const Row<DT>& c, int o) {
+        const int i = a.index[entry_at(c, o)];
+        return lane + 64 * o >= a.top || (unsigned)i >= (unsigned)a.V ? -1 : i;
+    };
+    auto fetch_entries = [&](const Row<DT>& c, long long then) {   // row c's turn is next, row `then`'s after that
+        ix = ix_next;
+        t = t_next;
+        if (lane + 64 * wave >= a.top || (unsigned)ix >= (unsigned)a.V) ix = -1;
+        zr = raw_at(c.z, DT, max(ix, 0));
         edge = raw_at(c.z, DT, max(c.edge_at(a.V), 0));
+        const long long j = then * a.top + min(lane + 64 * wave, a.top - 1);
+        ix_next = a.index[j];
+        t_next = raw_at(a.t, a.t_dtype, j);
     };
     auto fetch = [&](const Row<DT>& c, int q) {
         r[q] = __builtin_amdgcn_raw_buffer_load_b128(dma::make_rsrc(c.zb, c.bytes), tid * 16, q * NT * 16, kOnce);
@@ -314,11 +297,13 @@ distill_kernel(DistillArgs a)
 
     long long row = blockIdx.x, before = -1;
     Row<DT> c(a, row, GRAD, true);
-    fetch_entries(c);
+    ix_next = a.index[entry_at(c, wave)];
+    t_next = raw_at(a.t, a.t_dtype, entry_at(c, wave));
 #pragma unroll
     for (int o = 0; o < L; ++o) fetch_hold(c, o);
 #pragma unroll
     for (int q = 0; q < P; ++q) fetch(c, q);
+    fetch_entries(c, min(row + (GRAD ? gridDim.x : 0), a.rows - 1));
     for (int par = 0;; par ^= 1) {
         const bool last = !GRAD || row + gridDim.x >= a.rows;
         const Row<DT> n(a, last ? row : row + gridDim.x, GRAD, !last);
@@ -327,35 +312,24 @@ distill_kernel(DistillArgs a)
 
         const bool look = !GRAD || c.w != 0.0f;   // a row that is not trained on: its logits are not looked at
         float z_own = 0.0f;                       // of the wave's first entries
-        bool twice = chunks > 1;                  // an index may come more than once
+        bool twice = false;                       // the lane's index comes more than once
         if (look) {
-            // The entries' own logits arrive behind the row's.
-            if (lane + 64 * wave >= a.top || (unsigned)ix >= (unsigned)a.V) ix = -1;
-            const unsigned zr = raw_at(c.z, DT, max(ix, 0));
             float best = -INFINITY, psum = 0.0f;
             if (wave < chunks) {
                 auto take = [&](int o, int i, unsigned raw) {
                     const int j = lane + 64 * o;
                     const float v = i >= 0 ? value_of(raw, a.t_dtype) : -INFINITY;
                     best = fmaxf(best, v);
-                    if (j < a.top) {
-                        idx[par][j] = i;
-                        val[par][j] = v;
-                    }
+                    idx[par][j] = i;
+                    val[par][j] = v;
                 };
                 take(wave, ix, t);
-                for (int o = wave + NW; o < chunks; o += NW) {
-                    const int i = a.index[entry_at(c, o)];
-                    take(o, lane + 64 * o >= a.top || (unsigned)i >= (unsigned)a.V ? -1 : i, raw_at(a.t, a.t_dtype, entry_at(c, o)));
-                }
+                for (int o = wave + NW; o < chunks; o += NW) take(o, entry_of(c, o), raw_at(a.t, a.t_dtype, entry_at(c, o)));
                 best = wave_max(best);
                 for (int j = lane + 64 * wave; j < a.top; j += NT)
                     if (idx[par][j] >= 0) psum += expf((val[par][j] - (best > -INFINITY ? best : 0.0f)) / a.T);
                 psum = wave_sum(psum);
-                if (GRAD && chunks == 1) {   // the wave's own entries are all there are
-                    for (int k = 0; k < a.top; ++k) twice |= ix >= 0 && idx[par][k] == ix && k != lane;
-                    twice = __ballot(twice) != 0;
-                }
+                if (GRAD && chunks == 1) twice = ix >= 0 && repeats(idx[par], a.top, ix) > 1;   // while the row arrives
             }
 
             // A running maximum and sum of 2^((z - mx) scale), 16 values at a time.
@@ -447,7 +421,8 @@ distill_kernel(DistillArgs a)
                     if constexpr (GRAD) {
                         float pt = pj;
                         bool first = i >= 0;
-                        if (twice && first)
+                        if (chunks > 1) twice = first && repeats(idx[par], a.top, i) > 1;
+                        if (twice)
                             for (int k = 0; k < a.top; ++k)
                                 if (idx[par][k] == i && k != j) {
                                     first &= k > j;
@@ -460,7 +435,7 @@ distill_kernel(DistillArgs a)
                 };
                 entry(wave, z_own);
                 for (int o = wave + NW; o < chunks; o += NW)
-                    entry(o, value_of(raw_at(c.z, DT, max(idx[par][min(lane + 64 * o, a.top - 1)], 0)), DT));
+                    entry(o, value_of(raw_at(c.z, DT, max(idx[par][lane + 64 * o], 0)), DT));
                 sum = wave_sum(sum);
                 if (lane == 0) lsum[par][wave] = c.w * a.T * a.T * sum;
             }
@@ -496,7 +471,7 @@ distill_kernel(DistillArgs a)
 #pragma unroll
                 for (int b = 0; b < 4; ++b) store_once(grad_of(x[b]), rs, (tid + b * NT) * 16);
             }
-        fetch_entries(n);
+        fetch_entries(n, min(row + 2 * (long long)gridDim.x, a.rows - 1));
         if (before >= 0) finish_row(before, par ^ 1);   // behind the loads: its stores need not be waited for
         before = on ? row : -1;
 #pragma unroll
@@ -523,49 +498,78 @@ distill_kernel(DistillArgs a)
 }
 
 // The gradient from a given lse: no sum over the row, so a row is cut into
-// strips of 64 KB, a workgroup each.
-constexpr int kGradThreads = 256, kGradPieces = 16;
-
-template <int DT>
-__global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillArgs a, int strips)
+// strips of NT x P pieces, a workgroup each. Up to 128 entries: a wave a strip
+// with no barrier, as many as fit a CU; a wave's chain of loads (entries,
+// their logits) is a few microseconds long.
+template <int DT, int NT, int P, int TOP>
+__global__ void __launch_bounds__(NT) distill_grad_kernel(DistillArgs a, int strips)
 {
     typedef Piece<DT> Pc;
     typedef typename Pc::T T;
-    constexpr int E = Pc::E, NT = kGradThreads, P = kGradPieces;
-    __shared__ float p[kMaxTop];
-    __shared__ int idx[kMaxTop];
+    constexpr int E = Pc::E, MORE = TOP / NT;
+    static_assert(TOP % NT == 0 && MORE * NT == TOP, "entries a thread");
+    __shared__ float val[TOP];
+    __shared__ __attribute__((aligned(16))) int idx[TOP];
     __shared__ float red[NT / 64];
     const int tid = threadIdx.x;
     const long long row = blockIdx.x / strips;
     const int strip = blockIdx.x % strips;
     const T* z = static_cast<const T*>(a.z) + row * a.ldz;
     T* g = static_cast<T*>(a.grad) + row * a.ldg;
-    const float w = a.weight ? a.weight[row] : 1.0f;
-    const float lse = a.lse[row];
     const Span sp = span_of<DT>(z, a.V);
-    const u4* zb = reinterpret_cast<const u4*>(z + sp.head);
     const int first = strip * NT * P, here = sp.pieces - first;
-    const __amdgpu_buffer_rsrc_t rz = dma::make_rsrc(zb + first, 16ll * here);
+    // Entries first: what hangs on them is the longer chain.
+    int ix[MORE];
+    unsigned tr[MORE], zr[MORE];
+#pragma unroll
+    for (int o = 0; o < MORE; ++o) {
+        const long long j = row * a.top + min(tid + o * NT, a.top - 1);
+        ix[o] = a.index[j];
+        tr[o] = raw_at(a.t, a.t_dtype, j);
+    }
+    const __amdgpu_buffer_rsrc_t rz = dma::make_rsrc(reinterpret_cast<const u4*>(z + sp.head) + first, 16ll * here);
     // Aligned to a value: the hardware's unaligned stores.
     const __amdgpu_buffer_rsrc_t rg = dma::make_rsrc(g + sp.head + (long long)first * E, 16ll * here);
     u4 r[P];
 #pragma unroll
     for (int q = 0; q < P; ++q) r[q] = __builtin_amdgcn_raw_buffer_load_b128(rz, tid * 16, q * NT * 16, 0);
     // The first strip takes the values before the pieces, the last those behind.
-    float edge = 0.0f;
     int edge_at = -1;
     if (strip == 0 && tid < sp.head) edge_at = tid;
     if (strip == strips - 1 && tid >= 32 && tid - 32 < a.V - sp.tail0) edge_at = sp.tail0 + tid - 32;
-    if (edge_at >= 0) edge = (float)z[edge_at];
-    const int begin = strip == 0 ? 0 : sp.head + first * E;
-    const int end = strip == strips - 1 ? a.V : sp.head + (first + NT * P) * E;
+    const unsigned edge_r = raw_at(z, DT, max(edge_at, 0));
+    // Entries go to the strip that writes their place: those behind the
+    // pieces are the last strip's, also where a strip before it ends there.
+    const int begin = strip == 0 ? 0 : min(sp.head + first * E, sp.tail0);
+    const int end = strip == strips - 1 ? a.V : min(sp.head + (first + NT * P) * E, sp.tail0);
+    const float w = a.weight ? constant(a.weight, row) : 1.0f, lse = a.lse[row];
+#pragma unroll
+    for (int o = 0; o < MORE; ++o) {
+        if (tid + o * NT >= a.top || (unsigned)ix[o] >= (unsigned)a.V) ix[o] = -1;
+        zr[o] = raw_at(z, DT, max(ix[o], 0));
+    }
 
-    float best;
-    const float psum = teacher_row<NT>(a, row, p, idx, red, best);
-    const bool on = w != 0.0f && !(psum == 0.0f) && !(lse == -INFINITY);
+    float best = -INFINITY, psum = 0.0f;
+#pragma unroll
+    for (int o = 0; o < MORE; ++o)
+        if (ix[o] >= 0) best = fmaxf(best, value_of(tr[o], a.t_dtype));
+    best = block_reduce<NT>(best, red, [](float x, float y) { return fmaxf(x, y); });
     const float tp = best > -INFINITY ? best : 0.0f;
-    for (int j = tid; j < a.top; j += NT) p[j] = idx[j] >= 0 ? expf((p[j] - tp) / a.T) / psum : 0.0f;
+    float pj[MORE];
+#pragma unroll
+    for (int o = 0; o < MORE; ++o) {
+        pj[o] = ix[o] >= 0 ? expf((value_of(tr[o], a.t_dtype) - tp) / a.T) : 0.0f;
+        psum += pj[o];
+    }
+    psum = block_reduce<NT>(psum, red, [](float x, float y) { return x + y; });
+#pragma unroll
+    for (int o = 0; o < MORE; ++o) {
+        pj[o] = ix[o] >= 0 ? pj[o] / psum : 0.0f;
+        idx[tid + o * NT] = ix[o];
+        val[tid + o * NT] = pj[o];
+    }
     __syncthreads();
+    const bool on = w != 0.0f && !(psum == 0.0f) && !(lse == -INFINITY);
     const float wt = w * a.T;
     // lse is at least every v / T; where its rounding says otherwise (it is
     // coarse for logits next to a type's lowest value) q is 1, not more. A NaN
@@ -574,23 +578,25 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillArgs 
         const float d = fmaf(v, a.inv_hi, -lse) + v * a.inv_lo;
         return pow2((d > 0.0f ? 0.0f : d) * 1.44269504088896341f);
     };
-    constexpr int MORE = kMaxTop / NT;
+    // An index is written by its first entry, for all of them.
     float gv[MORE];
-    int gat[MORE];
 #pragma unroll
     for (int o = 0; o < MORE; ++o) {
-        const int j = tid + o * NT;
-        gat[o] = -1;
-        if (on && j < a.top && idx[j] >= begin && idx[j] < end) {
-            const float pt = total_p(a, p, idx, j);
-            if (!(pt < 0.0f)) {
-                gat[o] = idx[j];
-                const float v = (float)z[idx[j]];
-                gv[o] = wt * ((v == -INFINITY ? 0.0f : q_of(v)) - pt);
-            }
-        }
+        gv[o] = 0.0f;
+        if (!on || ix[o] < begin || ix[o] >= end) ix[o] = -1;
+        if (ix[o] < 0) continue;
+        const int i = ix[o], j = tid + o * NT;
+        float pt = pj[o];
+        if (repeats(idx, a.top, i) > 1)
+            for (int k = 0; k < a.top; ++k)
+                if (idx[k] == i && k != j) {
+                    pt += val[k];
+                    if (k < j) ix[o] = -1;
+                }
+        const float v = value_of(zr[o], DT);
+        gv[o] = wt * ((v == -INFINITY ? 0.0f : q_of(v)) - pt);
     }
-    __syncthreads();
+    __syncthreads();   // a wave's logits are all read before any of the row is written
 #pragma unroll
     for (int q = 0; q < P; ++q) {
         float v[E];
@@ -599,35 +605,46 @@ __global__ void __launch_bounds__(kGradThreads) distill_grad_kernel(DistillArgs 
         for (int k = 0; k < E; ++k) v[k] = !on || v[k] == -INFINITY ? 0.0f : wt * q_of(v[k]);
         store_once(Pc::put(v), rg, (tid + q * NT) * 16);
     }
-    if (edge_at >= 0) g[edge_at] = (T)(!on || edge == -INFINITY ? 0.0f : wt * q_of(edge));
+    if (edge_at >= 0) {
+        const float edge = value_of(edge_r, DT);
+        g[edge_at] = (T)(!on || edge == -INFINITY ? 0.0f : wt * q_of(edge));
+    }
     __syncthreads();
 #pragma unroll
     for (int o = 0; o < MORE; ++o)
-        if (gat[o] >= 0) g[gat[o]] = (T)gv[o];
+        if (ix[o] >= 0) g[ix[o]] = (T)gv[o];
 }
 
 // per: workgroups of a CU that take rows in turn.
-template <int DT, int NT, int P, int L, bool REST = false>
+template <int DT, int NT, int P, int L, bool REST = false, int TOP = kMaxTop>
 hipError_t run(const DistillArgs& a, int per, hipStream_t s)
 {
     const dim3 block(NT);
     if (a.grad)
-        hipLaunchKernelGGL((distill_kernel<DT, NT, P, L, REST, true>), dim3((unsigned)(a.rows < 256 * per ? a.rows : 256 * per)),
-                           block, 0, s, a);
+        hipLaunchKernelGGL((distill_kernel<DT, NT, P, L, REST, true, TOP>),
+                           dim3((unsigned)(a.rows < 256 * per ? a.rows : 256 * per)), block, 0, s, a);
     else   // the loss alone has no use for what it has read
-        hipLaunchKernelGGL((distill_kernel<DT, NT, P, 0, REST, false>), dim3((unsigned)a.rows), block, 0, s, a);
+        hipLaunchKernelGGL((distill_kernel<DT, NT, P, 0, REST, false, TOP>), dim3((unsigned)a.rows), block, 0, s, a);
     return hipGetLastError();
 }
 
 // Threads and registers by the row's length, so that each holds a row and two
 // to four workgroups share a CU (4096 x 32768 bf16: three of 512 threads 110
-// us, two 114, three of 256 with twice the registers 122, one of 1024 138);
+// us, two 114, three of 256 with twice the registers 122, one of 1024 138, all
+// before the entries' logits came ahead, too);
 // few rows: as many threads as fit, for latency.
 template <int DT>
 hipError_t pick(const DistillArgs& a, hipStream_t s)
 {
     const long long pieces = ((long long)a.V + Piece<DT>::E - 1) / Piece<DT>::E;
     const bool few = a.rows <= 256;
+    // Many short rows: a wave each and no barrier, so that a CU has 16 to 20
+    // on their way (3127 x 2917 f16: four of 256 threads 27 us, this 15).
+    if (a.rows > 1024 && a.top <= kFewTop) {
+        if (pieces <= 64 * 4) return run<DT, 64, 4, 0, false, kFewTop>(a, 20, s);
+        if (pieces <= 64 * 8) return run<DT, 64, 8, 0, false, kFewTop>(a, 20, s);
+        if (pieces <= 64 * 16) return run<DT, 64, 16, 0, false, kFewTop>(a, 16, s);
+    }
     if (pieces <= 256 * 4) return run<DT, 256, 4, 0>(a, 4, s);
     if (few && pieces <= 1024 * 4) return run<DT, 1024, 4, 0>(a, 1, s);
     if (few && pieces <= 1024 * 8) return run<DT, 1024, 8, 0>(a, 1, s);
@@ -646,19 +663,34 @@ hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t s)
     return dtype == DT_BF16 ? pick<DT_BF16>(a, s) : pick<DT_F16>(a, s);
 }
 
+namespace {
+
+template <int DT, int NT, int P, int TOP>
+hipError_t run_grad(const DistillArgs& a, hipStream_t s)
+{
+    const long long per = (long long)NT * P * Piece<DT>::E;
+    const int strips = (int)((a.V + per - 1) / per);
+    hipLaunchKernelGGL((distill_grad_kernel<DT, NT, P, TOP>), dim3((unsigned)(a.rows * strips)), dim3(NT), 0, s, a, strips);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t pick_grad(const DistillArgs& a, hipStream_t s)
+{
+    if (a.top > kFewTop) return run_grad<DT, 256, 16, kMaxTop>(a, s);
+    const long long pieces = ((long long)a.V + Piece<DT>::E - 1) / Piece<DT>::E;
+    if (pieces <= 64 * 4) return run_grad<DT, 64, 4, kFewTop>(a, s);
+    // Strips of 8 pieces a lane while their number fits a grid (checked for strips of twice that).
+    if (pieces <= 64 * 8 || a.rows * (pieces / 512 + 1) < (1ll << 31) - 1) return run_grad<DT, 64, 8, kFewTop>(a, s);
+    return run_grad<DT, 256, 16, kMaxTop>(a, s);
+}
+
+}  // namespace
+
 hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t s)
 {
-    const long long e = dtype == DT_F32 ? 4 : 8;
-    const long long per = (long long)kGradThreads * kGradPieces * e;
-    const int strips = (int)((a.V + per - 1) / per);
-    const dim3 grid((unsigned)(a.rows * strips)), block(kGradThreads);
-    if (dtype == DT_F32)
-        hipLaunchKernelGGL((distill_grad_kernel<DT_F32>), grid, block, 0, s, a, strips);
-    else if (dtype == DT_BF16)
-        hipLaunchKernelGGL((distill_grad_kernel<DT_BF16>), grid, block, 0, s, a, strips);
-    else
-        hipLaunchKernelGGL((distill_grad_kernel<DT_F16>), grid, block, 0, s, a, strips);
-    return hipGetLastError();
+    if (dtype == DT_F32) return pick_grad<DT_F32>(a, s);
+    return dtype == DT_BF16 ? pick_grad<DT_BF16>(a, s) : pick_grad<DT_F16>(a, s);
 }
 
 }  // namespace sam

@@ -149,18 +149,41 @@ def test_outermost_temperatures(T):
 def test_workgroups_take_many_rows(dtype):
     """More rows than workgroups, so that each takes several: rows that are not
     trained on, empty and masked ones between the others, odd lengths."""
-    for R, V in ((3500, 1001), (2300, 9001), (1100, 20011)):
-        z, t, idx, w = make(R, V, 70, dtype, 14)
+    for R, V, k in ((11000, 701, 70), (6000, 5003, 128), (3500, 1001, 129), (2300, 9001, 70), (1100, 20011, 70)):
+        z, t, idx, w = make(R, V, k, dtype, 14)
         w[::3] = 0.0
         z[w == 0] = math.nan
         idx[1::5] = -1
         z[2::7] = torch.where(w[2::7, None] == 0, z[2::7], torch.full_like(z[2::7], -math.inf))
-        idx[4::9, 30:] = idx[4::9, :40]
+        idx[4::9, 30:60] = idx[4::9, :30]
         zz = torch.where(w[:, None] == 0, torch.zeros_like(z), z)     # the reference has no such rows
         want = ref.reference(zz, t, idx, w, 1.5)
         loss, grad = sam.distill(z, t, idx, w, 1.5)
         ref.close(loss, *want[0])
         ref.close(grad, *want[2])
+        loss, lse = sam.distill_loss(z, t, idx, w, 1.5)
+        ref.close(loss, *want[0])
+        ref.close(sam.distill_grad(z, lse, t, idx, w, 1.5), *want[2])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_entries_at_the_ends_of_strips(dtype):
+    """The gradient from an lse cuts rows into strips of 512 pieces (of 256 in
+    short rows): entries on the values around every cut and at a row's end,
+    where values that fill no piece belong to the last strip."""
+    e = 4 if dtype == "f32" else 8
+    for pieces in (256, 512, 1024):
+        for over in (-1, 0, 1, 3):
+            V = pieces * e + over
+            z, t, _, w = make(40, V + 8, 48, dtype, 15)
+            at = torch.cat([torch.arange(V - 16, V), torch.arange(V // 2 - 16, V // 2 + 16)])
+            idx = at.to(torch.int32).cuda().expand(40, 48).contiguous()
+            for off in (0, 1, 5):     # rows start anywhere
+                zv = z[:, off:off + V]
+                loss, lse = sam.distill_loss(zv, t, idx, w)
+                want = ref.reference(zv, t, idx, w, 1.0)
+                for _ in range(3):
+                    ref.close(sam.distill_grad(zv, lse, t, idx, w), *want[2], f"V={V} offset {off}")
 
 
 def test_gradient_is_the_loss_difference():
