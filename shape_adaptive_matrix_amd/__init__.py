@@ -511,7 +511,10 @@ def _address(t):
 
 def _stream_address(stream):
     import torch
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object around it
+    return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
 
 
 def _adapter_operands(X, W, A, B, ids, scale, trans_w):

@@ -145,11 +145,11 @@ Layout layout(const Call& c)
     // form a block's second adapter has a workgroup too, and the CUs room for
     // 64 of them: few blocks have one in long runs, but two passes of one
     // workgroup, or one that starts when another ends, last as long as two of
-    // all (4096 x 11008, rank 64, 4 adapters in runs: 39 us, so SLOT_US).
+    // all (4096 x 11008, rank 64, 4 adapters in runs: 39 us, so 36).
     const int sides = c.back && c.want_ad ? 2 : 1;
     const long long blocks = (c.M + 15) / 16, longest = c.back && c.N > c.K ? c.N : c.K;
     L.wide = blocks > 8;
-    L.merged = !c.back && L.prod.split > 0 && L.prod.tile >= 3;
+    L.merged = c.M > 0 && L.prod.split > 0 && L.prod.tile >= 3 && (!c.back || c.want_dx);
     long long s, most;
     if (L.wide) {
         s = (2 * kCUs - 64) / ((c.M + 63) / 64 * sides);
@@ -191,10 +191,11 @@ Layout layout(const Call& c)
         // (4096 rows, 8192 columns: 256 rows 22 us, 128 the same and twice the
         // partials; 1025 rows, 2817 columns: 256 rows 18 us, 64 9 us).
         const long long strips = (c.K + 255) / 256 + (c.N + 255) / 256;
-        long long chunk = 64;
+        // Up to 128 rows are one chunk: nothing is left to add.
+        long long chunk = c.M <= 128 ? 128 : 64;
         while (chunk < (1 << 20) && (c.M / (2 * chunk)) * strips >= 2 * kCUs) chunk *= 2;
         L.chunk = (int)chunk;
-        L.max_chunks = (int)((c.M + chunk - 1) / chunk + (c.n < c.M ? c.n : c.M));
+        L.max_chunks = (int)((c.M + chunk - 1) / chunk + c.n);
         take(L.outer, 4ull * L.max_chunks * c.r * (c.K + c.N));
         take(L.chunk_first, 4ull * (c.n + 1));
         take(L.chunks, 16ull * (L.max_chunks + 1));
@@ -295,8 +296,13 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
                 a.chunks = static_cast<int4*>(at(L.chunks));
             }
         }
-        if (e == hipSuccess && !L.merged && (c.M > 0 || c.want_ad)) e = launch_adapter_shrink(c.dtype, a, s);
+        if (!L.merged && (c.M > 0 || c.want_ad)) {
+            if (e == hipSuccess) e = launch_adapter_shrink(c.dtype, a, s);
+            if (e == hipSuccess && a.round) e = launch_adapter_round(c.dtype, a, s);
+        }
     }
+    FinishArgs f{};
+    bool finish = false;   // the split product's partials are still to be added
     if (e == hipSuccess && c.M > 0 && (!c.back || c.want_dx)) {
         const long long cols = c.back ? c.K : c.N, k = c.back ? c.N : c.K;
         const void* X = c.back ? p.dY : p.X;
@@ -329,26 +335,24 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
         } else {
             const ShrinkArgs none{};
             e = launch_adapter_ring(L.prod.tile, c.dtype, bt, g, (int)cols, nullptr, L.merged && term ? &a : &none, s);
-            if (e == hipSuccess) {
-                FinishArgs f{};
-                f.part = g.out;
-                f.ldp = g.N;
-                f.split = L.prod.split;
-                f.t32 = static_cast<const float*>(c.back ? at(L.t32b) : at(L.t32));
-                f.tsplit = a.round ? 1 : L.ksplit;
-                f.B = B;
-                f.ldb = lb;
-                f.ids = p.ids;
-                f.M = (int)c.M;
-                f.N = (int)cols;
-                f.n = (int)c.n;
-                f.r = (int)c.r;
-                f.rp = L.rp;
-                f.Y = p.Y;
-                f.ldy = ldo;
-                f.out16 = out16;
-                e = launch_adapter_finish(c.dtype, f, s);
-            }
+            if (e == hipSuccess && L.merged && term && a.round) e = launch_adapter_round(c.dtype, a, s);
+            finish = true;
+            f.part = g.out;
+            f.ldp = g.N;
+            f.split = L.prod.split;
+            f.t32 = static_cast<const float*>(c.back ? at(L.t32b) : at(L.t32));
+            f.tsplit = a.round ? 1 : L.ksplit;
+            f.B = B;
+            f.ldb = lb;
+            f.ids = p.ids;
+            f.M = (int)c.M;
+            f.N = (int)cols;
+            f.n = (int)c.n;
+            f.r = (int)c.r;
+            f.rp = L.rp;
+            f.Y = p.Y;
+            f.ldy = ldo;
+            f.out16 = out16;
         }
     }
     if (e == hipSuccess && c.back && c.want_ad && term) {
@@ -358,6 +362,7 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
         o.r = (int)c.r;
         o.rp = L.rp;
         o.order = static_cast<const int*>(at(L.order));
+        o.chunk = L.chunk;
         o.max_chunks = L.max_chunks;
         o.chunk_first = a.chunk_first;
         o.chunks = a.chunks;
@@ -366,7 +371,9 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
                      p.dA, part};
         o.side[1] = {static_cast<const float*>(at(L.t32)), static_cast<const float*>(at(L.factor2)), p.dY, L.ldy, (int)c.N,
                      p.dB, part + (long long)L.max_chunks * c.r * c.K};
-        e = launch_adapter_outer(c.dtype, o, s);
+        e = launch_adapter_outer(c.dtype, o, finish ? &f : nullptr, s);
+    } else if (e == hipSuccess && finish) {
+        e = launch_adapter_finish(c.dtype, f, s);
     }
     if (e != hipSuccess) return api_fail(SAM_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
     return api_ok();

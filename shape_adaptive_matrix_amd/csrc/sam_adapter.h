@@ -48,7 +48,7 @@ struct ShrinkArgs {
     int* seg;            // [n + 1] where each adapter's rows start in it
     // ... and chunks of its rows, listed by the second kernel:
     int chunk;           // rows per chunk
-    int max_chunks;      // ceil(M / chunk) + min(n, M)
+    int max_chunks;      // ceil(M / chunk) + n
     int* chunk_first;    // [n + 1] each adapter's first chunk
     int4* chunks;        // [max_chunks] adapter (-1: no such chunk), place in `order`, rows, first row of a run or -1
 };
@@ -105,7 +105,7 @@ struct OuterArgs {
     OuterSide side[2];
     int M, n, r, rp;
     const int* order;
-    int max_chunks;      // as in ShrinkArgs
+    int chunk, max_chunks;   // as in ShrinkArgs
     const int* chunk_first;
     const int4* chunks;
 };
@@ -114,14 +114,17 @@ constexpr int kMaxPads = 5;
 // Up to kMaxPads copies of 16-bit operands in one launch.
 hipError_t launch_adapter_pad(const PadCopy* c, int n, hipStream_t s);
 hipError_t launch_adapter_shrink(int dtype, const ShrinkArgs& a, hipStream_t s);
+// The second kernel: sums over K ranges, their rounding, the list of chunks.
+hipError_t launch_adapter_round(int dtype, const ShrinkArgs& a, hipStream_t s);
 hipError_t launch_adapter_finish(int dtype, const FinishArgs& a, hipStream_t s);
-hipError_t launch_adapter_outer(int dtype, const OuterArgs& a, hipStream_t s);
+// `f`: the sum of the split product's partials in the same launch, or null.
+hipError_t launch_adapter_outer(int dtype, const OuterArgs& a, const FinishArgs* f, hipStream_t s);
 // Tiles of the ring kernels used here. `tile` 0: 256 x 256, 1: 192 x 256, 2:
 // 128 x 128 (with the adapters' term, or split-K partials with `x` null), 3:
 // 64 x 128, 4: 32 x 128, 5: 16 x 128 (partials only). bt: W given as n rows of
 // K; g.N is n, the product's columns, rounded up to 8. `shrink`, with tiles 3
-// to 5: workgroups of the same launch that make T's partial sums (not null; no
-// rows: none).
+// to 5: workgroups of the same launch that make T's partial sums and group the
+// rows (not null; no rows: none).
 struct AdapterTile {
     int bm, bn;
 };

@@ -96,4 +96,78 @@ __device__ __forceinline__ void shrink_part(const ShrinkArgs& a, int wg)
     }
 }
 
+// Rows sorted by adapter, one workgroup per adapter: it counts the valid ids
+// below its own (where its rows start) and writes its rows in row order. Each
+// wave has a range of the rows, eight loads under way at once.
+template <int NW>
+__device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad, int (&sums)[2 * NW])
+{
+    constexpr int U = 8;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int per = ((a.M + NW * 64 - 1) / (NW * 64)) * 64;
+    const int m0 = min(wave * per, a.M), m1 = min(m0 + per, a.M);
+    auto load = [&](int m, int (&id)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = a.ids[min(m + 64 * u + lane, a.M - 1)];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (m + 64 * u + lane >= m1) id[u] = -1;
+    };
+    int below = 0, mine = 0;
+    for (int m = m0; m < m1; m += 64 * U) {
+        int id[U];
+        load(m, id);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            below += (unsigned)id[u] < (unsigned)ad;
+            mine += id[u] == ad;
+        }
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+        below += __shfl_xor(below, d);
+        mine += __shfl_xor(mine, d);
+    }
+    if (lane == 0) {
+        sums[wave] = below;
+        sums[NW + wave] = mine;
+    }
+    __syncthreads();
+    int at = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        at += sums[w] + (w < wave ? sums[NW + w] : 0);
+        all += sums[w] + sums[NW + w];
+    }
+    if (tid == 0) {
+        a.seg[ad] = at;
+        if (ad == a.n - 1) a.seg[a.n] = all;
+    }
+    for (int m = m0; m < m1; m += 64 * U) {
+        int id[U];
+        load(m, id);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned long long b = __ballot(id[u] == ad);
+            if (id[u] == ad) a.order[at + __popcll(b & ((1ull << lane) - 1))] = m + 64 * u + lane;
+            at += __popcll(b);
+        }
+    }
+}
+
+// The workgroups of a grid that make T of up to 128 rows, and the grouping.
+__host__ __device__ inline int shrink_all_wgs(const ShrinkArgs& a) { return shrink_wgs(a) + (a.order ? a.n : 0); }
+
+template <int DT, int NW>
+__device__ __forceinline__ void shrink_or_group(const ShrinkArgs& a, int wg)
+{
+    __shared__ int sums[2 * NW];
+    const int wgs = shrink_wgs(a);
+    if (wg >= wgs)
+        group_rows<NW>(a, wg - wgs, sums);
+    else
+        shrink_part<DT, NW>(a, wg);
+}
+
 }  // namespace sam

@@ -52,66 +52,6 @@ __device__ __forceinline__ void split3_bits(float v, unsigned short (&o)[3])
 
 constexpr int kShrinkWaves = 4, kWideRows = 64;
 
-// Rows sorted by adapter, one workgroup per adapter: it counts the valid ids
-// below its own (where its rows start) and writes its rows in row order. Each
-// wave has a range of the rows, eight loads under way at once.
-template <int NW>
-__device__ __forceinline__ void group_rows(const ShrinkArgs& a, int ad, int (&sums)[2 * NW])
-{
-    constexpr int U = 8;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int per = ((a.M + NW * 64 - 1) / (NW * 64)) * 64;
-    const int m0 = min(wave * per, a.M), m1 = min(m0 + per, a.M);
-    auto load = [&](int m, int (&id)[U]) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) id[u] = a.ids[min(m + 64 * u + lane, a.M - 1)];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (m + 64 * u + lane >= m1) id[u] = -1;
-    };
-    int below = 0, mine = 0;
-    for (int m = m0; m < m1; m += 64 * U) {
-        int id[U];
-        load(m, id);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            below += (unsigned)id[u] < (unsigned)ad;
-            mine += id[u] == ad;
-        }
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        below += __shfl_xor(below, d);
-        mine += __shfl_xor(mine, d);
-    }
-    if (lane == 0) {
-        sums[wave] = below;
-        sums[NW + wave] = mine;
-    }
-    __syncthreads();
-    int at = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-        at += sums[w] + (w < wave ? sums[NW + w] : 0);
-        all += sums[w] + sums[NW + w];
-    }
-    if (tid == 0) {
-        a.seg[ad] = at;
-        if (ad == a.n - 1) a.seg[a.n] = all;
-    }
-    for (int m = m0; m < m1; m += 64 * U) {
-        int id[U];
-        load(m, id);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned long long b = __ballot(id[u] == ad);
-            if (id[u] == ad) a.order[at + __popcll(b & ((1ull << lane) - 1))] = m + 64 * u + lane;
-            at += __popcll(b);
-        }
-    }
-}
-
 // Rounds a row of T, held by 32 threads (column c0 + 32 q): divides by the
 // power of two below the row's largest value. A row of zeros gets the
 // smallest one (it then never sets the scale of rows that are added up with
@@ -153,12 +93,7 @@ __device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide&
 template <int DT>
 __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_kernel(ShrinkArgs a)
 {
-    __shared__ int sums[2 * kShrinkWaves];
-    const int wgs = shrink_wgs(a);
-    if ((int)blockIdx.x >= wgs)
-        group_rows<kShrinkWaves>(a, blockIdx.x - wgs, sums);
-    else
-        shrink_part<DT, kShrinkWaves>(a, blockIdx.x);
+    shrink_or_group<DT, kShrinkWaves>(a, blockIdx.x);
 }
 
 // T of 64 rows over one range of K, for calls with many rows: for each
@@ -311,7 +246,7 @@ __device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
     for (int a0 = 0; a0 < a.n; a0 += 256) {
         const int ad = a0 + tid;
         const int begin = ad < a.n ? a.seg[ad] : 0, rows = ad < a.n ? a.seg[ad + 1] - begin : 0;
-        const int count = (rows + a.chunk - 1) / a.chunk;
+        const int count = ad < a.n ? max((rows + a.chunk - 1) / a.chunk, 1) : 0;   // without rows: one that gives zeros
         int sum = count;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -330,9 +265,9 @@ __device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
         if (ad < a.n) a.chunk_first[ad] = first;
         for (int c = 0; c < count; ++c) {
             const int at = begin + c * a.chunk, n = min(a.chunk, rows - c * a.chunk);
-            const int row0 = a.order[at];
+            const int row0 = n ? a.order[at] : 0;
             // Rows of one run need no look-up.
-            a.chunks[first + c] = make_int4(ad, at, n, a.order[at + n - 1] - row0 == n - 1 ? row0 : -1);
+            a.chunks[first + c] = make_int4(ad, at, n, n == 0 || a.order[at + n - 1] - row0 == n - 1 ? row0 : -1);
         }
     }
     if (tid == 0) a.chunk_first[a.n] = base;
@@ -395,16 +330,16 @@ __device__ __forceinline__ void floats_of(const uint2& w, float (&o)[4])
 // id, so all first loads go out before the first is used. Measured at 64 rows
 // x 11008, rank 16, 2 partials: 6.8 us (one load at a time, 5 partials: 39).
 template <int DT, int WS>
-__global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
+__device__ __forceinline__ void finish_rows(const FinishArgs& a, int wg)
 {
     constexpr int UP = WS == 4 ? 4 : 8, UB = 8;   // partials, rows of B under way at once; what is more than there are comes from L1
     __shared__ float4 red[3][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int strips = (a.N + 255) / 256;
-    const int m = WS == 4 ? blockIdx.x / strips : blockIdx.x / strips * 4 + wave;
+    const int m = WS == 4 ? wg / strips : wg / strips * 4 + wave;
     if (WS == 1 && m >= a.M) return;
-    const int c = (blockIdx.x % strips) * 256 + 4 * lane;
+    const int c = (wg % strips) * 256 + 4 * lane;
     const int left = a.N - c, cc = left > 0 ? c : 0;   // lanes past N read the first columns
     const int p = WS == 4 ? wave : 0;
     const int s0 = a.split * p / WS, s1 = a.split * (p + 1) / WS;
@@ -522,7 +457,7 @@ constexpr int kOuterCols = 256;
 // Chunks of adapters with one chunk go to `out`, others to `part`, which
 // outer_sum adds in order.
 template <int DT, int NR>
-__global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
+__device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
 {
     using namespace dma;
     constexpr int RP = 16 * NR;
@@ -537,9 +472,9 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int strips0 = (a.side[0].cols + kOuterCols - 1) / kOuterCols;
     const int wgs0 = strips0 * a.max_chunks;
-    const bool second = (int)blockIdx.x >= wgs0;
+    const bool second = block >= wgs0;
     const OuterSide& sd = a.side[second];
-    const int wg = second ? blockIdx.x - wgs0 : blockIdx.x;
+    const int wg = second ? block - wgs0 : block;
     const int ch = wg % a.max_chunks, c0 = (wg / a.max_chunks) * kOuterCols;
     const int4 w = a.chunks[ch];
     const int ad = w.x, rows = w.z, row0 = w.w;
@@ -557,7 +492,7 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
         if (lane == 0) fmax_s[wave] = big;
         __syncthreads();
         big = fmaxf(fmaxf(fmax_s[0], fmax_s[1]), fmaxf(fmax_s[2], fmax_s[3]));
-        e = ilogbf(big);   // factors are powers of two, at least 2^-126
+        if (rows) e = ilogbf(big);   // factors are powers of two, at least 2^-126
     }
 
     // Loads of step s into registers: X 32 rows x 512 bytes, four 16-byte
@@ -678,8 +613,29 @@ __global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
         }
 }
 
-// Adapters without rows get zeros, those with several chunks the sum of
-// their partials in chunk order. 1024 values a workgroup.
+template <int DT, int WS>
+__global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
+{
+    finish_rows<DT, WS>(a, blockIdx.x);
+}
+
+template <int DT, int NR>
+__global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
+{
+    outer_tile<DT, NR>(a, blockIdx.x);
+}
+
+// Both in one launch, where the backward pass has both: neither needs the other.
+template <int DT, int NR, int WS>
+__global__ void __launch_bounds__(256) adapter_outer_finish_kernel(OuterArgs o, FinishArgs f, int outer_wgs)
+{
+    if ((int)blockIdx.x < outer_wgs)
+        outer_tile<DT, NR>(o, blockIdx.x);
+    else
+        finish_rows<DT, WS>(f, blockIdx.x - outer_wgs);
+}
+
+// Adapters with several chunks get the sum of their partials in chunk order. 1024 values a workgroup.
 __global__ void __launch_bounds__(256) adapter_outer_sum_kernel(OuterArgs a)
 {
     const long long v0 = (long long)a.r * a.side[0].cols, v1 = (long long)a.r * a.side[1].cols;
@@ -754,47 +710,82 @@ __global__ void __launch_bounds__(256) adapter_pad_kernel(PadArgs a)
 template <int DT>
 hipError_t shrink_dt(const ShrinkArgs& a, hipStream_t s)
 {
-    const int more = a.order ? a.n : 0;
     const dim3 block(kShrinkWaves * 64);
-    if (a.wide) {
-        const dim3 grid((unsigned)((a.M + kWideRows - 1) / kWideRows * a.slots * a.ksplit * a.sides + more));
-        switch (a.rp) {
-        case 16: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 1>), grid, block, 0, s, a); break;
-        case 32: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 2>), grid, block, 0, s, a); break;
-        case 64: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 4>), grid, block, 0, s, a); break;
-        case 128: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 8>), grid, block, 0, s, a); break;
-        default: return hipErrorInvalidValue;
-        }
-    } else {
-        hipLaunchKernelGGL((adapter_shrink_kernel<DT>), dim3((unsigned)(shrink_wgs(a) + more)), block, 0, s, a);
+    if (!a.wide) {
+        hipLaunchKernelGGL((adapter_shrink_kernel<DT>), dim3((unsigned)shrink_all_wgs(a)), block, 0, s, a);
+        return hipGetLastError();
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.round) return e;
-    const dim3 rgrid((unsigned)((a.M + 7) / 8 + (a.order ? 1 : 0)), (unsigned)a.sides), rblock(256);
-    switch ((a.rp + 31) / 32) {
-    case 1: hipLaunchKernelGGL((adapter_round_kernel<DT, 1>), rgrid, rblock, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((adapter_round_kernel<DT, 2>), rgrid, rblock, 0, s, a); break;
-    default: hipLaunchKernelGGL((adapter_round_kernel<DT, 4>), rgrid, rblock, 0, s, a); break;
+    const dim3 grid((unsigned)((a.M + kWideRows - 1) / kWideRows * a.slots * a.ksplit * a.sides + (a.order ? a.n : 0)));
+    switch (a.rp) {
+    case 16: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 1>), grid, block, 0, s, a); break;
+    case 32: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 2>), grid, block, 0, s, a); break;
+    case 64: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 4>), grid, block, 0, s, a); break;
+    case 128: hipLaunchKernelGGL((adapter_shrink_wide_kernel<DT, 8>), grid, block, 0, s, a); break;
+    default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
 template <int DT>
-hipError_t outer_dt(const OuterArgs& a, hipStream_t s)
+hipError_t round_dt(const ShrinkArgs& a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.M + 7) / 8 + (a.order ? 1 : 0)), (unsigned)a.sides), block(256);
+    switch ((a.rp + 31) / 32) {
+    case 1: hipLaunchKernelGGL((adapter_round_kernel<DT, 1>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((adapter_round_kernel<DT, 2>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((adapter_round_kernel<DT, 4>), grid, block, 0, s, a); break;
+    }
+    return hipGetLastError();
+}
+
+// Four waves a row while that leaves CUs free (64 rows x 11008: 9.2 us with
+// four, 6.8 with one; one row x 4096: 3.6 and 8.1).
+bool share_rows(const FinishArgs& f) { return (f.N + 255) / 256 * (long long)f.M <= 1024; }
+
+unsigned finish_wgs(const FinishArgs& f)
+{
+    return (unsigned)((f.N + 255) / 256 * (long long)(share_rows(f) ? f.M : (f.M + 3) / 4));
+}
+
+template <int DT>
+hipError_t finish_dt(const FinishArgs& f, hipStream_t s)
+{
+    const dim3 grid(finish_wgs(f)), block(256);
+    if (share_rows(f))
+        hipLaunchKernelGGL((adapter_finish_kernel<DT, 4>), grid, block, 0, s, f);
+    else
+        hipLaunchKernelGGL((adapter_finish_kernel<DT, 1>), grid, block, 0, s, f);
+    return hipGetLastError();
+}
+
+template <int DT, int NR>
+void outer_nr(const OuterArgs& a, const FinishArgs* f, unsigned wgs, hipStream_t s)
+{
+    const dim3 block(256);
+    if (!f)
+        hipLaunchKernelGGL((adapter_outer_kernel<DT, NR>), dim3(wgs), block, 0, s, a);
+    else if (share_rows(*f))
+        hipLaunchKernelGGL((adapter_outer_finish_kernel<DT, NR, 4>), dim3(wgs + finish_wgs(*f)), block, 0, s, a, *f, (int)wgs);
+    else
+        hipLaunchKernelGGL((adapter_outer_finish_kernel<DT, NR, 1>), dim3(wgs + finish_wgs(*f)), block, 0, s, a, *f, (int)wgs);
+}
+
+template <int DT>
+hipError_t outer_dt(const OuterArgs& a, const FinishArgs* f, hipStream_t s)
 {
     const long long strips = (a.side[0].cols + kOuterCols - 1) / kOuterCols + (a.side[1].cols + kOuterCols - 1) / kOuterCols;
-    const dim3 grid((unsigned)(strips * a.max_chunks)), block(256);
-    if (grid.x) switch (a.rp / 16) {
-    case 1: hipLaunchKernelGGL((adapter_outer_kernel<DT, 1>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((adapter_outer_kernel<DT, 2>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((adapter_outer_kernel<DT, 4>), grid, block, 0, s, a); break;
-    case 8: hipLaunchKernelGGL((adapter_outer_kernel<DT, 8>), grid, block, 0, s, a); break;
+    const unsigned wgs = (unsigned)(strips * a.max_chunks);
+    switch (a.rp) {
+    case 16: outer_nr<DT, 1>(a, f, wgs, s); break;
+    case 32: outer_nr<DT, 2>(a, f, wgs, s); break;
+    case 64: outer_nr<DT, 4>(a, f, wgs, s); break;
+    case 128: outer_nr<DT, 8>(a, f, wgs, s); break;
     default: return hipErrorInvalidValue;
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || a.M <= a.chunk) return e;   // no adapter has a second chunk
     const long long b = ((long long)a.r * a.side[0].cols + 1023) / 1024 + ((long long)a.r * a.side[1].cols + 1023) / 1024;
-    hipLaunchKernelGGL(adapter_outer_sum_kernel, dim3((unsigned)(a.n * b)), block, 0, s, a);
+    hipLaunchKernelGGL(adapter_outer_sum_kernel, dim3((unsigned)(a.n * b)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -805,25 +796,14 @@ hipError_t launch_adapter_shrink(int dtype, const ShrinkArgs& a, hipStream_t s)
     return dtype == DT_BF16 ? shrink_dt<DT_BF16>(a, s) : shrink_dt<DT_F16>(a, s);
 }
 
+hipError_t launch_adapter_round(int dtype, const ShrinkArgs& a, hipStream_t s)
+{
+    return dtype == DT_BF16 ? round_dt<DT_BF16>(a, s) : round_dt<DT_F16>(a, s);
+}
+
 hipError_t launch_adapter_finish(int dtype, const FinishArgs& a, hipStream_t s)
 {
-    // Four waves a row while that leaves CUs free (64 rows x 11008: 9.2 us with
-    // four, 6.8 with one; one row x 4096: 3.6 and 8.1).
-    const long long strips = (a.N + 255) / 256;
-    const bool share = strips * a.M <= 1024;
-    const dim3 grid((unsigned)(strips * (share ? a.M : (a.M + 3) / 4))), block(256);
-    if (dtype == DT_BF16) {
-        if (share)
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_BF16, 4>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_BF16, 1>), grid, block, 0, s, a);
-    } else {
-        if (share)
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_F16, 4>), grid, block, 0, s, a);
-        else
-            hipLaunchKernelGGL((adapter_finish_kernel<DT_F16, 1>), grid, block, 0, s, a);
-    }
-    return hipGetLastError();
+    return dtype == DT_BF16 ? finish_dt<DT_BF16>(a, s) : finish_dt<DT_F16>(a, s);
 }
 
 hipError_t launch_adapter_pad(const PadCopy* c, int n, hipStream_t s)
@@ -842,9 +822,9 @@ hipError_t launch_adapter_pad(const PadCopy* c, int n, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_adapter_outer(int dtype, const OuterArgs& a, hipStream_t s)
+hipError_t launch_adapter_outer(int dtype, const OuterArgs& a, const FinishArgs* f, hipStream_t s)
 {
-    return dtype == DT_BF16 ? outer_dt<DT_BF16>(a, s) : outer_dt<DT_F16>(a, s);
+    return dtype == DT_BF16 ? outer_dt<DT_BF16>(a, f, s) : outer_dt<DT_F16>(a, f, s);
 }
 
 }  // namespace sam

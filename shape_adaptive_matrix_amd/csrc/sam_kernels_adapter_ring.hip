@@ -309,7 +309,7 @@ __attribute__((amdgpu_waves_per_eu(1, ring16_waves_per_eu<BM, BN, WM, WN, 64, NB
 adapter_part_shrink_kernel(GemmArgs g, int n, ShrinkArgs a, int more)
 {
     if ((int)blockIdx.x < more) {
-        if ((int)blockIdx.x < shrink_wgs(a)) shrink_part<DT, WM * WN>(a, blockIdx.x);
+        if ((int)blockIdx.x < shrink_all_wgs(a)) shrink_or_group<DT, WM * WN>(a, blockIdx.x);
         return;
     }
     int tm, tn, s;
@@ -367,7 +367,7 @@ hipError_t launch_adapter_ring(int tile, int dtype, int bt, const GemmArgs& g, i
         if (!fn) return hipErrorInvalidDeviceFunction;
         hipLaunchKernelGGL(fn, grid, dim3(k.threads), 0, s, AdapterRingArgs{g, *x});
     } else if (const AdapterPartShrinkFn beside = k.shrink[dtype - 1][bt]) {
-        const int more = (shrink_wgs(*shrink) + 7) / 8 * 8;
+        const int more = (shrink_all_wgs(*shrink) + 7) / 8 * 8;
         hipLaunchKernelGGL(beside, dim3(grid.x + more), dim3(k.threads), 0, s, g, n, *shrink, more);
     } else {
         const AdapterPartFn fn = k.part[dtype - 1][bt];
