@@ -25,10 +25,12 @@ struct Product {
     int tiles_m, tiles_n;
 };
 
-// Fused tiles take whole K, so they need enough tiles to fill the CUs; the
-// rates are those the ring kernels reach with all CUs busy, as parts of the
-// matrix peak. A split product writes and reads its partials once more.
-Product choose(long long rows, long long cols, long long k)
+// Fused tiles take whole K, a round of them as long as the K loop; the rates
+// are those the ring kernels reach with all CUs busy, as parts of the matrix
+// peak. A split product fills the CUs with few tiles, but writes and reads its
+// partials once more.
+// `beside`: the pass that adds the partials has a launch to go with.
+Product choose(long long rows, long long cols, long long k, bool beside)
 {
     static const struct { int tile; double rate; } fused[] = {{0, 0.575}, {1, 0.545}, {2, 0.40}};
     Product best{};
@@ -42,8 +44,7 @@ Product choose(long long rows, long long cols, long long k)
             best = {f.tile, 0, 0, (int)tm, (int)tn};
         }
     }
-    const long long t128 = ((rows + 127) / 128) * ((cols + 127) / 128);
-    if (k <= 4 * kBK || (rows > 64 && t128 >= 160)) return best;
+    if (k <= 4 * kBK) return best;
     Product p{};
     p.tile = rows <= 16 ? 5 : (rows <= 32 ? 4 : (rows <= 64 ? 3 : 2));
     const AdapterTile t = adapter_tile(p.tile);
@@ -56,7 +57,16 @@ Product choose(long long rows, long long cols, long long k)
     s = s < 1 ? 1 : (s > most ? most : s);
     p.k_chunk = (int)(((k + s - 1) / s + kBK - 1) / kBK * kBK);
     p.split = (int)((k + p.k_chunk - 1) / p.k_chunk);
-    return p;
+    if (rows <= 64) return p;
+    // 7.6 us per 1024 values of K in a tile, 0.9 us per MB of partials, and
+    // what the launches cost: T of up to 128 rows takes one more beside a
+    // fused product, the sum of the partials none where it goes with the
+    // adapters' gradients. As measured over 100 to 1024 rows, K and N 512 to 4096,
+    // bf16, rank 16 (512 x 512 x 4096: 17.5 us fused, 31 split; 1024 x 2048 x
+    // 2048: 31 and 35; 256 x 4096 x 2048: 45 and 30; 100 x 1024 x 4096: 25 and 21).
+    const double fused_us = 14 + (rows <= 128 ? 3 : 0) + 7.6 / 1024 * k;
+    const double split_us = (beside ? 9 : 13) + 7.6 / 1024 * p.k_chunk + 0.9e-6 * 4 * p.split * rows * cols;
+    return fused_us <= split_us ? best : p;
 }
 
 int round8(long long x) { return (int)((x + 7) & ~7ll); }
@@ -111,7 +121,7 @@ Layout layout(const Call& c)
     Layout L{};
     L.rp = c.n == 0 ? 0 : (c.r > 64 ? 128 : (c.r > 32 ? 64 : (c.r > 16 ? 32 : 16)));
     const long long rows = c.M, cols = c.back ? c.K : c.N, k = c.back ? c.N : c.K;
-    L.prod = choose(rows, cols, k);
+    L.prod = choose(rows, cols, k, c.back && c.want_ad && c.n);
     unsigned long long at = 0;
     auto take = [&](Region& r, unsigned long long bytes) {
         r.off = at;
@@ -153,7 +163,10 @@ Layout layout(const Call& c)
     long long s, most;
     if (L.wide) {
         s = (2 * kCUs - 64) / ((c.M + 63) / 64 * sides);
-        most = (longest + 255) / 256;
+        // One range is rounded where it is made, a launch less; from 1536
+        // values on several are sooner there all the same (256 x 2048, N 4096:
+        // 34 us and 32; 2049 x 1536: 46 and 47; 4096 x 1024: 46 and 49).
+        most = !c.back && c.K <= 1536 ? 1 : (longest + 255) / 256;
     } else {
         s = (longest + 1023) / 1024 * (L.merged && L.prod.tile == 5 ? 2 : 1);   // waves: four, or the narrowest tile's two
         most = 16;

@@ -53,6 +53,9 @@ struct ShrinkArgs {
     int4* chunks;        // [max_chunks] adapter (-1: no such chunk), place in `order`, rows, first row of a run or -1
 };
 
+// Whether the shrink rounds T itself: there is nothing left to add up.
+__host__ __device__ inline bool shrink_rounds(const ShrinkArgs& a) { return a.wide && a.ksplit == 1; }
+
 // Sum of the split partials of X W plus T B.
 struct FinishArgs {
     const float* part;   // [split][M] rows of N floats, row stride ldp (a multiple of 4)

@@ -52,16 +52,23 @@ __device__ __forceinline__ void split3_bits(float v, unsigned short (&o)[3])
 
 constexpr int kShrinkWaves = 4, kWideRows = 64;
 
-// Rounds a row of T, held by 32 threads (column c0 + 32 q): divides by the
-// power of two below the row's largest value. A row of zeros gets the
+// Rounds a row of T, held by LANES threads (column c0 + LANES q): divides by
+// the power of two below the row's largest value. A row of zeros gets the
 // smallest one (it then never sets the scale of rows that are added up with
 // it), one with Inf or NaN gets 1.
-template <int DT, int NQ>
-__device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide& sd, const float (&t)[NQ], float big,
-                                          bool odd, long long m, int c0, bool mine)
+template <int DT, int NQ, int LANES>
+__device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide& sd, const float (&t)[NQ], long long m,
+                                          int c0, bool mine)
 {
+    float big = 0.0f;
+    bool odd = false;
 #pragma unroll
-    for (int s = 16; s; s >>= 1) {
+    for (int q = 0; q < NQ; ++q) {
+        big = fmaxf(big, fabsf(t[q]));
+        odd |= !(fabsf(t[q]) < INFINITY);
+    }
+#pragma unroll
+    for (int s = LANES / 2; s; s >>= 1) {
         big = fmaxf(big, __shfl_xor(big, s));
         odd |= __shfl_xor((int)odd, s) != 0;
     }
@@ -72,7 +79,7 @@ __device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide&
     unsigned short* o = static_cast<unsigned short*>(sd.t16) + m * a.np * a.rp;
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-        const int c = c0 + 32 * q;
+        const int c = c0 + LANES * q;
         if (c >= a.rp) continue;
         const float v = ldexpf(t[q], -e);
         if (DT == DT_BF16 && a.np == 3) {
@@ -100,9 +107,9 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_kernel(Shrin
 // distinct adapter among them a product of 64 rows and RP ranks. Both operands
 // go straight into LDS, rows of 128 bytes or 256 a wave instruction (loads
 // into fragments would touch 64 lines per KB: measured at 4096 x 11008, rank
-// 64, 54 us, this 39 us), through a ring of NBUF stages; wave w has rows
+// 64, 54 us, this 36), through a ring of NBUF stages; wave w has rows
 // 16 w .. + 15. The partial sums of the K ranges are added, and rounded, by
-// adapter_round_kernel.
+// adapter_round_kernel; one range alone is rounded here.
 // Bound by reading X once: A's traffic from L2 is r / 64 of X's.
 template <int DT, int NR>
 __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_wide_kernel(ShrinkArgs a)
@@ -227,25 +234,33 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_wide_kernel(
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int row = 16 * wave + 4 * grp + v;
-            if (!((same >> row) & 1)) continue;
-            float* o = sd.t32 + ((long long)split * a.M + m0 + row) * RP + lrow;
+            const bool mine = (same >> row) & 1;
+            float t[NR];
 #pragma unroll
-            for (int q = 0; q < NR; ++q)   // ranks past r: zeros also where X holds Inf
-                o[16 * q] = 16 * q + lrow < a.r ? acc[q][v] * f : 0.0f;
+            for (int q = 0; q < NR; ++q) t[q] = 16 * q + lrow < a.r ? acc[q][v] * f : 0.0f;   // ranks past r: zeros also where X holds Inf
+            if (mine && (sd.keep || !shrink_rounds(a))) {
+                float* o = sd.t32 + ((long long)split * a.M + m0 + row) * RP + lrow;
+#pragma unroll
+                for (int q = 0; q < NR; ++q) o[16 * q] = t[q];
+            }
+            if (shrink_rounds(a) && sd.factor) round_row<DT, NR, 16>(a, sd, t, m0 + row, lrow, mine);
         }
     }
 }
 
 // The adapters' rows cut into chunks of a.chunk, numbered in adapter order:
-// where each adapter's chunks start, and each chunk's place. One workgroup.
+// where each adapter's chunks start, and each chunk's place. One workgroup,
+// 256 adapters at a time; a thread has every 256th of their chunks (65536 rows
+// of one adapter, 512 chunks: 4.6 us; with an adapter's chunks on one thread
+// 170).
 __device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
 {
-    __shared__ int sums[4];
+    __shared__ int sums[4], firsts[256], begins[257];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     int base = 0;
     for (int a0 = 0; a0 < a.n; a0 += 256) {
         const int ad = a0 + tid;
-        const int begin = ad < a.n ? a.seg[ad] : 0, rows = ad < a.n ? a.seg[ad + 1] - begin : 0;
+        const int begin = a.seg[min(ad, a.n)], rows = a.seg[min(ad + 1, a.n)] - begin;
         const int count = ad < a.n ? max((rows + a.chunk - 1) / a.chunk, 1) : 0;   // without rows: one that gives zeros
         int sum = count;
 #pragma unroll
@@ -253,21 +268,31 @@ __device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
             const int o = __shfl_up(sum, d);
             if (lane >= d) sum += o;
         }
-        __syncthreads();   // the last step's sums are read
+        __syncthreads();   // the last step's values are read
         if (lane == 63) sums[wave] = sum;
+        begins[tid] = begin;
+        if (tid == 255) begins[256] = begin + rows;
         __syncthreads();
+        const int from = base;
         int first = base + sum - count;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             first += w < wave ? sums[w] : 0;
             base += sums[w];
         }
+        firsts[tid] = first;   // past the last adapter: `base`, as it is now
         if (ad < a.n) a.chunk_first[ad] = first;
-        for (int c = 0; c < count; ++c) {
-            const int at = begin + c * a.chunk, n = min(a.chunk, rows - c * a.chunk);
+        __syncthreads();
+        for (int c = from + tid; c < base; c += 256) {
+            int of = 0;   // the last adapter whose chunks start at c or before
+#pragma unroll
+            for (int d = 128; d; d >>= 1)
+                if (firsts[of + d] <= c) of += d;
+            const int skip = (c - firsts[of]) * a.chunk;
+            const int at = begins[of] + skip, n = min(a.chunk, begins[of + 1] - at);
             const int row0 = n ? a.order[at] : 0;
             // Rows of one run need no look-up.
-            a.chunks[first + c] = make_int4(ad, at, n, n == 0 || a.order[at + n - 1] - row0 == n - 1 ? row0 : -1);
+            a.chunks[c] = make_int4(a0 + of, at, n, n == 0 || a.order[at + n - 1] - row0 == n - 1 ? row0 : -1);
         }
     }
     if (tid == 0) a.chunk_first[a.n] = base;
@@ -279,7 +304,7 @@ __device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
 template <int DT, int NQ>
 __global__ void __launch_bounds__(256) adapter_round_kernel(ShrinkArgs a)
 {
-    if ((int)blockIdx.x >= (a.M + 7) / 8) {
+    if (shrink_rounds(a) || (int)blockIdx.x >= (a.M + 7) / 8) {
         if (blockIdx.y == 0) list_chunks(a);
         return;
     }
@@ -288,8 +313,7 @@ __global__ void __launch_bounds__(256) adapter_round_kernel(ShrinkArgs a)
     const ShrinkSide& sd = a.side[blockIdx.y];
     const int id = m < a.M ? a.ids[m] : -1;
     const bool mine = (unsigned)id < (unsigned)a.n;
-    float t[NQ], big = 0.0f;
-    bool odd = false;
+    float t[NQ];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
         const int c = c0 + 32 * q;
@@ -304,11 +328,9 @@ __global__ void __launch_bounds__(256) adapter_round_kernel(ShrinkArgs a)
             for (int u = 0; u < 8; ++u) v += w[u];
         }
         t[q] = v;
-        big = fmaxf(big, fabsf(v));
-        odd |= !(fabsf(v) < INFINITY);
         if (sd.keep && a.ksplit > 1 && mine && c < a.rp) sd.t32[(long long)m * a.rp + c] = v;
     }
-    if (sd.factor) round_row<DT, NQ>(a, sd, t, big, odd, m, c0, mine);
+    if (sd.factor) round_row<DT, NQ, 32>(a, sd, t, m, c0, mine);
 }
 
 // 4 values of B as floats.
@@ -452,7 +474,7 @@ constexpr int kOuterCols = 256;
 // factors, so that the type's range keeps it), a value and its remainder, the
 // sum right to 2^-22 of the chunk's largest.
 // Bound by reading X once. Measured at X, dY 4096 x 4096, rank 16, 8
-// adapters in runs: 24 us (with the look-up of every row's place in
+// adapters in runs: 21 us (with the look-up of every row's place in
 // front of its load 26 us; loads two steps ahead spill).
 // Chunks of adapters with one chunk go to `out`, others to `part`, which
 // outer_sum adds in order.
@@ -635,34 +657,59 @@ __global__ void __launch_bounds__(256) adapter_outer_finish_kernel(OuterArgs o, 
         finish_rows<DT, WS>(f, blockIdx.x - outer_wgs);
 }
 
-// Adapters with several chunks get the sum of their partials in chunk order. 1024 values a workgroup.
+// Adapters with several chunks get the sum of their partials. A wave has 256
+// values; WS 4: the four waves of a workgroup have the same ones and a quarter
+// of the chunks each, in chunk order, and their sums are added in wave order.
+// Latency bounds it, so all of a batch's loads go out together.
+template <int WS>
 __global__ void __launch_bounds__(256) adapter_outer_sum_kernel(OuterArgs a)
 {
+    __shared__ float sums[3][256];
+    constexpr int V = 1024 / WS;   // values of a workgroup
     const long long v0 = (long long)a.r * a.side[0].cols, v1 = (long long)a.r * a.side[1].cols;
-    const int b0 = (int)((v0 + 1023) / 1024), b1 = (int)((v1 + 1023) / 1024);
-    const int ad = blockIdx.x / (b0 + b1), b = blockIdx.x % (b0 + b1);
+    const int b0 = (int)((v0 + V - 1) / V), b1 = (int)((v1 + V - 1) / V);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int ad = (int)(blockIdx.x / (unsigned)(b0 + b1)), b = (int)(blockIdx.x % (unsigned)(b0 + b1));
     const int first = a.chunk_first[ad], count = a.chunk_first[ad + 1] - first;
     if (count == 1) return;
     const bool second = b >= b0;
     const OuterSide& sd = a.side[second];
     const long long vals = second ? v1 : v0;
-    const long long at = (long long)(second ? b - b0 : b) * 1024 + threadIdx.x;
-    float* out = sd.out + (long long)ad * vals;
+    const long long at = (long long)(second ? b - b0 : b) * V + (WS == 4 ? 0 : wave * 256) + lane;
     const float* part = sd.part + (long long)first * vals;
+    const int begin = WS == 4 ? (int)((long long)count * wave / 4) : 0;
+    const int end = WS == 4 ? (int)((long long)count * (wave + 1) / 4) : count;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = begin; c < end; c += 8) {
+        float x[8][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const long long i = at + 256 * q;
-        if (i >= vals) continue;
-        float v = 0.0f;
-        for (int c = 0; c < count; c += 8) {
-            float x[8];
+        for (int u = 0; u < 8; ++u)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = part[(long long)min(c + u, count - 1) * vals + i];
+            for (int q = 0; q < 4; ++q) {
+                const long long i = at + 64 * q;
+                x[u][q] = c + u < end && i < vals ? part[(long long)(c + u) * vals + i] : 0.0f;
+            }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v += c + u < count ? x[u] : 0.0f;
-        }
-        out[i] = v;
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] += x[u][q];
     }
+    if (WS == 4) {
+        if (wave) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sums[wave - 1][lane + 64 * q] = v[q];
+        }
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int w = 0; w < 3; ++w) v[q] += sums[w][lane + 64 * q];
+    }
+    float* out = sd.out + (long long)ad * vals;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (at + 64 * q < vals) out[at + 64 * q] = v[q];
 }
 
 // Copies of operands whose rows are no whole 16-byte pieces, into rows that
@@ -729,7 +776,9 @@ hipError_t shrink_dt(const ShrinkArgs& a, hipStream_t s)
 template <int DT>
 hipError_t round_dt(const ShrinkArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.M + 7) / 8 + (a.order ? 1 : 0)), (unsigned)a.sides), block(256);
+    const int rows = shrink_rounds(a) ? 0 : (a.M + 7) / 8;
+    const dim3 grid((unsigned)(rows + (a.order ? 1 : 0)), (unsigned)(rows ? a.sides : 1)), block(256);
+    if (!grid.x) return hipSuccess;
     switch ((a.rp + 31) / 32) {
     case 1: hipLaunchKernelGGL((adapter_round_kernel<DT, 1>), grid, block, 0, s, a); break;
     case 2: hipLaunchKernelGGL((adapter_round_kernel<DT, 2>), grid, block, 0, s, a); break;
@@ -784,8 +833,17 @@ hipError_t outer_dt(const OuterArgs& a, const FinishArgs* f, hipStream_t s)
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.M <= a.chunk) return e;   // no adapter has a second chunk
-    const long long b = ((long long)a.r * a.side[0].cols + 1023) / 1024 + ((long long)a.r * a.side[1].cols + 1023) / 1024;
-    hipLaunchKernelGGL(adapter_outer_sum_kernel, dim3((unsigned)(a.n * b)), dim3(256), 0, s, a);
+    // Four waves a value where an adapter can have many chunks: 512 of 8192
+    // values 10 us (one wave each, a value at a time, 57); 16 of 131072 values
+    // 6.9 with four waves, 5.1 with one.
+    const bool share = (a.M + a.chunk - 1) / a.chunk > 32;
+    const int vals = share ? 256 : 1024;
+    const long long b = ((long long)a.r * a.side[0].cols + vals - 1) / vals + ((long long)a.r * a.side[1].cols + vals - 1) / vals;
+    const dim3 grid((unsigned)(a.n * b));
+    if (share)
+        hipLaunchKernelGGL(adapter_outer_sum_kernel<4>, grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL(adapter_outer_sum_kernel<1>, grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -59,6 +59,26 @@ def test_backward(shape, dtype):
             ref.close(g, *w, f"{name} trans_w={trans_w}")
 
 
+# One adapter with hundreds of chunks of rows; T in one K range for both
+# gradients; more adapters than a workgroup lists at a time, some with two
+# chunks; whole tiles over a longer K.
+MANY = [(20000, 64, 72, 8, 1), (33000, 136, 64, 24, 3), (20000, 40, 24, 4, 300), (300, 1000, 2000, 16, 4)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", MANY, ids=str)
+def test_many_rows_chunks_and_adapters(shape, dtype):
+    M, K, N, r, n = shape
+    for runs in (True, False):
+        X, W, A, B, ids, scale = make(*shape, dtype, 31 + runs, runs, runs)
+        dY = (torch.randn(M, N, generator=torch.Generator().manual_seed(6)) * 0.1).to(X.dtype).cuda()
+        Y = sam.adapter_gemm(X, W, A, B, ids, scale, trans_w=runs)
+        ref.close(Y, *ref.forward(X, W, A, B, ids, scale, runs), f"Y runs={runs}")
+        got = sam.adapter_backward(dY, X, W, A, B, ids, scale, trans_w=runs)
+        for g, w, name in zip(got, ref.backward(dY, X, W, A, B, ids, scale, runs), ("dX", "dA", "dB")):
+            ref.close(g, *w, f"{name} runs={runs}")
+
+
 @pytest.mark.parametrize("M", [40, 2049])
 def test_other_requests_inf_and_nan_stay_out(M):
     K, N, r, n = (2048, 384, 16, 6) if M == 40 else (72, 4097, 16, 6)
