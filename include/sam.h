@@ -290,8 +290,9 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  * a SAM_BF16 result) relative to its row's largest value. Other base
  * addresses must be 16-byte aligned; rows that are no whole 16-byte pieces (K
  * or N not a multiple of 8, or such a stride) are copied into the workspace
- * first. Y must not overlap anything
- * else. Workspace: sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when
+ * first, all but W of rows along N with a stride that is a multiple of 8: it
+ * is read in place, in aligned 16-byte pieces, up to 14 bytes behind a row's
+ * end with the last of them. Y must not overlap anything else. Workspace: sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when
  * short. N, K and strides up to 2.08 M values. Asynchronous on `stream`, no
  * atomics on results, fixed summation order. */
 sam_status sam_adapter_gemm(sam_dtype dtype, sam_op trans_w, int64_t M,

@@ -131,7 +131,11 @@ Layout layout(const Call& c)
     // Rows that are no whole 16-byte pieces are copied into rows that are.
     const long long wr = c.trans_w ? c.N : c.K, wc = c.trans_w ? c.K : c.N;   // W as stored
     L.pad_x = c.K % 8 || c.ldx % 8;
-    L.pad_w = wc % 8 || c.ldw % 8;
+    // Of W only where its rows run along the product's K: values behind a
+    // shorter row then reach columns that are not stored, and they share their
+    // 16 aligned bytes with the row's last ones.
+    const bool along_k = (c.trans_w != 0) != c.back;
+    L.pad_w = (along_k && wc % 8) || c.ldw % 8;
     L.pad_a = c.n && c.K % 8;
     L.pad_b = c.n && c.N % 8;
     L.pad_dy = c.back && (c.N % 8 || c.lddy % 8);

@@ -84,6 +84,23 @@ def test_workspace_queries():
     assert q(sam.BF16, 0, 64, 64, 64, 2, 8, 64, 64, 64, 0, 1) == 0 and b.value <= whole
 
 
+def test_w_with_padded_rows_takes_no_copy():
+    """Rows along the product's columns: read in place; along its K: copied."""
+    def need(trans_w, M, N, K, ldw, back):
+        b = ctypes.c_uint64()
+        if back:
+            assert L.sam_adapter_backward_workspace(sam.BF16, trans_w, M, N, K, 2, 16, N, K, ldw, 1, 0, ctypes.byref(b)) == 0
+        else:
+            assert L.sam_adapter_gemm_workspace(sam.BF16, trans_w, M, N, K, 2, 16, K, ldw, ctypes.byref(b)) == 0
+        return b.value
+
+    copy = 2 * 512 * 4008
+    assert need(0, 40, 4001, 512, 4001, 0) - need(0, 40, 4001, 512, 4008, 0) >= copy
+    assert need(1, 40, 512, 4001, 4001, 0) == need(1, 40, 512, 4001, 4008, 0)
+    assert need(1, 40, 512, 4001, 4001, 1) - need(1, 40, 512, 4001, 4008, 1) >= copy
+    assert need(0, 40, 4001, 512, 4001, 1) == need(0, 40, 4001, 512, 4008, 1)
+
+
 def _tensors():
     t = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
     return dict(X=t(4, 32), W=t(32, 48), A=t(2, 8, 32), B=t(2, 8, 48), ids=torch.zeros(4, dtype=torch.int32),

@@ -154,6 +154,23 @@ def test_views_with_padded_rows(shape, pad):
     assert (dXp[:, K:] == -77.0).all() and (dXp[M] == -77.0).all()
 
 
+@pytest.mark.parametrize("M", [7, 40, 300, 2049])
+def test_w_with_padded_rows_is_read_in_place(M):
+    """W's rows along the product's columns: what is behind a row is not looked at."""
+    K, N = 520, 2501
+    X, W, A, B, ids, scale = make(M, K, N, 16, 3, "bf16", 13)
+    Wp = torch.full((K, 2504), float("nan"), device="cuda").to(X.dtype)
+    Wp[:, :N] = W
+    Y = sam.adapter_gemm(X, Wp[:, :N], A, B, ids, scale)
+    ref.close(Y, *ref.forward(X, W, A, B, ids, scale, False))
+    assert torch.equal(Y, sam.adapter_gemm(X, W, A, B, ids, scale))
+    dY = torch.randn(M, K, device="cuda").to(X.dtype)   # of the projection onto W^T: dX = dY W
+    Xt = torch.randn(M, N, device="cuda").to(X.dtype)
+    got = sam.adapter_backward(dY, Xt, Wp[:, :N], B, A, ids, scale, trans_w=True)
+    for g, w in zip(got, ref.backward(dY, Xt, W, B, A, ids, scale, True)):
+        ref.close(g, *w)
+
+
 def test_parts_of_the_backward_pass_alone():
     X, W, A, B, ids, scale = make(300, 264, 136, 16, 3, "bf16", 9)
     dY = torch.randn(300, 136, device="cuda").to(X.dtype)
