@@ -474,8 +474,8 @@ constexpr int kOuterCols = 256;
 // factors, so that the type's range keeps it), a value and its remainder, the
 // sum right to 2^-22 of the chunk's largest.
 // Bound by reading X once. Measured at X, dY 4096 x 4096, rank 16, 8
-// adapters in runs: 21 us (with the look-up of every row's place in
-// front of its load 26 us; loads two steps ahead spill).
+// adapters in runs, both gradients: 18 us with loads two steps ahead, 22.6 one
+// step ahead, 14 with all of it but the loads.
 // Chunks of adapters with one chunk go to `out`, others to `part`, which
 // outer_sum adds in order.
 template <int DT, int NR>
@@ -517,53 +517,57 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
         if (rows) e = ilogbf(big);   // factors are powers of two, at least 2^-126
     }
 
-    // Loads of step s into registers: X 32 rows x 512 bytes, four 16-byte
-    // pieces a thread; T 32 rows x RP floats, RP / 8 a thread.
+    // Loads of step s into one of two register sets: X 32 rows x 512 bytes,
+    // four 16-byte pieces a thread; T 32 rows x RP floats, RP / 8 a thread.
+    // None sits behind a condition (the compiler could not count how many
+    // follow it, and would wait for all): rows past the chunk's end and
+    // columns past X's read its last ones, and become zeros in `put`. A step's
+    // row numbers come a step ahead of it.
     constexpr int TP = RP / 8;
-    u4 rx[4];
-    float rt[TP];
+    struct Set {
+        u4 x[4];
+        float t[TP];
+    };
+    Set set[2];
+    int next_row = 0;   // of the next step to load, row lane % 32
     const int trow = tid >> 3, tc = (tid & 7) * TP;
-    auto load = [&](int s) {
+    const int col = c0 + (tid & 31) * 8;
+    const unsigned short* xc = static_cast<const unsigned short*>(sd.X) + min(col, (sd.cols - 1) & ~7);
+    auto load = [&](int s, Set& r) {
+        const int rows_here = next_row;
+        next_row = order[min((s + 1) * 32 + (lane & 31), rows - 1)];
+        auto row_of = [&](int i) -> long long {
+            return run ? row0 + min(s * 32 + i, rows - 1) : __shfl(rows_here, i);
+        };
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = s * 32 + q * 8 + (tid >> 5), c = c0 + (tid & 31) * 8;
-            rx[q] = u4{0u, 0u, 0u, 0u};
-            if (i < rows && c < sd.cols) {
-                const long long m = run ? row0 + i : order[i];
-                rx[q] = *reinterpret_cast<const u4*>(static_cast<const unsigned short*>(sd.X) + m * sd.ldx + c);
-            }
-        }
-        const int i = s * 32 + trow;
+        for (int q = 0; q < 4; ++q) r.x[q] = *reinterpret_cast<const u4*>(xc + row_of(q * 8 + (tid >> 5)) * sd.ldx);
+        const float* p = sd.t32 + row_of(trow) * RP + tc;
 #pragma unroll
-        for (int q = 0; q < TP; ++q) rt[q] = 0.0f;
-        if (i < rows) {
-            const long long m = run ? row0 + i : order[i];
-            const float* p = sd.t32 + m * RP + tc;
-#pragma unroll
-            for (int q = 0; q < TP; q += 2) {
-                const float2 v = *reinterpret_cast<const float2*>(p + q);
-                rt[q] = v.x;
-                rt[q + 1] = v.y;
-            }
+        for (int q = 0; q < TP; q += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(p + q);
+            r.t[q] = v.x;
+            r.t[q + 1] = v.y;
         }
     };
-    auto put = [&](int s) {
+    auto put = [&](int s, const Set& r) {
         unsigned char* xb = lds[s & 1];
         unsigned char* tb = xb + XB;
+        const int left = rows - s * 32;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int row = q * 8 + (tid >> 5), c = (tid & 31) ^ nsw(row);
-            *reinterpret_cast<u4*>(xb + row * kOuterCols * 2 + c * 16) = rx[q];
+            *reinterpret_cast<u4*>(xb + row * kOuterCols * 2 + c * 16) = row < left && col < sd.cols ? r.x[q] : u4{0u, 0u, 0u, 0u};
         }
 #pragma unroll
         for (int q = 0; q < TP; q += 2) {
             unsigned short h[2][NP];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+                const float t = trow < left ? r.t[q + k] : 0.0f;
                 if constexpr (NP == 3)
-                    split3_bits(rt[q + k], h[k]);
+                    split3_bits(t, h[k]);
                 else
-                    split_bits<DT>(ldexpf(rt[q + k], -e), h[k][0], h[k][1]);
+                    split_bits<DT>(ldexpf(t, -e), h[k][0], h[k][1]);
             }
 #pragma unroll
             for (int k = 0; k < NP; ++k)
@@ -611,12 +615,26 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
     // A step's values are in LDS from its `put` to the barrier after the next
     // one's: two buffers, one barrier a step.
     const int steps = (rows + 31) / 32;
-    load(0);
-    for (int s = 0; s < steps; ++s) {
-        put(s);
-        load(s + 1);   // past the last step: nothing is read
+    if (steps) {
+        next_row = order[min(lane & 31, rows - 1)];
+        load(0, set[0]);
+        load(1, set[1]);
+    }
+    int s = 0;
+    for (; s + 2 < steps; s += 2)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            put(s + h, set[h]);
+            load(s + h + 2, set[h]);   // past the last step: its last row, not used
+            __syncthreads();
+            multiply(s + h);
+        }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (s + h >= steps) break;
+        put(s + h, set[h]);
         __syncthreads();
-        multiply(s);
+        multiply(s + h);
     }
     const bool direct = a.chunk_first[ad + 1] - a.chunk_first[ad] == 1;
     float* o = direct ? sd.out + (long long)ad * a.r * sd.cols : sd.part + (long long)ch * a.r * sd.cols;
@@ -641,15 +659,19 @@ __global__ void __launch_bounds__(256) adapter_finish_kernel(FinishArgs a)
     finish_rows<DT, WS>(a, blockIdx.x);
 }
 
+// Waves a SIMD that the outer product's registers have to leave room for.
+constexpr int outer_waves(int nr) { return nr <= 2 ? 3 : (nr == 4 ? 2 : 1); }
+
 template <int DT, int NR>
-__global__ void __launch_bounds__(256) adapter_outer_kernel(OuterArgs a)
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(outer_waves(NR)))) adapter_outer_kernel(OuterArgs a)
 {
     outer_tile<DT, NR>(a, blockIdx.x);
 }
 
 // Both in one launch, where the backward pass has both: neither needs the other.
 template <int DT, int NR, int WS>
-__global__ void __launch_bounds__(256) adapter_outer_finish_kernel(OuterArgs o, FinishArgs f, int outer_wgs)
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(outer_waves(NR))))
+adapter_outer_finish_kernel(OuterArgs o, FinishArgs f, int outer_wgs)
 {
     if ((int)blockIdx.x < outer_wgs)
         outer_tile<DT, NR>(o, blockIdx.x);
