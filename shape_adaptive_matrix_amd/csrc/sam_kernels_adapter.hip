@@ -855,10 +855,11 @@ hipError_t outer_dt(const OuterArgs& a, const FinishArgs* f, hipStream_t s)
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.M <= a.chunk) return e;   // no adapter has a second chunk
-    // Four waves a value where an adapter can have many chunks: 512 of 8192
+    // Four waves a value where the adapters have many chunks: 512 of 8192
     // values 10 us (one wave each, a value at a time, 57); 16 of 131072 values
     // 6.9 with four waves, 5.1 with one.
-    const bool share = (a.M + a.chunk - 1) / a.chunk > 32;
+    const long long chunks = (a.M + a.chunk - 1) / a.chunk;
+    const bool share = chunks > 32 && chunks > 4ll * a.n;
     const int vals = share ? 256 : 1024;
     const long long b = ((long long)a.r * a.side[0].cols + vals - 1) / vals + ((long long)a.r * a.side[1].cols + vals - 1) / vals;
     const dim3 grid((unsigned)(a.n * b));
