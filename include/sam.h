@@ -290,11 +290,13 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  * a SAM_BF16 result) relative to its row's largest value. Other base
  * addresses must be 16-byte aligned; rows that are no whole 16-byte pieces (K
  * or N not a multiple of 8, or such a stride) are copied into the workspace
- * first, all but W of rows along N with a stride that is a multiple of 8: it
- * is read in place, in aligned 16-byte pieces, up to 14 bytes behind a row's
- * end with the last of them. Y must not overlap anything else. Workspace: sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when
- * short. N, K and strides up to 2.08 M values. Asynchronous on `stream`, no
- * atomics on results, fixed summation order. */
+ * first, all but a W whose rows run along the result's columns (N here, K in
+ * the gradients) with a stride that is a multiple of 8: it is read in place,
+ * in aligned 16-byte pieces, up to 14 bytes behind a row's end with the last
+ * of them. Y must not overlap anything else. Workspace:
+ * sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when short. N, K and
+ * strides up to 2.08 M values. Asynchronous on `stream`, no atomics on
+ * results, fixed summation order. */
 sam_status sam_adapter_gemm(sam_dtype dtype, sam_op trans_w, int64_t M,
                             int64_t N, int64_t K, int64_t n_adapters,
                             int64_t rank, const void* X, int64_t ldx,
@@ -320,9 +322,10 @@ sam_status sam_adapter_gemm_workspace(sam_dtype dtype, sam_op trans_w,
  * n_adapters x rank rows) are written whole, zeros for adapters without
  * rows. dX (type `out`: SAM_F32 or dtype, row stride lddx >= K) may be NULL,
  * and so may dA and dB together; what is not wanted is not computed. Rows
- * are added up in row order in chunks of a fixed size: the same bits every
- * time. dA and dB take the intermediate whole (SAM_BF16) or to 22 bits. Everything else as for sam_adapter_gemm. With M == 0 dA and dB are
- * zeros. */
+ * are added up in row order in chunks of a fixed size, and these in a fixed
+ * order: the same bits every time. dA and dB take the intermediate whole
+ * (SAM_BF16) or to 22 bits. Everything else as for sam_adapter_gemm. With M ==
+ * 0 dA and dB are zeros. */
 sam_status sam_adapter_backward(sam_dtype dtype, sam_op trans_w, int64_t M,
                                 int64_t N, int64_t K, int64_t n_adapters,
                                 int64_t rank, const void* dY, int64_t lddy,
