@@ -210,9 +210,10 @@ struct Row {
 // for all): pieces past a row's end read zeros, entries past the last read
 // the last, and what they hold is dropped when it is used.
 // A row has one barrier, between its sums and what follows from them: the
-// teacher's entries go 64 to a wave, and what is to be written behind the
-// whole row (the loss, the entries' own gradients) goes out behind the next
-// row's barrier.
+// teacher's entries go 64 to a wave (more than the waves take at once have
+// their logits read behind it, and a second barrier before the row's stores),
+// and what is to be written behind the whole row (the loss, the entries' own
+// gradients) goes out behind the next row's barrier.
 // Measured, loss and gradient: 4096 x 32768 bf16 100 us (rows on
 // workgroups of their own, everything between barriers: 123), 1024 x 131072
 // FP32 219 us (274).
@@ -446,6 +447,10 @@ distill_kernel(DistillArgs a)
             if (on) finish_row(row, par);
             return;
         }
+        // The gradient may take the logits' place: no wave stores any of it
+        // while another still reads the logits of its further entries.
+        if constexpr (NW > 1 && TOP > 64 * NW)
+            if (chunks > NW) __syncthreads();
 
         T* g = static_cast<T*>(a.grad) + row * a.ldg;
         const T* gb = g + c.sp.head;   // aligned to a value: the hardware's unaligned stores

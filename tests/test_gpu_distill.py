@@ -253,3 +253,30 @@ def test_far_rows():
     ref.close(lse[some], *want[1])
     sam.distill_grad(z, lse, ta, ia, wa, grad=z)
     ref.close(z[some], *want[2])
+
+
+# More entries than the workgroup's waves take at once (64 each): 256 threads
+# up to V = 8192 in 16 bits (16384 with many rows), 512 threads up to 65536
+# with many rows; more rows than workgroups in the last three.
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("R,V,k", [(R, V, k) for R in (40, 600) for V in (700, 4096, 8192, 16000, 60000)
+                                   for k in (257, 300, 513, 700, 1024)] + [(2300, 700, 1024), (2300, 4000, 300), (1600, 20011, 600)])
+def test_many_entries_in_the_logits_place(R, V, k, dtype):
+    """The same bits in the logits' place as apart from them, and those of the definition."""
+    g = torch.Generator(device="cuda").manual_seed(R + V + k)
+    z = (torch.randn(R, V, device="cuda", generator=g) * 3).to(TYPES[dtype])
+    t = (torch.randn(R, k, device="cuda", generator=g) * 4).to(TYPES[dtype])
+    idx = torch.randint(-1, V, (R, k), device="cuda", generator=g, dtype=torch.int32)   # some more than once
+    w = torch.rand(R, device="cuda", generator=g) + 0.25
+    w[1::7] = 0.0
+    loss, grad = sam.distill(z, t, idx, w, 1.5)
+    own, _ = sam.distill_loss(z, t, idx, w, 1.5)
+    place = z.clone()
+    loss_in_place, same = sam.distill(place, t, idx, w, 1.5, grad=place)
+    assert same is place
+    assert torch.equal(loss, loss_in_place) and torch.equal(grad, place)
+    for rows in torch.arange(R, device="cuda").split(256):
+        want = ref.reference(z[rows], t[rows], idx[rows], w[rows], 1.5)
+        ref.close(loss[rows], *want[0], "loss with gradient")
+        ref.close(own[rows], *want[0], "loss")
+        ref.close(grad[rows], *want[2], "gradient")
