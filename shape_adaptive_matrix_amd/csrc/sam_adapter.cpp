@@ -44,7 +44,7 @@ Product choose(long long rows, long long cols, long long k, bool beside)
             best = {f.tile, 0, 0, (int)tm, (int)tn};
         }
     }
-    if (k <= 4 * kBK) return best;
+    if (rows == 0 || k <= 4 * kBK) return best;   // no rows: no tiles to share the CUs
     Product p{};
     p.tile = rows <= 16 ? 5 : (rows <= 32 ? 4 : (rows <= 64 ? 3 : 2));
     const AdapterTile t = adapter_tile(p.tile);

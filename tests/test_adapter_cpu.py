@@ -1,6 +1,9 @@
 """What the adapter entry points refuse, and their workspace queries, without a
 GPU: everything is rejected on the host before any device call."""
 import ctypes
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 import torch
@@ -120,3 +123,26 @@ def test_binding_refuses(change):
     dY = torch.zeros(4, 48, dtype=torch.bfloat16)
     with pytest.raises((TypeError, ValueError)):
         sam.adapter_backward(dY, **args)
+
+
+@pytest.mark.parametrize("N,K", [(72, 64), (512, 64), (64, 512), (4096, 4096), (2049, 1025)])
+def test_no_rows_is_answered(N, K):
+    """In a process of its own: the library must not end it."""
+    code = f"""
+import ctypes, shape_adaptive_matrix_amd as sam
+L, b, P = sam.lib(), ctypes.c_uint64(), 1 << 20
+for trans in (0, 1):
+    ldw = {K} if trans else {N}
+    for n in (0, 1, 3):
+        assert L.sam_adapter_gemm_workspace(sam.BF16, trans, 0, {N}, {K}, n, 8, {K}, ldw, ctypes.byref(b)) == 0
+        for dx, dab in ((0, 0), (0, 1), (1, 0), (1, 1)):
+            assert L.sam_adapter_backward_workspace(sam.F16, trans, 0, {N}, {K}, n, 8, {N}, {K}, ldw, dx, dab,
+                                                    ctypes.byref(b)) == 0
+            if dab and n:
+                assert 0 < b.value < 1 << 30
+    # Refused for its short workspace, so the layout is made and nothing is launched.
+    assert L.sam_adapter_backward(sam.BF16, trans, 0, {N}, {K}, 3, 8, P, {N}, 2 * P, {K}, None, ldw, 4 * P, 5 * P, 6 * P,
+                                  None, sam.F32, None, {K}, 8 * P, 12 * P, 16 * P, 1, None) == -3
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-500:]

@@ -253,3 +253,15 @@ def test_far_rows():
     assert not dX[left].any()
     ref.close(dA, *want[1])
     ref.close(dB, *want[2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("K,N", [(64, 72), (64, 512), (4096, 2049)])
+def test_no_rows_over_any_length(K, N, dtype):
+    X, W, A, B, ids, scale = make(1, K, N, 8, 3, dtype, 6)
+    assert sam.adapter_gemm(X[:0], W, A, B, ids[:0], scale).shape == (0, N)
+    for need_dx in (True, False):
+        full = {name: torch.full((3, 8, c), 7.0, device="cuda") for name, c in (("dA", K), ("dB", N))}
+        dX, dA, dB = sam.adapter_backward(X.new_empty(0, N), X[:0], W, A, B, ids[:0], scale, need_dx=need_dx, **full)
+        assert (dX.shape == (0, K)) if need_dx else dX is None
+        assert dA is full["dA"] and dB is full["dB"] and not dA.any() and not dB.any()
