@@ -338,9 +338,12 @@ def gemm_noalloc(A, B, C=None, dtype=None, stream=None):
 
 def _rows(t, name):
     """Row stride of a 2-D tensor whose rows are contiguous (a compact matrix
-    or a view of one with padded rows)."""
+    or a view of one with padded rows). Rows that share memory (an expanded
+    tensor's) have no such stride."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows share memory (stride {t.stride(0)}, rows of {t.shape[1]}): pass a copy")
     return max(int(t.stride(0)), int(t.shape[1]), 1)
 
 
@@ -493,6 +496,8 @@ def _matrix(t, name):
     (rows, cols), (ld, step) = t.shape, t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name}'s rows share memory (stride {ld}, rows of {cols}): pass a copy")
     return rows, cols, max(ld, cols, 1)
 
 

@@ -423,3 +423,17 @@ def test_no_alloc_pairs_still_need_scratch():
     firsts = [sam.plan(*pair[0][:3], pair[0][3])["workspace_bytes"] for pair in PAIRS]
     seconds = [sam.plan(*pair[1][:3], pair[1][3])["workspace_bytes"] for pair in PAIRS]
     assert any(b < a for a, b in zip(firsts, seconds))        # a smaller second call is covered
+
+
+@pytest.mark.parametrize("strides", [(0, 1), (1, 1), (31, 1)], ids=str)
+def test_gemm_ex_refuses_rows_that_share_memory(strides):
+    """A row stride under a row's length was taken for a compact matrix."""
+    import torch
+    good = lambda: torch.zeros(32, 32)  # noqa: E731
+    bad = lambda: torch.zeros(4096).as_strided((32, 32), strides)  # noqa: E731
+    for args in ((bad(), good()), (good(), bad())):
+        with pytest.raises(ValueError, match="share memory"):
+            sam.gemm_ex(*args)
+    with pytest.raises(ValueError, match="share memory"):
+        sam._rows(bad(), "C")
+    assert sam._rows(good()[:, :20], "A") == 32 and sam._rows(good()[:1].expand(1, 32), "A") == 32

@@ -146,3 +146,30 @@ for trans in (0, 1):
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parent.parent, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-500:]
+
+
+SHARED = [(0, 1), (1, 1), (31, 1)]   # strides of rows of 32 and 48 that share memory: broadcast, and overlapping windows
+
+
+@pytest.mark.parametrize("strides", SHARED, ids=str)
+def test_rows_that_share_memory_are_refused(strides, monkeypatch):
+    """A row stride under a row's length was taken for a compact matrix."""
+    shared = lambda rows, cols, like: like.new_zeros(4096).as_strided((rows, cols), strides)  # noqa: E731
+    args = _tensors()
+    h, f = args["X"], args["scale"]
+    dY = h.new_zeros(4, 48)
+    monkeypatch.setattr(sam, "_one_gpu", lambda *a: 0)   # host tensors, for results are looked at behind that check
+    for change in (dict(X=shared(4, 32, h)), dict(W=shared(32, 48, h)), dict(W=shared(48, 32, h), trans_w=True)):
+        with pytest.raises(ValueError, match="share memory"):
+            sam.adapter_gemm(**{**args, **change})
+        with pytest.raises(ValueError, match="share memory"):
+            sam.adapter_backward(dY, **{**args, **change})
+    with pytest.raises(ValueError, match="share memory"):
+        sam.adapter_gemm(**args, Y=shared(4, 48, f))
+    with pytest.raises(ValueError, match="share memory"):
+        sam.adapter_backward(shared(4, 48, h), **args)
+    with pytest.raises(ValueError, match="share memory"):
+        sam.adapter_backward(dY, **args, dX=shared(4, 32, f))
+    # One row, one column, or none shares nothing.
+    for rows, cols, st in ((1, 32, (0, 1)), (1, 32, (7, 1)), (4, 1, (1, 0)), (0, 32, (0, 1)), (4, 32, (32, 1)), (4, 32, (40, 1))):
+        assert sam._matrix(h.new_zeros(4096).as_strided((rows, cols), st), "X")[:2] == (rows, cols)

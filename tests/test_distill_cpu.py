@@ -79,3 +79,18 @@ def test_binding_refuses(change):
     for call in (sam.distill_loss, sam.distill, lambda **a: sam.distill_grad(lse=torch.zeros(4), **a)):
         with pytest.raises((TypeError, ValueError)):
             call(**args)
+
+
+@pytest.mark.parametrize("strides", [(0, 1), (1, 1), (49, 1)], ids=str)
+def test_rows_that_share_memory_are_refused(strides, monkeypatch):
+    """A row stride under a row's length was taken for a compact matrix."""
+    shared = lambda: torch.zeros(4096).as_strided((4, 50), strides)  # noqa: E731
+    rest = dict(teacher=torch.zeros(4, 5), index=torch.zeros(4, 5, dtype=torch.int32), weight=torch.ones(4))
+    monkeypatch.setattr(sam, "_one_gpu", lambda *a: 0)   # host tensors, for results are looked at behind that check
+    lse = torch.zeros(4)
+    for call in (sam.distill_loss, sam.distill, lambda z, **a: sam.distill_grad(z, lse, **a)):
+        with pytest.raises(ValueError, match="share memory"):
+            call(shared(), **rest)
+    for call in (sam.distill, lambda z, **a: sam.distill_grad(z, lse, **a)):
+        with pytest.raises(ValueError, match="share memory"):
+            call(torch.zeros(4, 50), **rest, grad=shared())
