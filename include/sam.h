@@ -295,7 +295,7 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  * in aligned 16-byte pieces, up to 14 bytes behind a row's end with the last
  * of them. Y must not overlap anything else. Workspace:
  * sam_adapter_gemm_workspace() bytes, SAM_ERR_WORKSPACE when short. N, K and
- * strides up to 2.08 M values. Asynchronous on `stream`, no atomics on
+ * strides up to 2.08 M values (a single row's stride may be any). Asynchronous on `stream`, no atomics on
  * results, fixed summation order. */
 sam_status sam_adapter_gemm(sam_dtype dtype, sam_op trans_w, int64_t M,
                             int64_t N, int64_t K, int64_t n_adapters,

@@ -424,6 +424,13 @@ unsigned long long span(long long rows, long long ld, long long cols, int es)
     return rows > 0 ? ((unsigned long long)(rows - 1) * ld + cols) * es : 0;
 }
 
+// A single row's stride reaches nothing: it is neither a reason to refuse it
+// nor one to copy it.
+long long stride_of(long long rows, long long ld, long long cols)
+{
+    return rows <= 1 && cols >= 1 && cols < (1ll << 31) && ld > round8(cols) ? round8(cols) : ld;
+}
+
 Call forward_call(int dtype, int trans_w, long long M, long long N, long long K, long long n, long long r, long long ldx,
                   long long ldw, int out, long long ldy)
 {
@@ -435,10 +442,10 @@ Call forward_call(int dtype, int trans_w, long long M, long long N, long long K,
     c.K = K;
     c.n = n;
     c.r = r;
-    c.ldx = ldx;
-    c.ldw = ldw;
+    c.ldx = stride_of(M, ldx, K);
+    c.ldw = stride_of(trans_w ? N : K, ldw, trans_w ? K : N);
     c.out = out;
-    c.ldy = ldy;
+    c.ldy = stride_of(M, ldy, N);
     return c;
 }
 
@@ -502,9 +509,9 @@ static Call backward_call(sam_dtype dtype, sam_op trans_w, int64_t M, int64_t N,
 {
     Call c = forward_call(dtype, trans_w, M, N, K, n, r, ldx, ldw, out, N);
     c.back = true;
-    c.lddy = lddy;
+    c.lddy = stride_of(M, lddy, N);
     c.want_dx = dx;
-    c.lddx = dx ? lddx : K;
+    c.lddx = dx ? stride_of(M, lddx, K) : K;
     c.want_ad = ad;
     return c;
 }

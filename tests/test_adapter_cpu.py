@@ -173,3 +173,18 @@ def test_rows_that_share_memory_are_refused(strides, monkeypatch):
     # One row, one column, or none shares nothing.
     for rows, cols, st in ((1, 32, (0, 1)), (1, 32, (7, 1)), (4, 1, (1, 0)), (0, 32, (0, 1)), (4, 32, (32, 1)), (4, 32, (40, 1))):
         assert sam._matrix(h.new_zeros(4096).as_strided((rows, cols), st), "X")[:2] == (rows, cols)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks what is said without a GPU")
+def test_a_single_row_has_any_stride():
+    """The last position of one long sequence: its stride is the sequence's length times K."""
+    far = 300 * 8192
+    assert forward(M=1, ldx=far) == DEVICE and forward(M=1, ldy=far) == DEVICE
+    assert backward(M=1, ldx=far) == DEVICE and backward(M=1, lddy=far) == DEVICE and backward(M=1, lddx=far) == DEVICE
+    assert forward(K=1, ldw=far) == DEVICE and forward(trans=1, N=1, ldw=far) == DEVICE
+    assert forward(M=2, ldx=far) == INVALID and forward(K=2, ldw=far) == INVALID and backward(M=2, lddy=far) == INVALID
+    assert forward(M=1, ldx=63) == INVALID and backward(M=1, lddy=63) == INVALID
+    b = [ctypes.c_uint64() for _ in range(3)]
+    for q, ld in zip(b, (64, 67, far)):   # no copy of it either
+        assert L.sam_adapter_gemm_workspace(sam.BF16, 0, 1, 64, 64, 2, 8, ld, 64, ctypes.byref(q)) == 0
+    assert b[0].value == b[1].value == b[2].value

@@ -265,3 +265,26 @@ def test_no_rows_over_any_length(K, N, dtype):
         dX, dA, dB = sam.adapter_backward(X.new_empty(0, N), X[:0], W, A, B, ids[:0], scale, need_dx=need_dx, **full)
         assert (dX.shape == (0, K)) if need_dx else dX is None
         assert dA is full["dA"] and dB is full["dB"] and not dA.any() and not dB.any()
+
+
+@pytest.mark.parametrize("K,N", [(520, 264), (777, 2049)])
+def test_the_last_position_of_one_sequence(K, N):
+    """One row with its sequence's stride, beyond what rows may be apart."""
+    X, W, A, B, ids, scale = make(1, K, N, 16, 3, "bf16", 17)
+    S = (1 << 21) // min(K, N) + 3
+    ids.fill_(1)
+    seq, dseq, out = (X.new_zeros(1, S, c) for c in (K, N, N))
+    seq[:, -1], dseq[:, -1] = X, torch.randn(1, N, generator=torch.Generator().manual_seed(3)).to(X.dtype).cuda()
+    if K % 8 == 0:   # operands start on 16 bytes
+        Y = sam.adapter_gemm(seq[:, -1], W, A, B, ids, scale)
+        assert torch.equal(Y, sam.adapter_gemm(X, W, A, B, ids, scale))
+        ref.close(Y, *ref.forward(X, W, A, B, ids, scale, False))
+        sam.adapter_gemm(X, W, A, B, ids, scale, Y=out[:, -1])
+        assert torch.equal(out[:, -1], sam.adapter_gemm(X, W, A, B, ids, scale, out_dtype=X.dtype)) and not out[:, :-1].any()
+        got = sam.adapter_backward(dseq[:, -1], seq[:, -1], W, A, B, ids, scale)
+    else:
+        wide = X.new_zeros(1, 1 << 22)
+        wide[:, :K] = X
+        got = sam.adapter_backward(dseq[:, -1].clone(), wide[:, :K], W, A, B, ids, scale)
+    for g, w in zip(got, sam.adapter_backward(dseq[:, -1].clone(), X, W, A, B, ids, scale)):
+        assert torch.equal(g, w)
