@@ -324,7 +324,8 @@ sam_status sam_adapter_gemm_workspace(sam_dtype dtype, sam_op trans_w,
  * and so may dA and dB together; what is not wanted is not computed. Rows
  * are added up in row order in chunks of a fixed size, and these in a fixed
  * order: the same bits every time. dA and dB take the intermediate whole
- * (SAM_BF16) or to 22 bits. Everything else as for sam_adapter_gemm. With M ==
+ * (SAM_BF16) or to 22 bits of the largest value that its rank has in a chunk
+ * (SAM_F16); Inf and NaN in one rank leave the others as they are. Everything else as for sam_adapter_gemm. With M ==
  * 0 dA and dB are zeros. */
 sam_status sam_adapter_backward(sam_dtype dtype, sam_op trans_w, int64_t M,
                                 int64_t N, int64_t K, int64_t n_adapters,

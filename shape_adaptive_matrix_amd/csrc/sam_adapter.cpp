@@ -87,7 +87,7 @@ struct Layout {
     bool pad_x, pad_w, pad_a, pad_b, pad_dy;
     long long lx, lw, la, lb, ldy; // row strides that the kernels see
     Region x, w, a, b, dy;         // padded copies
-    Region t32, t32b, t16, factor, factor2, part, order, seg, chunk_first, chunks, outer;
+    Region t32, t32b, t16, factor, part, order, seg, chunk_first, chunks, outer;
     int chunk, max_chunks;
     unsigned long long total;
 };
@@ -197,7 +197,6 @@ Layout layout(const Call& c)
             take(L.t32b, t * L.ksplit);
             take(L.t16, t / 2 * L.np);
             take(L.factor, 4ull * c.M);
-            take(L.factor2, 4ull * c.M);
             take(L.order, 4ull * (c.M + 1));
             take(L.seg, 4ull * (c.n + 1));
         }
@@ -304,7 +303,6 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
             if (c.want_ad) {
                 a.sides = 2;
                 a.side[1] = x;
-                a.side[1].factor = static_cast<float*>(at(L.factor2));
                 a.order = static_cast<int*>(at(L.order));
                 a.seg = static_cast<int*>(at(L.seg));
                 a.chunk = L.chunk;
@@ -384,10 +382,9 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
         o.chunk_first = a.chunk_first;
         o.chunks = a.chunks;
         float* part = static_cast<float*>(at(L.outer));
-        o.side[0] = {static_cast<const float*>(at(L.t32b)), static_cast<const float*>(at(L.factor)), p.X, L.lx, (int)c.K,
-                     p.dA, part};
-        o.side[1] = {static_cast<const float*>(at(L.t32)), static_cast<const float*>(at(L.factor2)), p.dY, L.ldy, (int)c.N,
-                     p.dB, part + (long long)L.max_chunks * c.r * c.K};
+        o.side[0] = {static_cast<const float*>(at(L.t32b)), p.X, L.lx, (int)c.K, p.dA, part};
+        o.side[1] = {static_cast<const float*>(at(L.t32)), p.dY, L.ldy, (int)c.N, p.dB,
+                     part + (long long)L.max_chunks * c.r * c.K};
         e = launch_adapter_outer(c.dtype, o, finish ? &f : nullptr, s);
     } else if (e == hipSuccess && finish) {
         e = launch_adapter_finish(c.dtype, f, s);

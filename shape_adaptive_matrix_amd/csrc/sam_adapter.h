@@ -96,7 +96,6 @@ struct AdapterRingArgs {
 // of T[m][i] X[m][c].
 struct OuterSide {
     const float* t32;    // [M][rp], scaled
-    const float* factor; // [M]: a power of two at most twice the row's largest value from it
     const void* X;
     long long ldx;
     int cols;

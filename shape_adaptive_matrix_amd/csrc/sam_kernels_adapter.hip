@@ -53,9 +53,8 @@ __device__ __forceinline__ void split3_bits(float v, unsigned short (&o)[3])
 constexpr int kShrinkWaves = 4, kWideRows = 64;
 
 // Rounds a row of T, held by LANES threads (column c0 + LANES q): divides by
-// the power of two below the row's largest value. A row of zeros gets the
-// smallest one (it then never sets the scale of rows that are added up with
-// it), one with Inf or NaN gets 1.
+// the power of two below the row's largest value. One with Inf or NaN gets 1:
+// nothing finite comes of it.
 template <int DT, int NQ, int LANES>
 __device__ __forceinline__ void round_row(const ShrinkArgs& a, const ShrinkSide& sd, const float (&t)[NQ], long long m,
                                           int c0, bool mine)
@@ -470,9 +469,9 @@ constexpr int kOuterCols = 256;
 // registers into LDS (their order is the grouping's, so each lane has its own
 // address) and are read with the transposing LDS read; T is split into 16-bit
 // values, an MFMA each, and read the same way. bfloat16: three values, exactly
-// T. binary16: T divided by a power of two common to the chunk (from the rows'
-// factors, so that the type's range keeps it), a value and its remainder, the
-// sum right to 2^-22 of the chunk's largest.
+// T. binary16: each rank's T divided by a power of two of its own, the largest
+// finite T of the rank in the chunk (read once ahead for that), a value and its
+// remainder: right to 2^-22 of that largest, whatever the other ranks hold.
 // Bound by reading X once. Measured at X, dY 4096 x 4096, rank 16, 8
 // adapters in runs, both gradients: 18 us with loads two steps ahead, 22.6 one
 // step ahead, 14 with all of it but the loads.
@@ -489,7 +488,6 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
     constexpr int TROW = NP * RP + (NP * RP % 64 == 0 ? 8 : 0);
     constexpr int XB = 32 * kOuterCols * 2, TB = 32 * TROW * 2;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[2][XB + TB];
-    __shared__ float fmax_s[4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int strips0 = (a.side[0].cols + kOuterCols - 1) / kOuterCols;
@@ -504,19 +502,6 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
     const int* order = a.order + w.y;
     const bool run = row0 >= 0;
 
-    // The chunk's scale: the largest of its rows' factors.
-    int e = 0;
-    if constexpr (DT == DT_F16) {
-        float big = 0.0f;
-        for (int m = tid; m < rows; m += 256) big = fmaxf(big, sd.factor[order[m]]);
-#pragma unroll
-        for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
-        if (lane == 0) fmax_s[wave] = big;
-        __syncthreads();
-        big = fmaxf(fmaxf(fmax_s[0], fmax_s[1]), fmaxf(fmax_s[2], fmax_s[3]));
-        if (rows) e = ilogbf(big);   // factors are powers of two, at least 2^-126
-    }
-
     // Loads of step s into one of two register sets: X 32 rows x 512 bytes,
     // four 16-byte pieces a thread; T 32 rows x RP floats, RP / 8 a thread.
     // None sits behind a condition (the compiler could not count how many
@@ -528,6 +513,8 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
         u4 x[4];
         float t[TP];
     };
+    __shared__ float largest[4][DT == DT_F16 ? RP : 1];
+    __shared__ int exponent[DT == DT_F16 ? RP : 1];   // of each rank's scale
     Set set[2];
     int next_row = 0;   // of the next step to load, row lane % 32
     const int trow = tid >> 3, tc = (tid & 7) * TP;
@@ -567,7 +554,7 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
                 if constexpr (NP == 3)
                     split3_bits(t, h[k]);
                 else
-                    split_bits<DT>(ldexpf(t, -e), h[k][0], h[k][1]);
+                    split_bits<DT>(ldexpf(t, -exponent[tc + q + k]), h[k][0], h[k][1]);
             }
 #pragma unroll
             for (int k = 0; k < NP; ++k)
@@ -615,10 +602,60 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
     // A step's values are in LDS from its `put` to the barrier after the next
     // one's: two buffers, one barrier a step.
     const int steps = (rows + 31) / 32;
-    if (steps) {
+    auto fill = [&] {
+        if (!steps) return;
         next_row = order[min(lane & 31, rows - 1)];
         load(0, set[0]);
         load(1, set[1]);
+    };
+    if constexpr (DT == DT_F16) {
+        // The ranks' exponents: a thread has four ranks of every R-th row, U of
+        // them under way at once, the first ones ahead of the steps' loads. Not
+        // seen up to rank 32; with 256 rows of 64 ranks 4.6 us of 36 (4096 x
+        // 4096 and 4096 x 4096, rank 64, both gradients).
+        constexpr int LR = RP / 4, R = 256 / LR, U = RP <= 32 ? 4 : 16;
+        const int rank = tid % LR * 4;
+        float4 v[U] = {};
+        float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto peek = [&](int m) {   // rows past the end: the last one again; no load waits for another
+            const float* p = sd.t32 + rank;
+            if (run) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    v[u] = *reinterpret_cast<const float4*>(p + (long long)(row0 + min(m + u * R + tid / LR, rows - 1)) * RP);
+            } else {
+                int o[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) o[u] = order[min(m + u * R + tid / LR, rows - 1)];
+#pragma unroll
+                for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const float4*>(p + (long long)o[u] * RP);
+            }
+        };
+        if (rows) peek(0);
+        fill();
+        for (int m = 0; m < rows; m += U * R) {
+            if (m) peek(m);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float t[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) big[q] = fabsf(t[q]) < INFINITY ? fmaxf(big[q], fabsf(t[q])) : big[q];
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int d = LR; d < 64; d <<= 1) big[q] = fmaxf(big[q], __shfl_xor(big[q], d));
+            if (lane < LR) largest[wave][rank + q] = big[q];
+        }
+        __syncthreads();
+        if (tid < RP) {
+            const float t = fmaxf(fmaxf(largest[0][tid], largest[1][tid]), fmaxf(largest[2][tid], largest[3][tid]));
+            exponent[tid] = t > 0.0f ? max(ilogbf(t), -126) : -126;
+        }
+        __syncthreads();
+    } else {
+        fill();
     }
     int s = 0;
     for (; s + 2 < steps; s += 2)
@@ -638,13 +675,14 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
     }
     const bool direct = a.chunk_first[ad + 1] - a.chunk_first[ad] == 1;
     float* o = direct ? sd.out + (long long)ad * a.r * sd.cols : sd.part + (long long)ch * a.r * sd.cols;
-    const float back = ldexpf(1.0f, e);
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int row = 16 * i + 4 * grp + v;
             if (row >= a.r) continue;
+            float back = 1.0f;
+            if constexpr (DT == DT_F16) back = ldexpf(1.0f, exponent[row]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int c = c0 + wave * 64 + 16 * j + s16;

@@ -288,3 +288,51 @@ def test_the_last_position_of_one_sequence(K, N):
         got = sam.adapter_backward(dseq[:, -1].clone(), wide[:, :K], W, A, B, ids, scale)
     for g, w in zip(got, sam.adapter_backward(dseq[:, -1].clone(), X, W, A, B, ids, scale)):
         assert torch.equal(g, w)
+
+
+def far_ranks(M, K, N, r, n, dtype, seed):
+    """Small integers, each rank of A and B times a power of two of its own
+    between 2^10 and 2^-14: T and the adapters' gradients are exact in FP32 (a
+    rank's T are at most 2^10 multiples of its power), and the ranks' sizes
+    are 24 bits apart."""
+    g = torch.Generator().manual_seed(seed)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=g).double()  # noqa: E731
+    by = 2.0 ** torch.linspace(10, -14, r).round().double()[None, :, None]
+    X, W, A, B, dY = ints(M, K), ints(K, N), ints(n, r, K) * by, ints(n, r, N) * by.flip(1), ints(M, N)
+    ids = torch.randint(-1, n, (M,), generator=g, dtype=torch.int32).cuda()
+    X, W, A, B, dY = (t.to(TYPES[dtype]).cuda() for t in (X, W, A, B, dY))
+    return X, W, A, B, ids, torch.tensor([1.0, 2.0, -0.5], device="cuda")[:n], dY
+
+
+def exact_gradients(X, W, A, B, ids, scale, dY):
+    """dA and dB in 64 bits, where they are finite (the library's FP32 values exactly)."""
+    (_, (dA, _), (dB, _)) = ref.backward(dY, X, W, A, B, ids, scale, False)
+    return dA, dB
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(16, 96, 80, 8, 3), (100, 520, 264, 3, 2), (700, 96, 80, 24, 3), (5000, 200, 40, 40, 2),
+                                   (3000, 72, 104, 128, 1)], ids=str)
+def test_gradients_of_ranks_far_apart(shape, dtype):
+    """A rank's gradient is as exact next to much larger ranks as alone."""
+    args = far_ranks(*shape, dtype, 3)
+    dA, dB = exact_gradients(*args)
+    _, gA, gB = sam.adapter_backward(args[-1], *args[:-1])
+    assert dA.abs().amax(2).min() > 0 and dB.abs().amax(2).min() > 0
+    assert torch.equal(gA.double(), dA) and torch.equal(gB.double(), dB)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(40, 96, 80, 8, 3), (700, 96, 80, 24, 3), (5000, 200, 40, 40, 3)], ids=str)
+def test_inf_and_nan_of_one_rank_stay_in_it(shape, dtype):
+    """A's rank makes a row of dB Inf or NaN, B's a row of dA: the other ranks keep their bits."""
+    X, W, A, B, ids, scale, dY = far_ranks(*shape, dtype, 4)
+    dA, dB = exact_gradients(X, W, A, B, ids, scale, dY)
+    A[1, 2, 5], B[2, 4, 7], A[2, 1, 0] = float("inf"), float("nan"), float("-inf")
+    _, gA, gB = sam.adapter_backward(dY, X, W, A, B, ids, scale)
+    for got, want, gone in ((gB, dB, [(1, 2), (2, 1)]), (gA, dA, [(2, 4)])):
+        keep = torch.ones(want.shape[:2], dtype=torch.bool, device="cuda")
+        for a, i in gone:
+            keep[a, i] = False
+            assert not torch.isfinite(got[a, i]).any()
+        assert torch.equal(got[keep].double(), want[keep])
