@@ -87,8 +87,8 @@ struct Layout {
     bool pad_x, pad_w, pad_a, pad_b, pad_dy;
     long long lx, lw, la, lb, ldy; // row strides that the kernels see
     Region x, w, a, b, dy;         // padded copies
-    Region t32, t32b, t16, factor, part, order, seg, chunk_first, chunks, outer;
-    int chunk, max_chunks;
+    Region t32, t32b, t16, factor, part, order, seg, chunk_first, part_first, chunks, outer;
+    int chunk, max_chunks, max_parts;
     unsigned long long total;
 };
 
@@ -212,7 +212,12 @@ Layout layout(const Call& c)
         while (chunk < (1 << 20) && (c.M / (2 * chunk)) * strips >= 2 * kCUs) chunk *= 2;
         L.chunk = (int)chunk;
         L.max_chunks = (int)((c.M + chunk - 1) / chunk + c.n);
-        take(L.outer, 4ull * L.max_chunks * c.r * (c.K + c.N));
+        // Partials: of adapters with more than `chunk` rows, of which there are
+        // no more than M / (chunk + 1); the others' sums are results at once.
+        const long long several = c.M / (chunk + 1);
+        L.max_parts = (int)(several ? c.M / chunk + (several < c.n ? several : c.n) : 0);
+        take(L.outer, 4ull * L.max_parts * c.r * (c.K + c.N));
+        take(L.part_first, 4ull * c.n);
         take(L.chunk_first, 4ull * (c.n + 1));
         take(L.chunks, 16ull * (L.max_chunks + 1));
     }
@@ -308,6 +313,7 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
                 a.chunk = L.chunk;
                 a.max_chunks = L.max_chunks;
                 a.chunk_first = static_cast<int*>(at(L.chunk_first));
+                a.part_first = static_cast<int*>(at(L.part_first));
                 a.chunks = static_cast<int4*>(at(L.chunks));
             }
         }
@@ -380,11 +386,12 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
         o.chunk = L.chunk;
         o.max_chunks = L.max_chunks;
         o.chunk_first = a.chunk_first;
+        o.part_first = a.part_first;
         o.chunks = a.chunks;
         float* part = static_cast<float*>(at(L.outer));
         o.side[0] = {static_cast<const float*>(at(L.t32b)), p.X, L.lx, (int)c.K, p.dA, part};
         o.side[1] = {static_cast<const float*>(at(L.t32)), p.dY, L.ldy, (int)c.N, p.dB,
-                     part + (long long)L.max_chunks * c.r * c.K};
+                     part + (long long)L.max_parts * c.r * c.K};
         e = launch_adapter_outer(c.dtype, o, finish ? &f : nullptr, s);
     } else if (e == hipSuccess && finish) {
         e = launch_adapter_finish(c.dtype, f, s);

@@ -50,6 +50,7 @@ struct ShrinkArgs {
     int chunk;           // rows per chunk
     int max_chunks;      // ceil(M / chunk) + n
     int* chunk_first;    // [n + 1] each adapter's first chunk
+    int* part_first;     // [n] ... and its first place among the partials, which adapters with several chunks have
     int4* chunks;        // [max_chunks] adapter (-1: no such chunk), place in `order`, rows, first row of a run or -1
 };
 
@@ -100,7 +101,7 @@ struct OuterSide {
     long long ldx;
     int cols;
     float* out;          // [n][r][cols]
-    float* part;         // [chunks][r][cols], chunks of adapters that have more than one
+    float* part;         // [][r][cols]: the chunks of adapters that have more than one, in adapter order
 };
 
 struct OuterArgs {
@@ -109,6 +110,7 @@ struct OuterArgs {
     const int* order;
     int chunk, max_chunks;   // as in ShrinkArgs
     const int* chunk_first;
+    const int* part_first;
     const int4* chunks;
 };
 

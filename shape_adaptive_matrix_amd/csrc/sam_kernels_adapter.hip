@@ -248,39 +248,52 @@ __global__ void __launch_bounds__(kShrinkWaves * 64) adapter_shrink_wide_kernel(
 }
 
 // The adapters' rows cut into chunks of a.chunk, numbered in adapter order:
-// where each adapter's chunks start, and each chunk's place. One workgroup,
+// where each adapter's chunks start, and each chunk's place; of adapters with
+// several chunks also where their partials start. One workgroup,
 // 256 adapters at a time; a thread has every 256th of their chunks (65536 rows
 // of one adapter, 512 chunks: 4.6 us; with an adapter's chunks on one thread
 // 170).
 __device__ __forceinline__ void list_chunks(const ShrinkArgs& a)
 {
-    __shared__ int sums[4], firsts[256], begins[257];
+    __shared__ int sums[2][4], firsts[256], begins[257];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int base = 0;
+    int base = 0, parts = 0;
     for (int a0 = 0; a0 < a.n; a0 += 256) {
         const int ad = a0 + tid;
         const int begin = a.seg[min(ad, a.n)], rows = a.seg[min(ad + 1, a.n)] - begin;
         const int count = ad < a.n ? max((rows + a.chunk - 1) / a.chunk, 1) : 0;   // without rows: one that gives zeros
-        int sum = count;
+        const int several = count > 1 ? count : 0;
+        int sum = count, psum = several;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(sum, d);
-            if (lane >= d) sum += o;
+            const int o = __shfl_up(sum, d), p = __shfl_up(psum, d);
+            if (lane >= d) {
+                sum += o;
+                psum += p;
+            }
         }
         __syncthreads();   // the last step's values are read
-        if (lane == 63) sums[wave] = sum;
+        if (lane == 63) {
+            sums[0][wave] = sum;
+            sums[1][wave] = psum;
+        }
         begins[tid] = begin;
         if (tid == 255) begins[256] = begin + rows;
         __syncthreads();
         const int from = base;
-        int first = base + sum - count;
+        int first = base + sum - count, part = parts + psum - several;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            first += w < wave ? sums[w] : 0;
-            base += sums[w];
+            first += w < wave ? sums[0][w] : 0;
+            part += w < wave ? sums[1][w] : 0;
+            base += sums[0][w];
+            parts += sums[1][w];
         }
         firsts[tid] = first;   // past the last adapter: `base`, as it is now
-        if (ad < a.n) a.chunk_first[ad] = first;
+        if (ad < a.n) {
+            a.chunk_first[ad] = first;
+            a.part_first[ad] = part;
+        }
         __syncthreads();
         for (int c = from + tid; c < base; c += 256) {
             int of = 0;   // the last adapter whose chunks start at c or before
@@ -673,8 +686,9 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
         __syncthreads();
         multiply(s + h);
     }
-    const bool direct = a.chunk_first[ad + 1] - a.chunk_first[ad] == 1;
-    float* o = direct ? sd.out + (long long)ad * a.r * sd.cols : sd.part + (long long)ch * a.r * sd.cols;
+    const int first_ch = a.chunk_first[ad], part = a.part_first[ad] + ch - first_ch;
+    const bool direct = a.chunk_first[ad + 1] - first_ch == 1;
+    float* o = (direct ? sd.out : sd.part) + (long long)(direct ? ad : part) * a.r * sd.cols;
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
@@ -730,13 +744,13 @@ __global__ void __launch_bounds__(256) adapter_outer_sum_kernel(OuterArgs a)
     const int b0 = (int)((v0 + V - 1) / V), b1 = (int)((v1 + V - 1) / V);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ad = (int)(blockIdx.x / (unsigned)(b0 + b1)), b = (int)(blockIdx.x % (unsigned)(b0 + b1));
-    const int first = a.chunk_first[ad], count = a.chunk_first[ad + 1] - first;
+    const int count = a.chunk_first[ad + 1] - a.chunk_first[ad];
     if (count == 1) return;
     const bool second = b >= b0;
     const OuterSide& sd = a.side[second];
     const long long vals = second ? v1 : v0;
     const long long at = (long long)(second ? b - b0 : b) * V + (WS == 4 ? 0 : wave * 256) + lane;
-    const float* part = sd.part + (long long)first * vals;
+    const float* part = sd.part + (long long)a.part_first[ad] * vals;
     const int begin = WS == 4 ? (int)((long long)count * wave / 4) : 0;
     const int end = WS == 4 ? (int)((long long)count * (wave + 1) / 4) : count;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -188,3 +188,14 @@ def test_a_single_row_has_any_stride():
     for q, ld in zip(b, (64, 67, far)):   # no copy of it either
         assert L.sam_adapter_gemm_workspace(sam.BF16, 0, 1, 64, 64, 2, 8, ld, 64, ctypes.byref(q)) == 0
     assert b[0].value == b[1].value == b[2].value
+
+
+@pytest.mark.parametrize("M,n,parts", [(64, 1000, 0), (128, 4, 0), (1025, 1000, 31), (1025, 3, 19), (5000, 50000, 154)])
+def test_partials_for_adapters_that_have_them(M, n, parts):
+    """dA and dB of an adapter with no more rows than a chunk (64, or all of up
+    to 128) are written at once: partials do not grow with the adapters."""
+    K, N, r = 1024, 1024, 16
+    b = ctypes.c_uint64()
+    assert L.sam_adapter_backward_workspace(sam.BF16, 0, M, N, K, n, r, N, K, N, 0, 1, ctypes.byref(b)) == 0
+    rest = 2 * 4 * M * r * 32 + 3 * 2 * M * r + 4 * (4 * n + 8 * M) + 16 * (M // 64 + n) + (1 << 16)   # T's sums, lists
+    assert b.value <= parts * 4 * r * (K + N) + rest

@@ -336,3 +336,22 @@ def test_inf_and_nan_of_one_rank_stay_in_it(shape, dtype):
             keep[a, i] = False
             assert not torch.isfinite(got[a, i]).any()
         assert torch.equal(got[keep].double(), want[keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_partials_stay_in_the_workspace(dtype):
+    """As many adapters with two chunks as there can be (65 rows each), others
+    with one or none, in a workspace of just the size that the library asks for."""
+    M, K, N, r, n = 5000, 264, 136, 16, 90
+    X, W, A, B, ids, scale = make(M, K, N, r, n, dtype, 19)
+    g = torch.Generator().manual_seed(20)
+    ids = (torch.arange(M, dtype=torch.int32) // 65)[torch.randperm(M, generator=g)].cuda()   # 77 adapters
+    dY = torch.randn(M, N, generator=g).to(X.dtype).cuda()
+    code = sam.BF16 if dtype == "bf16" else sam.F16
+    need = sam._adapter_workspace_bytes("sam_adapter_backward_workspace", code, 0, M, N, K, n, r, N, K, N, 1, 1)
+    whole = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    got = sam.adapter_backward(dY, X, W, A, B, ids, scale, workspace=whole[:need])
+    for x, w, name in zip(got, ref.backward(dY, X, W, A, B, ids, scale, False), ("dX", "dA", "dB")):
+        ref.close(x, *w, name)
+    assert (whole[need:] == 77).all()
+    assert not got[1][77:].any() and not got[2][77:].any()
