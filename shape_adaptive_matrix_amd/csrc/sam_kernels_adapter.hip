@@ -623,10 +623,11 @@ __device__ __forceinline__ void outer_tile(const OuterArgs& a, int block)
     };
     if constexpr (DT == DT_F16) {
         // The ranks' exponents: a thread has four ranks of every R-th row, U of
-        // them under way at once, the first ones ahead of the steps' loads. Not
-        // seen up to rank 32; with 256 rows of 64 ranks 4.6 us of 36 (4096 x
-        // 4096 and 4096 x 4096, rank 64, both gradients).
-        constexpr int LR = RP / 4, R = 256 / LR, U = RP <= 32 ? 4 : 16;
+        // them under way at once, the first ones ahead of the steps' loads.
+        // Chunks of 64 rows: not seen (1025 rows, 768 x 2049, rank 24, both
+        // gradients 32.4 us with and without); of 256 rows of 4096 x 4096 0 us
+        // at rank 16, 2.3 of 54 at 32, 4.6 of 79 at 64.
+        constexpr int LR = RP / 4, R = 256 / LR, U = RP == 16 ? 4 : (RP == 32 ? 2 : 16);
         const int rank = tid % LR * 4;
         float4 v[U] = {};
         float big[4] = {0.0f, 0.0f, 0.0f, 0.0f};
