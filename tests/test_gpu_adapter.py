@@ -355,3 +355,57 @@ def test_partials_stay_in_the_workspace(dtype):
         ref.close(x, *w, name)
     assert (whole[need:] == 77).all()
     assert not got[1][77:].any() and not got[2][77:].any()
+
+
+# Split products (their partials added) and whole tiles with the term inside.
+WHOLE = [(6, 64, 136, 8, 3), (20, 512, 264, 24, 2), (100, 264, 80, 16, 5), (300, 128, 520, 40, 3), (2100, 64, 264, 128, 2)]
+
+
+def fits_two_values(t):
+    """Whether rounding to two bfloat16 values would keep every one of t."""
+    hi = t.to(torch.bfloat16).double()
+    return torch.equal(hi + (t - hi).to(torch.bfloat16).double(), t)
+
+
+def large_and_sparse(shape, dtype, seed):
+    M, K, N, r, n = shape
+    g = torch.Generator().manual_seed(seed)
+    large = lambda *s: torch.randint(0, 128, s, generator=g).to(TYPES[dtype]).cuda()  # noqa: E731
+    unit = lambda p, *s: ((torch.rand(*s, generator=g) < p) * (1 - 2 * torch.randint(0, 2, s, generator=g))).to(TYPES[dtype]).cuda()  # noqa: E731
+    return large, unit, torch.randint(-1, n, (M,), generator=g, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", WHOLE, ids=str)
+def test_fp32_results_take_the_intermediate_whole(shape, dtype):
+    """T of 18 to 21 bits, and every sum exact in FP32: bfloat16 keeps T whole
+    in an FP32 result, binary16 22 bits of the row's largest."""
+    M, K, N, r, n = shape
+    large, unit, ids = large_and_sparse(shape, dtype, 5)
+    X, W, A = large(M, K), unit(0.5, K, N), large(n, r, K)
+    B = torch.zeros(n, r, N, dtype=X.dtype, device="cuda")
+    at = torch.arange(N, device="cuda")
+    B[:, at % r, at] = 1 - 2 * (at // r % 2).to(X.dtype)     # a column takes one rank
+    t = X.double() @ A[0].double().t()
+    assert t.max() < 2 ** 22 and not fits_two_values(t)
+    for trans_w in (False, True):
+        Y = sam.adapter_gemm(X, W.t().contiguous() if trans_w else W, A, B, ids, trans_w=trans_w)
+        want = ref.forward(X, W, A, B, ids, None, False)[0]
+        assert want.abs().max() < 2 ** 24
+        assert torch.equal(Y.double(), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", WHOLE, ids=str)
+def test_gradients_take_the_intermediate_whole(shape, dtype):
+    """As above: T of X under dB, T of dY under dA."""
+    M, K, N, r, n = shape
+    large, unit, ids = large_and_sparse(shape, dtype, 6)
+    W, A, B = unit(0.5, K, N), large(n, r, K), large(n, r, N)
+    for X, dY, side in ((large(M, K), unit(2 / M, M, N), 2), (unit(2 / M, M, K), large(M, N), 1)):
+        left, P, right = (X, A, dY) if side == 2 else (dY, B, X)
+        t = left.double() @ P[0].double().t()
+        assert t.max() < 2 ** 22 and not fits_two_values(t)
+        assert (t.max() * right.double().abs().sum(0)).max() < 2 ** 24
+        got = sam.adapter_backward(dY, X, W, A, B, ids, need_dx=False)
+        assert torch.equal(got[side].double(), ref.backward(dY, X, W, A, B, ids, None, False)[side][0])
