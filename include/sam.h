@@ -273,7 +273,9 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  * and only X[m] W where ids[m] names no adapter (any value outside 0 ..
  * n_adapters - 1, -1 by custom). Rows may come in any order; rows of one
  * request next to each other cost least. What another request's adapter
- * holds (Inf and NaN too) never reaches a row.
+ * holds (Inf and NaN too) never reaches a row. Inf and NaN of a row's own
+ * operands go where the formulas take them and no further; an Inf of theirs
+ * may come out as NaN, which depends on the sizes.
  *   dtype   SAM_BF16 or SAM_F16: X, W, A and B.
  *   X       device, M rows of K values, row stride ldx >= K.
  *   W       device, K rows of N values (trans_w SAM_OP_N, ldw >= N) or N rows

@@ -9,9 +9,11 @@
 // remainders, so T counts with 2^-17 (bf16) or 2^-22 (f16) relative to its
 // row's largest value, not with 2^-9 or 2^-12; an FP32 result of bf16 takes
 // a third, T exactly) and B[a]'s rows in LDS. Measured at 4096 x 11008 x 4096,
-// rank 64: 12 us of 290; 256 x 4096 x 11008, rank 32: 5 of 46. Each row was divided by a power of two before it was rounded, so that binary16
-// neither overflows nor loses small rows; the accumulators are multiplied by
-// it before the K loop starts.
+// rank 64: 12 us of 290; 256 x 4096 x 11008, rank 32: 5 of 46. Each row was
+// divided by a power of two before it was rounded, so that binary16 neither
+// overflows nor loses small rows; the accumulators are multiplied by it before
+// the K loop starts. An Inf in a row's own B meets T's values one by one (one
+// of them may be 0, or of the other sign) and may come out as NaN.
 #include "sam_adapter.h"
 #include "sam_adapter_shrink.h"
 #include "sam_ring16.h"

@@ -409,3 +409,47 @@ def test_gradients_take_the_intermediate_whole(shape, dtype):
         assert (t.max() * right.double().abs().sum(0)).max() < 2 ** 24
         got = sam.adapter_backward(dY, X, W, A, B, ids, need_dx=False)
         assert torch.equal(got[side].double(), ref.backward(dY, X, W, A, B, ids, None, False)[side][0])
+
+
+# Split products and whole tiles, narrow and wide.
+@pytest.mark.parametrize("out", ["f32", "same"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(20, 512, 264, 8, 3), (40, 2048, 384, 40, 3), (300, 128, 520, 16, 3), (2049, 72, 4104, 16, 3)],
+                         ids=str)
+def test_inf_goes_where_the_formulas_take_it(shape, dtype, out):
+    """Inf (NaN too, for parts of T are multiplied one by one) where the
+    definition has Inf or NaN, and the other results' bits as without it."""
+    M, K, N, r, n = shape
+    X, W, A, B, ids, scale = make(M, K, N, r, n, dtype, 27, runs=False)
+    ids[:n] = torch.arange(n, dtype=torch.int32)
+    dY = (torch.randn(M, N, generator=torch.Generator().manual_seed(8)) * 0.1).to(X.dtype).cuda()
+    to = X.dtype if out == "same" else None
+
+    def results(X, A, B):
+        return (sam.adapter_gemm(X, W, A, B, ids, scale, out_dtype=to),
+                *sam.adapter_backward(dY, X, W, A, B, ids, scale, out_dtype=to))
+
+    def check(got, clean, gone):
+        for g, c, at, name in zip(got, clean, gone, ("Y", "dX", "dA", "dB")):
+            lost = torch.zeros(g.shape, dtype=torch.bool, device="cuda")
+            if at is not None:
+                lost[at] = True
+            assert not torch.isfinite(g[lost]).any(), name
+            assert torch.equal(g[~lost], c[~lost]), name
+
+    clean = results(X, A, B)
+    assert all(torch.isfinite(c).all() for c in clean)
+    mine = (ids == 1)[:, None]
+    # A row of B: column 5 of its rows, and through dY B^T their dX and the rank's dA.
+    B2, col, rank = B.clone(), torch.arange(N, device="cuda") == 5, torch.zeros(n, r, 1, dtype=torch.bool, device="cuda")
+    B2[1, 2, 5], rank[1, 2] = float("inf"), True
+    check(results(X, A, B2), clean, (mine & col, mine.expand(M, K), rank.expand(n, r, K), None))
+    # A row of A: all of its rows of Y, column 5 of dX, the rank's dB.
+    A2, col = A.clone(), torch.arange(K, device="cuda") == 5
+    A2[1, 2, 5] = float("-inf")
+    check(results(X, A2, B), clean, (mine.expand(M, N), mine & col, None, rank.expand(n, r, N)))
+    # A row of X: its Y, column 5 of its adapter's dA, all of its dB.
+    X2, whole = X.clone(), torch.zeros(n, 1, 1, dtype=torch.bool, device="cuda")
+    X2[1, 5], whole[1] = float("inf"), True
+    row = (torch.arange(M, device="cuda") == 1)[:, None]
+    check(results(X2, A, B), clean, (row.expand(M, N), None, (whole & col).expand(n, r, K), whole.expand(n, r, N)))
