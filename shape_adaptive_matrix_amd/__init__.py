@@ -249,10 +249,21 @@ def _operands(A, B, dtype):
     return code
 
 
-def _output(C, M, N, others, names, workspace=None):
+def _new(shape, dtype, device, stream):
+    """A result of a call on `stream` (torch's current stream when None), from
+    that stream's memory: another stream's work may still be using what the
+    caching allocator would hand out on it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(C, M, N, others, names, workspace=None, stream=None):
     """Checks, before anything reaches the library, that the caller's C is a
     compact float32 [M][N] matrix and that C, the workspace and the operands
-    (`others`) all live on one GPU; returns C, or a new one on that GPU."""
+    (`others`) all live on one GPU; returns C, or a new one on that GPU (_new)."""
     import torch
     if C is not None:
         if C.dtype != torch.float32:
@@ -265,7 +276,7 @@ def _output(C, M, N, others, names, workspace=None):
         raise ValueError("workspace must be contiguous")
     dev = _on_device((*others, C, workspace), (*names, "C", "workspace"))
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float32, device=dev)
+        C = _new((M, N), torch.float32, dev, stream)
     return C
 
 
@@ -294,7 +305,7 @@ def gemm(A, B, C=None, dtype=None, workspace=None, stream=None):
     code = _operands(A, B, dtype)
     M, K = A.shape
     N = B.shape[1]
-    C = _output(C, M, N, (A, B), ("A", "B"), workspace)
+    C = _output(C, M, N, (A, B), ("A", "B"), workspace, stream)
     p = plan(M, N, K, code)
     if workspace is None:
         workspace = workspace_for(p, A.device, stream)
@@ -311,7 +322,7 @@ def gemm_variant(vid: int, A, B, C=None, split_k: int = 0, dtype=None, workspace
     code = _operands(A, B, dtype)
     M, K = A.shape
     N = B.shape[1]
-    C = _output(C, M, N, (A, B), ("A", "B"), workspace)
+    C = _output(C, M, N, (A, B), ("A", "B"), workspace, stream)
     p = variant_plan(vid, M, N, K, code, split_k, raster)
     if workspace is None:
         workspace = workspace_for(p, A.device, stream)
@@ -331,7 +342,7 @@ def gemm_noalloc(A, B, C=None, dtype=None, stream=None):
     code = _operands(A, B, dtype)
     M, K = A.shape
     N = B.shape[1]
-    C = _output(C, M, N, (A, B), ("A", "B"))
+    C = _output(C, M, N, (A, B), ("A", "B"), stream=stream)
     _check(lib().sam_gemm_noalloc(code, _ptr(A), _ptr(B), _ptr(C), M, N, K, _stream_ptr(stream)))
     return C
 
@@ -382,7 +393,7 @@ def gemm_ex(A, B, C=None, trans_a=False, trans_b=False, alpha=1.0, beta=0.0, dty
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs C")
-        C = torch.empty((M, N), dtype=torch.float32, device=dev)
+        C = _new((M, N), torch.float32, dev, stream)
     if tuple(C.shape) != (M, N) or C.dtype != torch.float32:
         raise ValueError(f"C must be float32 [{M}, {N}]")
     ldc = _rows(C, "C")
@@ -420,7 +431,7 @@ def gemm_mxfp8(A, SA, Bt, SB, fmt_a="e4m3", fmt_b="e4m3", C=None, workspace=None
     device; returns C [M][N] FP32."""
     import torch
     M, N, K, fa, fb = _mx_operands(A, SA, Bt, SB, fmt_a, fmt_b)
-    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace)
+    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace, stream)
     if workspace is None:
         workspace = workspace_for(plan(M, N, K, MXFP8), A.device, stream)
     ws_bytes = _workspace_bytes(workspace)
@@ -434,7 +445,7 @@ def gemm_mxfp8_variant(vid: int, A, SA, Bt, SB, fmt_a="e4m3", fmt_b="e4m3", C=No
     """gemm_mxfp8 with a forced variant and split (0 = the variant's pick)."""
     import torch
     M, N, K, fa, fb = _mx_operands(A, SA, Bt, SB, fmt_a, fmt_b)
-    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace)
+    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace, stream)
     p = variant_plan(vid, M, N, K, MXFP8, split_k)
     if workspace is None:
         workspace = workspace_for(p, A.device, stream)
@@ -463,7 +474,7 @@ def gemm_mxfp4(A, SA, Bt, SB, C=None, workspace=None, stream=None):
     [N][K/32] E8M0 scale codes, all uint8 on the device; returns C [M][N] FP32."""
     import torch
     M, N, K = _mx4_operands(A, SA, Bt, SB)
-    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace)
+    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace, stream)
     if workspace is None:
         workspace = workspace_for(plan(M, N, K, MXFP4), A.device, stream)
     ws_bytes = _workspace_bytes(workspace)
@@ -476,7 +487,7 @@ def gemm_mxfp4_variant(vid: int, A, SA, Bt, SB, C=None, split_k: int = 0, worksp
     """gemm_mxfp4 with a forced variant and split (0 = the variant's pick)."""
     import torch
     M, N, K = _mx4_operands(A, SA, Bt, SB)
-    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace)
+    C = _output(C, M, N, (A, SA, Bt, SB), ("A", "scale_a", "Bt", "scale_b"), workspace, stream)
     p = variant_plan(vid, M, N, K, MXFP4, split_k)
     if workspace is None:
         workspace = workspace_for(p, A.device, stream)
@@ -551,7 +562,7 @@ def _adapter_operands(X, W, A, B, ids, scale, trans_w):
     return BF16 if dt == torch.bfloat16 else F16, M, N, K, n, rank, ldx, ldw
 
 
-def _adapter_result(Y, rows, cols, out_dtype, like, code, name):
+def _adapter_result(Y, rows, cols, out_dtype, like, code, name, stream):
     """The result tensor (given or new), its type code and row stride."""
     import torch
     if Y is not None:
@@ -565,7 +576,7 @@ def _adapter_result(Y, rows, cols, out_dtype, like, code, name):
     out = F32 if out_dtype == torch.float32 else code
     if Y is None:
         shape = (rows, cols)
-        Y = like.new_empty(shape) if out == code else torch.empty(shape, dtype=torch.float32, device=like.device)
+        Y = like.new_empty(shape) if out == code and stream is None else _new(shape, out_dtype, like.device, stream)
         return Y, out, max(cols, 1)
     r, c, ld = _matrix(Y, name)
     if r != rows or c != cols:
@@ -602,7 +613,7 @@ def adapter_gemm(X, W, A, B, ids, scale=None, Y=None, trans_w=False, out_dtype=N
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _one_gpu(("X", "W", "A", "B", "ids", "scale", "Y", "workspace"), (X, W, A, B, ids, scale, Y, workspace))
-    Y, out, ldy = _adapter_result(Y, M, N, out_dtype, X, code, "Y")
+    Y, out, ldy = _adapter_result(Y, M, N, out_dtype, X, code, "Y", stream)
     t = int(trans_w)
     if workspace is None:
         need = _adapter_workspace_bytes("sam_adapter_gemm_workspace", code, t, M, N, K, n, rank, ldx, ldw)
@@ -632,11 +643,11 @@ def adapter_backward(dY, X, W, A, B, ids, scale=None, dX=None, dA=None, dB=None,
              (dY, X, W, A, B, ids, scale, dX, dA, dB, workspace))
     out, lddx = F32, max(K, 1)
     if need_dx:
-        dX, out, lddx = _adapter_result(dX, M, K, out_dtype, X, code, "dX")
+        dX, out, lddx = _adapter_result(dX, M, K, out_dtype, X, code, "dX", stream)
     else:
         dX = None
     if need_dab:
-        dA, dB = (torch.empty(s, dtype=torch.float32, device=X.device) if t is None else t
+        dA, dB = (_new(s, torch.float32, X.device, stream) if t is None else t
                   for t, s in ((dA, A.shape), (dB, B.shape)))
         for t, like, name in ((dA, A, "dA"), (dB, B, "dB")):
             if t.dtype != torch.float32 or t.shape != like.shape or not t.is_contiguous():
@@ -678,20 +689,23 @@ def _distill_operands(logits, teacher, index, weight):
     return code, t_code, rows, V, shape[1], ldz
 
 
-def _per_row(t, rows, like, name):
+def _per_row(t, rows, like, name, stream=None):
     """t, checked, or (None) a new float32 tensor of `rows` beside `like`."""
     import torch
     if t is None:
-        return torch.empty(rows, dtype=torch.float32, device=like.device)
+        if stream is None:
+            return torch.empty(rows, dtype=torch.float32, device=like.device)
+        return _new(rows, torch.float32, like.device, stream)
     if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != rows or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {rows}")
     return t
 
 
-def _distill_result(grad, logits, V):
+def _distill_result(grad, logits, V, stream):
     """The gradient (given or new) and its row stride."""
     if grad is None:
-        return logits.new_empty(logits.shape), max(V, 1)
+        shape = logits.shape
+        return logits.new_empty(shape) if stream is None else _new(shape, logits.dtype, logits.device, stream), max(V, 1)
     if grad.dtype != logits.dtype or grad.shape != logits.shape:
         raise ValueError(f"grad must be {logits.dtype} {tuple(logits.shape)}")
     return grad, _matrix(grad, "grad")[2]
@@ -707,7 +721,7 @@ def distill_loss(logits, teacher, index, weight=None, temperature=1.0, loss=None
     float32 [rows]."""
     code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
     _one_gpu(("logits", "teacher", "index", "weight", "loss", "lse"), (logits, teacher, index, weight, loss, lse))
-    loss, lse = _per_row(loss, rows, logits, "loss"), _per_row(lse, rows, logits, "lse")
+    loss, lse = _per_row(loss, rows, logits, "loss", stream), _per_row(lse, rows, logits, "lse", stream)
     _check(lib().sam_distill_loss(code, rows, V, top, _address(logits), ldz, t_code, _address(teacher),
                                   _address(index), _address(weight), float(temperature), _address(loss),
                                   _address(lse), _stream_address(stream)))
@@ -720,7 +734,7 @@ def distill_grad(logits, lse, teacher, index, weight=None, temperature=1.0, grad
     code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
     _one_gpu(("logits", "lse", "teacher", "index", "weight", "grad"), (logits, lse, teacher, index, weight, grad))
     lse = _per_row(lse, rows, logits, "lse")
-    grad, ldg = _distill_result(grad, logits, V)
+    grad, ldg = _distill_result(grad, logits, V, stream)
     _check(lib().sam_distill_grad(code, rows, V, top, _address(logits), ldz, _address(lse), t_code, _address(teacher),
                                   _address(index), _address(weight), float(temperature), _address(grad), ldg,
                                   _stream_address(stream)))
@@ -733,8 +747,8 @@ def distill(logits, teacher, index, weight=None, temperature=1.0, loss=None, gra
     logits itself."""
     code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
     _one_gpu(("logits", "teacher", "index", "weight", "loss", "grad"), (logits, teacher, index, weight, loss, grad))
-    loss = _per_row(loss, rows, logits, "loss")
-    grad, ldg = _distill_result(grad, logits, V)
+    loss = _per_row(loss, rows, logits, "loss", stream)
+    grad, ldg = _distill_result(grad, logits, V, stream)
     _check(lib().sam_distill(code, rows, V, top, _address(logits), ldz, t_code, _address(teacher), _address(index),
                              _address(weight), float(temperature), _address(loss), _address(grad), ldg,
                              _stream_address(stream)))
