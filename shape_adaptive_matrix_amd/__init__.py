@@ -733,6 +733,8 @@ def distill_grad(logits, lse, teacher, index, weight=None, temperature=1.0, grad
     lse of distill_loss (sam_distill_grad). grad may be logits itself."""
     code, t_code, rows, V, top, ldz = _distill_operands(logits, teacher, index, weight)
     _one_gpu(("logits", "lse", "teacher", "index", "weight", "grad"), (logits, lse, teacher, index, weight, grad))
+    if lse is None:
+        raise ValueError("lse is what distill_loss returned; distill makes loss and gradient without it")
     lse = _per_row(lse, rows, logits, "lse")
     grad, ldg = _distill_result(grad, logits, V, stream)
     _check(lib().sam_distill_grad(code, rows, V, top, _address(logits), ldz, _address(lse), t_code, _address(teacher),

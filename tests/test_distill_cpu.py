@@ -94,3 +94,10 @@ def test_rows_that_share_memory_are_refused(strides, monkeypatch):
     for call in (sam.distill, lambda z, **a: sam.distill_grad(z, lse, **a)):
         with pytest.raises(ValueError, match="share memory"):
             call(torch.zeros(4, 50), **rest, grad=shared())
+
+
+def test_gradient_needs_its_lse(monkeypatch):
+    """None was replaced by new memory, and the gradient made of what it held."""
+    monkeypatch.setattr(sam, "_one_gpu", lambda *a: 0)
+    with pytest.raises(ValueError, match="lse"):
+        sam.distill_grad(torch.zeros(4, 50), None, torch.zeros(4, 5), torch.zeros(4, 5, dtype=torch.int32))
