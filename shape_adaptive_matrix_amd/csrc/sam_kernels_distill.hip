@@ -634,17 +634,21 @@ hipError_t run(const DistillArgs& a, int per, hipStream_t s)
 }
 
 // Threads and registers by the row's length, so that each holds a row and two
-// to four workgroups share a CU (4096 x 32768 bf16: three of 512 threads 110
-// us, two 114, three of 256 with twice the registers 122, one of 1024 138, all
-// before the entries' logits came ahead, too);
-// few rows: as many threads as fit, for latency.
+// to four workgroups share a CU. Loss and gradient, bf16, 32 entries, us:
+// 4096 x 32768: three of 512 threads 96, two 101, three of 256 with twice the
+// registers 108, one of 1024 111; 4096 x 16000: four of 256 57, three of 512 75.
+// Up to one row a CU: as many threads as fit, for latency (64 x 32768: 1024
+// threads 9.6, 512 10.3; 256 rows 11.2 and 11.8; 400 rows 17.4 and 15.5. 256 x
+// 65536: 14.9 and 15.6; 400 rows 26.6 and 22.0).
 template <int DT>
 hipError_t pick(const DistillArgs& a, hipStream_t s)
 {
     const long long pieces = ((long long)a.V + Piece<DT>::E - 1) / Piece<DT>::E;
     const bool few = a.rows <= 256;
     // Many short rows: a wave each and no barrier, so that a CU has 16 to 20
-    // on their way (3127 x 2917 f16: four of 256 threads 27 us, this 15).
+    // on their way (4096 x 4000: four of 256 threads 38 us, this 20; 1400 x
+    // 8000: both 18; 1024 rows of 1500, 4000, 8000: 13.1, 13.1, 13.9 with 256
+    // threads and 9.5, 10.7, 14.0 this way; 512 of 8000: 11.1 and 12.4).
     if (a.rows > 1024 && a.top <= kFewTop) {
         if (pieces <= 64 * 4) return run<DT, 64, 4, 0, false, kFewTop>(a, 20, s);
         if (pieces <= 64 * 8) return run<DT, 64, 8, 0, false, kFewTop>(a, 20, s);
