@@ -398,6 +398,86 @@ sam_status sam_distill(sam_dtype dtype, int64_t rows, int64_t V, int64_t top,
                        const float* weight, float temperature, float* loss,
                        void* grad, int64_t ldg, void* stream);
 
+/* MXFP4 tensors (the operands of sam_gemm_mxfp4) from values, and back. Of
+ * every block of 32 values of a row (zeros behind the last ones when K is no
+ * multiple of 32):
+ *   s = floor(log2(max |x|)) - 2, at least -127 (-127 too for a block of zeros)
+ *   code = E2M1(x / 2^s): the nearest value, ties to the even code, at most 6
+ *   scale code = s + 127
+ * A block that holds an Inf or NaN gets the scale code 255 and codes 0: it
+ * stands for NaN throughout.
+ *   dtype   SAM_F32, SAM_BF16 or SAM_F16: the values' type.
+ *   trans   SAM_OP_N: X is `rows` rows of K values, ldx >= K. SAM_OP_T: X is K
+ *           rows of `rows` values, ldx >= rows (a K x N weight becomes the N
+ *           rows of K that the products take).
+ *   X       device, aligned to one value (rows on 16 bytes cost least).
+ *   codes   device, rows x ceil(K / 32) x 16 bytes, compact, 16-byte aligned:
+ *           element k of a row in the low half of its byte k / 2 for even k.
+ *   scales  device, rows x ceil(K / 32) bytes, compact, any alignment.
+ * codes and scales overlap neither X nor each other. K >= 1, rows *
+ * ceil(K / 32) below 2^31; rows == 0 is a no-op. Asynchronous on `stream`. */
+sam_status sam_quantize_mxfp4(sam_dtype dtype, sam_op trans, int64_t rows,
+                              int64_t K, const void* X, int64_t ldx,
+                              uint8_t* codes, uint8_t* scales, void* stream);
+
+/* The values that codes and scales stand for, rounded to nearest even where
+ * `dtype` cannot hold them (SAM_F16: under 2^-14 or over 65504; SAM_BF16 and
+ * SAM_F32 hold all that sam_quantize_mxfp4 makes): X is `rows` rows of K
+ * values, row stride ldx >= K, aligned to one value. Scale code 255 gives
+ * NaN. */
+sam_status sam_dequantize_mxfp4(sam_dtype dtype, int64_t rows, int64_t K,
+                                const uint8_t* codes, const uint8_t* scales,
+                                void* X, int64_t ldx, void* stream);
+
+/* Projection by a weight kept in MXFP4, for single tokens, prompts and
+ * training:
+ *   Y = q(X) Wq^T
+ * q(X) are the values of X's rows after sam_quantize_mxfp4, Wq the N rows of K
+ * values that codes and scales stand for. Products and sums as in
+ * sam_gemm_mxfp4, FP32, rounded once (to nearest even) where `out` is a 16-bit
+ * type.
+ *   dtype   SAM_F32, SAM_BF16 or SAM_F16: X.
+ *   X       device, M rows of K values, row stride ldx >= K.
+ *   codes   device, N x ceil(K / 32) x 16 bytes, 16-byte aligned.
+ *   scales  device, N x ceil(K / 32) bytes, any alignment.
+ *   out     the type of Y: SAM_F32 or dtype.
+ *   Y       device, M rows of N values, row stride ldy >= N; write-only.
+ * X and Y are aligned to one value. A block of X or of the weight that stands
+ * for NaN makes the results of its row (of its column) NaN. N, K >= 1 and up
+ * to 2.08 M; M == 0 is a no-op; a single row's stride may be any. Y overlaps
+ * nothing else. Workspace: sam_linear_mxfp4_workspace() bytes,
+ * SAM_ERR_WORKSPACE when short. Asynchronous on `stream`, no atomics, a fixed
+ * order. */
+sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K,
+                            const void* X, int64_t ldx, const uint8_t* codes,
+                            const uint8_t* scales, sam_dtype out, void* Y,
+                            int64_t ldy, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes sam_linear_mxfp4 needs for these sizes and types (host only). */
+sam_status sam_linear_mxfp4_workspace(sam_dtype dtype, sam_dtype out, int64_t M,
+                                      int64_t N, int64_t K, uint64_t* bytes);
+
+/* Gradient of sam_linear_mxfp4 with respect to X for a given gradient dY of Y;
+ * the weight is frozen and the rounding of X is passed through as it is:
+ *   dX = dY Wq      (M rows of K)
+ * dY (dtype, M rows of N, row stride lddy >= N) is not rounded; Wq is taken in
+ * dtype, as sam_dequantize_mxfp4 gives it. dX (type `out`: SAM_F32 or dtype, row stride
+ * lddx >= K) is written whole. dY and dX must be 16-byte aligned; strides up
+ * to 2.08 M values (a single row's may be any). Everything else as for
+ * sam_linear_mxfp4. */
+sam_status sam_linear_mxfp4_backward(sam_dtype dtype, int64_t M, int64_t N,
+                                     int64_t K, const void* dY, int64_t lddy,
+                                     const uint8_t* codes,
+                                     const uint8_t* scales, sam_dtype out,
+                                     void* dX, int64_t lddx, void* workspace,
+                                     uint64_t workspace_bytes, void* stream);
+
+/* Workspace bytes sam_linear_mxfp4_backward needs (host only). */
+sam_status sam_linear_mxfp4_backward_workspace(sam_dtype dtype, sam_dtype out,
+                                               int64_t M, int64_t N, int64_t K,
+                                               uint64_t* bytes);
+
 /* Number of entries in the variant table (ids 0 .. count-1). */
 int32_t sam_variant_count(void);
 

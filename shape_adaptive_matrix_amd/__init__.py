@@ -124,6 +124,15 @@ def lib() -> ctypes.CDLL:
                               i64, vp], ctypes.c_int),
         "sam_distill": ([ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_int, vp, vp, vp, ctypes.c_float, vp, vp, i64,
                          vp], ctypes.c_int),
+        "sam_quantize_mxfp4": ([ctypes.c_int, ctypes.c_int, i64, i64, vp, i64, vp, vp, vp], ctypes.c_int),
+        "sam_dequantize_mxfp4": ([ctypes.c_int, i64, i64, vp, vp, vp, i64, vp], ctypes.c_int),
+        "sam_linear_mxfp4": ([ctypes.c_int, i64, i64, i64, vp, i64, vp, vp, ctypes.c_int, vp, i64, vp, u64, vp],
+                             ctypes.c_int),
+        "sam_linear_mxfp4_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, ctypes.POINTER(u64)], ctypes.c_int),
+        "sam_linear_mxfp4_backward": ([ctypes.c_int, i64, i64, i64, vp, i64, vp, vp, ctypes.c_int, vp, i64, vp, u64, vp],
+                                      ctypes.c_int),
+        "sam_linear_mxfp4_backward_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, ctypes.POINTER(u64)],
+                                                ctypes.c_int),
         "sam_device_check": ([], ctypes.c_int),
         "sam_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "sam_last_error": ([], ctypes.c_char_p),
@@ -598,7 +607,8 @@ def _adapter_workspace(nbytes, like, stream):
         return None
     if stream is not None:
         return workspace_for({"workspace_bytes": nbytes}, like.device, stream)
-    return like.new_empty((nbytes + 1) // 2)   # 16-bit values
+    es = like.element_size()
+    return like.new_empty((nbytes + es - 1) // es)
 
 
 def adapter_gemm(X, W, A, B, ids, scale=None, Y=None, trans_w=False, out_dtype=None, workspace=None, stream=None):
@@ -755,3 +765,144 @@ def distill(logits, teacher, index, weight=None, temperature=1.0, loss=None, gra
                              _address(weight), float(temperature), _address(loss), _address(grad), ldg,
                              _stream_address(stream)))
     return loss, grad
+
+
+# -- MXFP4 tensors and the 4-bit projection -----------------------------------------
+def _on_its_gpu(call):
+    """A call on its first tensor's GPU, whichever is current."""
+    @functools.wraps(call)
+    def on_its_gpu(first, *args, **more):
+        import torch
+        d = first.get_device()
+        if d < 0 or d == torch.cuda.current_device():
+            return call(first, *args, **more)
+        with torch.cuda.device(d):
+            return call(first, *args, **more)
+    return on_its_gpu
+
+
+def _value_code(t, name):
+    import torch
+    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    return code
+
+
+def _mxfp4_tensor(codes, scales):
+    """(rows, blocks) of a tensor's codes and scales."""
+    import torch
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or codes.shape[1] % 16:
+        raise ValueError(f"codes must be a contiguous uint8 [rows, 16 blocks] tensor (got {codes.dtype} {tuple(codes.shape)})")
+    rows, blocks = codes.shape[0], codes.shape[1] // 16
+    if scales.dtype != torch.uint8 or scales.shape != (rows, blocks) or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous uint8 [{rows}, {blocks}] tensor (got {scales.dtype} {tuple(scales.shape)})")
+    return rows, blocks
+
+
+def _columns(K, blocks, like=None):
+    """K values a row (those of `like`, a given result, or whole blocks when
+    None), which `blocks` blocks of 32 have to hold."""
+    if K is None:
+        if like is None or like.dim() != 2:
+            return 32 * blocks
+        K = like.shape[1]
+    if (K + 31) // 32 != blocks:
+        raise ValueError(f"rows of {K} values are {(K + 31) // 32} blocks, the codes have {blocks}")
+    return K
+
+
+@_on_its_gpu
+def quantize_mxfp4(X, trans=False, codes=None, scales=None, stream=None):
+    """MXFP4 codes and scales of X's rows (trans: of its columns, for a weight
+    stored K x N): (codes, scales), uint8 [rows, 16 ceil(K / 32)] and [rows,
+    ceil(K / 32)] (sam_quantize_mxfp4). X is 2-D float32, bfloat16 or float16
+    and may be a view with padded rows."""
+    import torch
+    code = _value_code(X, "X")
+    rows, K, ldx = _matrix(X, "X")
+    if trans:
+        rows, K = K, rows
+    _one_gpu(("X", "codes", "scales"), (X, codes, scales))
+    blocks = (K + 31) // 32
+    if codes is None:
+        codes = _new((rows, 16 * blocks), torch.uint8, X.device, stream)
+    if scales is None:
+        scales = _new((rows, blocks), torch.uint8, X.device, stream)
+    if _mxfp4_tensor(codes, scales) != (rows, blocks):
+        raise ValueError(f"codes and scales must be of {rows} rows and {blocks} blocks (got {tuple(scales.shape)})")
+    _check(lib().sam_quantize_mxfp4(code, int(trans), rows, K, _address(X), ldx, _address(codes), _address(scales),
+                                    _stream_address(stream)))
+    return codes, scales
+
+
+@_on_its_gpu
+def dequantize_mxfp4(codes, scales, K=None, out_dtype=None, X=None, stream=None):
+    """The values that codes and scales stand for (sam_dequantize_mxfp4): X
+    [rows, K], bfloat16 unless out_dtype (or X) says otherwise. K: 32 a block
+    unless given (or X is)."""
+    import torch
+    rows, blocks = _mxfp4_tensor(codes, scales)
+    K = _columns(K, blocks, X)
+    _one_gpu(("codes", "scales", "X"), (codes, scales, X))
+    if X is None:
+        X = _new((rows, K), torch.bfloat16 if out_dtype is None else out_dtype, codes.device, stream)
+    elif out_dtype is not None and X.dtype != out_dtype:
+        raise TypeError(f"X is {X.dtype}, out_dtype {out_dtype}")
+    code = _value_code(X, "X")
+    r, c, ldx = _matrix(X, "X")
+    if (r, c) != (rows, K):
+        raise ValueError(f"X must have shape ({rows}, {K}) (got {tuple(X.shape)})")
+    _check(lib().sam_dequantize_mxfp4(code, rows, K, _address(codes), _address(scales), _address(X), ldx,
+                                      _stream_address(stream)))
+    return X
+
+
+@_on_its_gpu
+def linear_mxfp4(X, codes, scales, Y=None, out_dtype=None, workspace=None, stream=None):
+    """Y = q(X)·Wq^T: X's rows rounded to MXFP4 times a weight kept in it
+    (sam_linear_mxfp4). X [M, K] float32, bfloat16 or float16, may be a view
+    with padded rows; codes and scales of the weight's N rows as
+    quantize_mxfp4 gives them. Returns Y [M, N], float32 unless out_dtype (or
+    Y) is of X's type."""
+    code = _value_code(X, "X")
+    N, blocks = _mxfp4_tensor(codes, scales)
+    M, K, ldx = _matrix(X, "X")
+    _columns(K, blocks)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _one_gpu(("X", "codes", "scales", "Y", "workspace"), (X, codes, scales, Y, workspace))
+    Y, out, ldy = _adapter_result(Y, M, N, out_dtype, X, code, "Y", stream)
+    if workspace is None:
+        need = _adapter_workspace_bytes("sam_linear_mxfp4_workspace", code, out, M, N, K)
+        workspace = _adapter_workspace(need, X, stream)
+    else:
+        need = _workspace_bytes(workspace)
+    _check(lib().sam_linear_mxfp4(code, M, N, K, _address(X), ldx, _address(codes), _address(scales), out, _address(Y),
+                                  ldy, _address(workspace), need, _stream_address(stream)))
+    return Y
+
+
+@_on_its_gpu
+def linear_mxfp4_backward(dY, codes, scales, K=None, dX=None, out_dtype=None, workspace=None, stream=None):
+    """Gradient of linear_mxfp4 with respect to X for dY [M, N], X's rounding
+    passed through (sam_linear_mxfp4_backward): dX = dY·Wq [M, K], float32
+    unless out_dtype (or dX) is of dY's type. K: 32 a block unless given (or dX is)."""
+    code = _value_code(dY, "dY")
+    N, blocks = _mxfp4_tensor(codes, scales)
+    K = _columns(K, blocks, dX)
+    M, n, lddy = _matrix(dY, "dY")
+    if n != N:
+        raise ValueError(f"dY has rows of {n}, the weight {N} rows")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _one_gpu(("dY", "codes", "scales", "dX", "workspace"), (dY, codes, scales, dX, workspace))
+    dX, out, lddx = _adapter_result(dX, M, K, out_dtype, dY, code, "dX", stream)
+    if workspace is None:
+        need = _adapter_workspace_bytes("sam_linear_mxfp4_backward_workspace", code, out, M, N, K)
+        workspace = _adapter_workspace(need, dY, stream)
+    else:
+        need = _workspace_bytes(workspace)
+    _check(lib().sam_linear_mxfp4_backward(code, M, N, K, _address(dY), lddy, _address(codes), _address(scales), out,
+                                           _address(dX), lddx, _address(workspace), need, _stream_address(stream)))
+    return dX

@@ -1,0 +1,385 @@
+// Kernels that make MXFP4 tensors and read them back (formulas in
+// sam_mxfp4.h).
+//
+// Bound by memory: 2 or 4 bytes a value on one side, 17 / 32 of a byte on the
+// other. The scaled conversions of gfx950 take a pair of values by a power of
+// two to E2M1 (to nearest, ties to even, saturating) and back; they were
+// compared with the definition for every finite 16-bit value and 4 million
+// FP32 ones at six distances from the block's exponent. A scale of code 0
+// (2^-127) is the float with all bits zero to them.
+#include "sam_mxfp4.h"
+
+namespace sam {
+
+namespace {
+
+typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+typedef u4 u4w __attribute__((aligned(4)));            // 16 bytes at any whole word
+typedef unsigned int u3w __attribute__((ext_vector_type(3), aligned(4)));
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+
+template <int DT> struct Ty;
+template <> struct Ty<DT_F32> { typedef float T; };
+template <> struct Ty<DT_BF16> { typedef __bf16 T; };
+template <> struct Ty<DT_F16> { typedef _Float16 T; };
+
+// W words of values, loaded as 16-byte pieces: `n` values at p are there
+// (all, unless the row ends inside), zeros behind them. ALIGNED: p is on 16
+// bytes. Otherwise p is on a value, and pieces are loaded from whole words
+// (16-bit values that start inside a word are shifted into place; the word
+// behind then holds the last of them, so nothing outside the row's own words
+// is touched).
+template <int DT, bool ALIGNED, int W>
+__device__ __forceinline__ void load_words(const typename Ty<DT>::T* p, int n, unsigned (&r)[W])
+{
+    constexpr int E = DT == DT_F32 ? W : 2 * W;
+    if (n >= E) {
+        if (ALIGNED || DT == DT_F32) {
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const u4 v = ALIGNED ? *reinterpret_cast<const u4*>(reinterpret_cast<const unsigned*>(p) + i)
+                                     : *reinterpret_cast<const u4w*>(reinterpret_cast<const unsigned*>(p) + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[i + j] = v[j];
+            }
+        } else {
+            const unsigned long long at = reinterpret_cast<unsigned long long>(p);
+            const unsigned* w = reinterpret_cast<const unsigned*>(at & ~3ull);
+            const unsigned shift = (unsigned)(at & 2) * 8;
+            unsigned v[W + 1];
+#pragma unroll
+            for (int i = 0; i < W; i += 4) {
+                const u4 x = *reinterpret_cast<const u4w*>(w + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i + j] = x[j];
+            }
+            v[W] = shift ? w[W] : 0;
+#pragma unroll
+            for (int i = 0; i < W; ++i) r[i] = __builtin_amdgcn_alignbit(v[i + 1], v[i], shift);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        if constexpr (DT == DT_F32) {
+            r[i] = i < n ? reinterpret_cast<const unsigned*>(p)[i] : 0u;
+        } else {
+            const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+            r[i] = 2 * i < n ? h[2 * i] : 0u;
+            if (2 * i + 1 < n) r[i] |= (unsigned)h[2 * i + 1] << 16;
+        }
+    }
+}
+
+// The largest |x| of packed words as bits that order like the values (16-bit
+// types: in each half), Inf and NaN above all others.
+template <int DT>
+__device__ __forceinline__ unsigned max_bits(unsigned a, unsigned x)
+{
+    if constexpr (DT == DT_F32) {
+        x &= 0x7FFFFFFFu;
+        return a > x ? a : x;
+    } else {
+        return __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, x & 0x7FFF7FFFu)));
+    }
+}
+
+// Of the largest value's bits (16-bit types: in the low half), the scale byte.
+template <int DT>
+__device__ __forceinline__ unsigned scale_code(unsigned bits)
+{
+    unsigned e;
+    if constexpr (DT == DT_F32) e = bits >> 23;
+    else if constexpr (DT == DT_BF16) e = (bits & 0xFFFF) >> 7;
+    else e = __float_as_uint((float)__builtin_bit_cast(_Float16, (unsigned short)bits)) >> 23;
+    return e == 255 ? 255 : (e > 2 ? e - 2 : 0);
+}
+
+// Eight values to eight codes: pairs x[0..3] of 16-bit values, or eight floats.
+template <int DT, int W>
+__device__ __forceinline__ unsigned to_codes(const unsigned (&x)[W], unsigned code)
+{
+    const float s = __uint_as_float(code << 23);
+    unsigned r = 0;
+    if constexpr (DT == DT_F32) {
+        static_assert(W == 8, "eight values");
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(x[0]), __uint_as_float(x[1]), s, 0);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(x[2]), __uint_as_float(x[3]), s, 1);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(x[4]), __uint_as_float(x[5]), s, 2);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, __uint_as_float(x[6]), __uint_as_float(x[7]), s, 3);
+    } else if constexpr (DT == DT_BF16) {
+        static_assert(W == 4, "eight values");
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(b2, x[0]), s, 0);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(b2, x[1]), s, 1);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(b2, x[2]), s, 2);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(b2, x[3]), s, 3);
+    } else {
+        static_assert(W == 4, "eight values");
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, x[0]), s, 0);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, x[1]), s, 1);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, x[2]), s, 2);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(h2, x[3]), s, 3);
+    }
+    return code == 255 ? 0u : r;
+}
+
+template <int CTRL>
+__device__ __forceinline__ unsigned quad(unsigned v)   // of another lane of the four
+{
+    return __builtin_amdgcn_update_dpp(0u, v, CTRL, 0xF, 0xF, true);
+}
+
+constexpr int kQuantThreads = 256, kQuantEach = 2;
+
+// A quarter of a block a lane: 16 (FP32: 32) bytes in, 4 out, both whole
+// lines a wave.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a)
+{
+    typedef typename Ty<DT>::T T;
+    constexpr int W = DT == DT_F32 ? 8 : 4;
+    const unsigned per_row = 4u * a.kb;
+    const long long first = (long long)blockIdx.x * (kQuantThreads * kQuantEach);
+    const long long row0 = first / per_row;
+    const unsigned rem0 = (unsigned)(first - row0 * per_row);
+    unsigned x[kQuantEach][W];
+    long long row[kQuantEach];
+    unsigned q[kQuantEach];
+#pragma unroll
+    for (int i = 0; i < kQuantEach; ++i) {
+        const unsigned at = rem0 + threadIdx.x + i * kQuantThreads;
+        const unsigned down = at / per_row;
+        row[i] = row0 + down;
+        q[i] = at - down * per_row;
+        // Lanes past the last row: no values, and nothing is stored.
+        const int n = row[i] < a.rows ? a.K - (int)q[i] * 8 : 0;
+        load_words<DT, ALIGNED>(static_cast<const T*>(a.x) + (n > 0 ? row[i] * a.ldx + q[i] * 8 : 0), n, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantEach; ++i) {
+        unsigned m = 0;
+#pragma unroll
+        for (int j = 0; j < W; ++j) m = max_bits<DT>(m, x[i][j]);
+        if (DT != DT_F32) m = max(m & 0xFFFFu, m >> 16);
+        m = max(m, quad<0xB1>(m));   // lanes 1 0 3 2
+        m = max(m, quad<0x4E>(m));   // lanes 2 3 0 1
+        const unsigned code = scale_code<DT>(m);
+        const unsigned c = to_codes<DT>(x[i], code);
+        if (row[i] < a.rows) {
+            reinterpret_cast<unsigned*>(a.codes)[row[i] * per_row + q[i]] = c;
+            if ((q[i] & 3) == 0) a.scales[row[i] * a.kb + (q[i] >> 2)] = (unsigned char)code;
+        }
+    }
+}
+
+// X given as K rows: a lane takes 16 bytes (C columns) of the 32 rows of a
+// block, eight lanes a 128-byte line, eight blocks a wave: what a wave stores
+// for a column is 128 bytes again. All 32 loads of a lane are under way at
+// once (32 KB a wave).
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(256) quant4_cols_kernel(Quant4Args a, int groups)
+{
+    typedef typename Ty<DT>::T T;
+    constexpr int C = DT == DT_F32 ? 4 : 8;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int down = blockIdx.x / groups, over = blockIdx.x - down * groups;
+    const int kb = down * 8 + lane / 8;
+    const long long c0 = ((long long)over * 4 + wave) * 8 * C + (lane % 8) * C;
+    const long long left = a.rows - c0;
+    if (kb >= a.kb || left <= 0) return;
+    const int n = left < C ? (int)left : C;
+    unsigned r[32][4];
+    const T* p = static_cast<const T*>(a.x) + (long long)kb * 32 * a.ldx + c0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        const bool in = kb * 32 + k < a.K;
+        load_words<DT, ALIGNED>(in ? p + k * a.ldx : p, in ? n : 0, r[k]);
+    }
+    unsigned m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = max_bits<DT>(m[j], r[k][j]);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int w = C == 8 ? c / 2 : c;
+        const unsigned code = scale_code<DT>(C == 8 && (c & 1) ? m[w] >> 16 : m[w]);
+        u4 out;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            if constexpr (DT == DT_F32) {
+                unsigned v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = r[8 * g + i][w];
+                out[g] = to_codes<DT>(v, code);
+            } else {
+                unsigned v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)   // the column's values of two rows
+                    v[i] = __builtin_amdgcn_perm(r[8 * g + 2 * i + 1][w], r[8 * g + 2 * i][w], c & 1 ? 0x07060302u : 0x05040100u);
+                out[g] = to_codes<DT>(v, code);
+            }
+        }
+        if (c < n) {
+            *reinterpret_cast<u4*>(a.codes + ((c0 + c) * a.kb + kb) * 16) = out;
+            a.scales[(c0 + c) * a.kb + kb] = (unsigned char)code;
+        }
+    }
+}
+
+// Eight codes to eight values, a quarter of a block a lane as above.
+template <int DT, int W>
+__device__ __forceinline__ void from_codes(unsigned c, unsigned code, unsigned (&x)[W])
+{
+    const float s = __uint_as_float(code << 23);
+    if constexpr (DT == DT_F32) {
+        const f2 v[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1),
+                         __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = code == 255 ? 0x7FC00000u : __float_as_uint(v[i / 2][i % 2]);
+    } else if constexpr (DT == DT_BF16) {
+        x[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
+        x[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
+        x[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
+        x[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = code == 255 ? 0x7FC07FC0u : x[i];
+    } else {
+        x[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0));
+        x[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1));
+        x[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2));
+        x[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = code == 255 ? 0x7E007E00u : x[i];
+    }
+}
+
+// Eight packed values to p, the first `n` of them; 16-bit values that start
+// inside a word as two halves and the three words between.
+template <int DT, bool ALIGNED, int W>
+__device__ __forceinline__ void store_words(typename Ty<DT>::T* p, int n, const unsigned (&r)[W])
+{
+    unsigned* w = reinterpret_cast<unsigned*>(p);
+    if (n >= 8) {
+        if constexpr (DT == DT_F32) {
+            if (ALIGNED) {
+                *reinterpret_cast<u4*>(w) = u4{r[0], r[1], r[2], r[3]};
+                *reinterpret_cast<u4*>(w + 4) = u4{r[4], r[5], r[6], r[7]};
+            } else {
+                *reinterpret_cast<u4w*>(w) = u4{r[0], r[1], r[2], r[3]};
+                *reinterpret_cast<u4w*>(w + 4) = u4{r[4], r[5], r[6], r[7]};
+            }
+        } else if (ALIGNED) {
+            *reinterpret_cast<u4*>(w) = u4{r[0], r[1], r[2], r[3]};
+        } else if ((reinterpret_cast<unsigned long long>(p) & 2) == 0) {
+            *reinterpret_cast<u4w*>(w) = u4{r[0], r[1], r[2], r[3]};
+        } else {
+            unsigned short* h = reinterpret_cast<unsigned short*>(p);
+            h[0] = (unsigned short)r[0];
+            *reinterpret_cast<u3w*>(h + 1) = u3w{__builtin_amdgcn_alignbit(r[1], r[0], 16), __builtin_amdgcn_alignbit(r[2], r[1], 16),
+                                                 __builtin_amdgcn_alignbit(r[3], r[2], 16)};
+            h[7] = (unsigned short)(r[3] >> 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        if (i >= n) return;
+        if constexpr (DT == DT_F32) w[i] = r[i];
+        else reinterpret_cast<unsigned short*>(p)[i] = (unsigned short)(i & 1 ? r[i / 2] >> 16 : r[i / 2]);
+    }
+}
+
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kQuantThreads) dequant4_kernel(Dequant4Args a)
+{
+    typedef typename Ty<DT>::T T;
+    constexpr int W = DT == DT_F32 ? 8 : 4;
+    const unsigned per_row = 4u * a.kb;
+    const long long first = (long long)blockIdx.x * (kQuantThreads * kQuantEach);
+    const long long row0 = first / per_row;
+    const unsigned rem0 = (unsigned)(first - row0 * per_row);
+    unsigned c[kQuantEach], s[kQuantEach], q[kQuantEach];
+    long long row[kQuantEach];
+#pragma unroll
+    for (int i = 0; i < kQuantEach; ++i) {
+        const unsigned at = rem0 + threadIdx.x + i * kQuantThreads;
+        const unsigned down = at / per_row;
+        row[i] = row0 + down;
+        q[i] = at - down * per_row;
+        const bool in = row[i] < a.rows;
+        c[i] = reinterpret_cast<const unsigned*>(a.codes)[in ? row[i] * per_row + q[i] : 0];
+        s[i] = a.scales[in ? row[i] * a.kb + (q[i] >> 2) : 0];
+    }
+#pragma unroll
+    for (int i = 0; i < kQuantEach; ++i) {
+        unsigned x[W];
+        from_codes<DT>(c[i], s[i], x);
+        const int n = row[i] < a.rows ? a.K - (int)q[i] * 8 : 0;
+        if (n > 0) store_words<DT, ALIGNED>(static_cast<T*>(a.x) + row[i] * a.ldx + q[i] * 8, n, x);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(256) convert4_kernel(Convert4Args a)
+{
+    typedef typename Ty<DT>::T T;
+    const long long n = a.rows * a.cols;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+        const long long row = i / a.cols;
+        static_cast<T*>(a.dst)[row * a.ldd + (i - row * a.cols)] = (T)a.src[i];
+    }
+}
+
+bool on16(const void* p, long long ld, int es) { return (reinterpret_cast<unsigned long long>(p) & 15) == 0 && ld * es % 16 == 0; }
+
+}  // namespace
+
+hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t s)
+{
+    const int es = dtype == DT_F32 ? 4 : 2;
+    const bool al = on16(a.x, a.ldx, es);
+    if (trans) {
+        const long long cols = 4 * 8 * 16 / es;
+        const long long groups = (a.rows + cols - 1) / cols, down = (a.kb + 7) / 8;
+        typedef void (*Fn)(Quant4Args, int);
+        static const Fn fn[3][2] = {{quant4_cols_kernel<DT_F32, false>, quant4_cols_kernel<DT_F32, true>},
+                                    {quant4_cols_kernel<DT_BF16, false>, quant4_cols_kernel<DT_BF16, true>},
+                                    {quant4_cols_kernel<DT_F16, false>, quant4_cols_kernel<DT_F16, true>}};
+        hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)(groups * down)), dim3(256), 0, s, a, (int)groups);
+        return hipGetLastError();
+    }
+    const long long pieces = a.rows * a.kb * 4, each = kQuantThreads * kQuantEach;
+    typedef void (*Fn)(Quant4Args);
+    static const Fn fn[3][2] = {{quant4_rows_kernel<DT_F32, false>, quant4_rows_kernel<DT_F32, true>},
+                                {quant4_rows_kernel<DT_BF16, false>, quant4_rows_kernel<DT_BF16, true>},
+                                {quant4_rows_kernel<DT_F16, false>, quant4_rows_kernel<DT_F16, true>}};
+    hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)((pieces + each - 1) / each)), dim3(kQuantThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_dequant4(int dtype, const Dequant4Args& a, hipStream_t s)
+{
+    const bool al = on16(a.x, a.ldx, dtype == DT_F32 ? 4 : 2);
+    const long long pieces = a.rows * a.kb * 4, each = kQuantThreads * kQuantEach;
+    typedef void (*Fn)(Dequant4Args);
+    static const Fn fn[3][2] = {{dequant4_kernel<DT_F32, false>, dequant4_kernel<DT_F32, true>},
+                                {dequant4_kernel<DT_BF16, false>, dequant4_kernel<DT_BF16, true>},
+                                {dequant4_kernel<DT_F16, false>, dequant4_kernel<DT_F16, true>}};
+    hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)((pieces + each - 1) / each)), dim3(kQuantThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_convert4(int dtype, const Convert4Args& a, hipStream_t s)
+{
+    const long long n = (a.rows * a.cols + 255) / 256;
+    typedef void (*Fn)(Convert4Args);
+    static const Fn fn[3] = {convert4_kernel<DT_F32>, convert4_kernel<DT_BF16>, convert4_kernel<DT_F16>};
+    hipLaunchKernelGGL(fn[dtype], dim3((unsigned)(n < 8192 ? n : 8192)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace sam

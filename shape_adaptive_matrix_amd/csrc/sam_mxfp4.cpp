@@ -1,0 +1,286 @@
+// Entry points of the MXFP4 tensors and the 4-bit projection (declared in
+// include/sam.h): argument checks, workspace layout and launches. Everything
+// that can be rejected is rejected before any HIP call.
+#include "sam_check.h"
+#include "sam_mxfp4.h"
+
+using namespace sam;
+
+namespace {
+
+constexpr long long kMostRow = 0x7FFFFFF0ll / (257 * 4);   // the products' offset range
+
+int elem(int dtype) { return dtype == SAM_F32 ? 4 : 2; }
+
+bool value_type(int dtype) { return dtype >= SAM_F32 && dtype <= SAM_F16; }
+
+struct Buf {
+    const void* p;
+    unsigned long long bytes;
+    const char* name;
+    int align;
+    bool written;
+};
+
+// Null, alignment and overlap: nothing that is written may overlap anything else.
+sam_status check_buffers(const Buf* b, int n)
+{
+    for (int i = 0; i < n; ++i) {
+        if (b[i].bytes && !b[i].p) return api_fail(SAM_ERR_INVALID_ARG, "%s is null", b[i].name);
+        if (b[i].bytes && (unsigned long long)b[i].p % (unsigned)b[i].align)
+            return api_fail(SAM_ERR_MISALIGNED, "%s must be %d-byte aligned", b[i].name, b[i].align);
+    }
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && b[i].written && ranges_overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
+                return api_fail(SAM_ERR_INVALID_ARG, "%s overlaps %s", b[i].name, b[j].name);
+    return SAM_OK;
+}
+
+unsigned long long span(long long rows, long long ld, long long cols, int es)
+{
+    return rows > 0 ? ((unsigned long long)(rows - 1) * ld + cols) * es : 0;
+}
+
+long long blocks_of(long long K) { return (K + 31) / 32; }
+
+// A tensor of `rows` rows of K values beside its codes. lines x line: how the
+// values are stored.
+sam_status check_tensor(int dtype, long long rows, long long K, long long lines, long long line, long long ldx)
+{
+    if (!value_type(dtype)) return api_fail(SAM_ERR_INVALID_ARG, "bad dtype %d", dtype);
+    if (rows < 0 || K < 1 || rows > (1ll << 30) || K > (1ll << 31) - 64 || rows > ((1ll << 31) - 1) / blocks_of(K))
+        return api_fail(SAM_ERR_INVALID_ARG, "bad sizes rows=%lld K=%lld", rows, K);
+    if (lines > 1 && (ldx < line || ldx > (1ll << 40)))
+        return api_fail(SAM_ERR_INVALID_ARG, "row stride %lld (rows of %lld)", ldx, line);
+    return SAM_OK;
+}
+
+sam_status done(hipError_t e)
+{
+    return e == hipSuccess ? api_ok() : api_fail(SAM_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
+}
+
+struct Region {
+    unsigned long long off = 0, bytes = 0;
+};
+
+struct Layout {
+    Region codes, scales, result, inner;   // forward
+    Region w, ids;                         // backward
+    unsigned long long total = 0;
+    void take(Region& r, unsigned long long bytes)
+    {
+        r.off = total;
+        r.bytes = bytes;
+        total += align256(bytes);
+    }
+};
+
+sam_status check_linear(int dtype, int out, long long M, long long N, long long K)
+{
+    if (!value_type(dtype)) return api_fail(SAM_ERR_INVALID_ARG, "bad dtype %d", dtype);
+    if (out != dtype && out != SAM_F32)
+        return api_fail(SAM_ERR_INVALID_ARG, "result type %d is neither SAM_F32 nor the operand's type", out);
+    if (M < 0 || N < 1 || K < 1 || N > kMostRow || K > kMostRow)
+        return api_fail(SAM_ERR_INVALID_ARG, "bad sizes M=%lld N=%lld K=%lld", M, N, K);
+    const long long wide = N > K ? N : K;
+    if (M > (1ll << 30) || M > ((1ll << 31) - 1) / blocks_of(wide))
+        return api_fail(SAM_ERR_INVALID_ARG, "M=%lld too many rows", M);
+    return SAM_OK;
+}
+
+sam_status forward_layout(int dtype, int out, long long M, long long N, long long K, Plan* p, Layout* L)
+{
+    const sam_status st = check_linear(dtype, out, M, N, K);
+    if (st != SAM_OK) return st;
+    *L = Layout{};
+    if (M == 0) return SAM_OK;
+    const long long kb = blocks_of(K);
+    if (!plan_auto(M, N, 32 * kb, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
+    L->take(L->codes, 16ull * M * kb);
+    L->take(L->scales, (unsigned long long)M * kb);
+    L->take(L->result, 4ull * M * N);
+    L->take(L->inner, p->ws_bytes);
+    return SAM_OK;
+}
+
+sam_status backward_layout(int dtype, int out, long long M, long long N, long long K, Layout* L)
+{
+    const sam_status st = check_linear(dtype, out, M, N, K);
+    if (st != SAM_OK) return st;
+    *L = Layout{};
+    if (M == 0) return SAM_OK;
+    const long long row = dtype == SAM_F32 ? (K + 3) / 4 * 4 : (K + 7) / 8 * 8;
+    L->take(L->w, (unsigned long long)N * row * elem(dtype));
+    uint64_t inner = 0;
+    sam_status e;
+    // Strides do not change what the products' own workspace holds beyond a
+    // copy of dY, for which the largest is taken.
+    if (dtype == SAM_F32) {
+        uint64_t other = 0;
+        e = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, N + 1, row, K + 1, 1.0f, 0.0f, &inner);
+        if (e == SAM_OK) e = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, N, row, K, 1.0f, 0.0f, &other);
+        if (other > inner) inner = other;
+    } else {
+        L->take(L->ids, 4ull * M);
+        e = sam_adapter_gemm_workspace((sam_dtype)dtype, SAM_OP_N, M, K, N, 0, 1, N + 1, row, &inner);
+    }
+    if (e != SAM_OK) return e;
+    L->take(L->inner, inner);
+    return SAM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sam_status sam_quantize_mxfp4(sam_dtype dtype, sam_op trans, int64_t rows, int64_t K, const void* X, int64_t ldx,
+                              uint8_t* codes, uint8_t* scales, void* stream)
+{
+    if (trans != SAM_OP_N && trans != SAM_OP_T) return api_fail(SAM_ERR_INVALID_ARG, "trans must be SAM_OP_N or SAM_OP_T");
+    const long long lines = trans ? K : rows, line = trans ? rows : K;
+    sam_status st = check_tensor(dtype, rows, K, lines, line, ldx);
+    if (st != SAM_OK) return st;
+    const long long kb = blocks_of(K);
+    const int es = elem(dtype);
+    const Buf bufs[] = {
+        {X, rows ? span(lines, ldx, line, es) : 0, "X", es, false},
+        {codes, 16ull * rows * kb, "codes", 16, true},
+        {scales, (unsigned long long)rows * kb, "scales", 1, true},
+    };
+    st = check_buffers(bufs, 3);
+    if (st != SAM_OK) return st;
+    if (rows == 0) return api_ok();
+    st = api_device_check();
+    if (st != SAM_OK) return st;
+    const Quant4Args a{X, lines > 1 ? ldx : line, rows, (int)K, (int)kb, codes, scales};
+    return done(launch_quant4(dtype, trans == SAM_OP_T, a, static_cast<hipStream_t>(stream)));
+}
+
+sam_status sam_dequantize_mxfp4(sam_dtype dtype, int64_t rows, int64_t K, const uint8_t* codes, const uint8_t* scales, void* X,
+                                int64_t ldx, void* stream)
+{
+    sam_status st = check_tensor(dtype, rows, K, rows, K, ldx);
+    if (st != SAM_OK) return st;
+    const long long kb = blocks_of(K);
+    const int es = elem(dtype);
+    const Buf bufs[] = {
+        {codes, 16ull * rows * kb, "codes", 16, false},
+        {scales, (unsigned long long)rows * kb, "scales", 1, false},
+        {X, span(rows, ldx, K, es), "X", es, true},
+    };
+    st = check_buffers(bufs, 3);
+    if (st != SAM_OK) return st;
+    if (rows == 0) return api_ok();
+    st = api_device_check();
+    if (st != SAM_OK) return st;
+    const Dequant4Args a{codes, scales, rows, (int)K, (int)kb, X, rows > 1 ? ldx : K};
+    return done(launch_dequant4(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+sam_status sam_linear_mxfp4_workspace(sam_dtype dtype, sam_dtype out, int64_t M, int64_t N, int64_t K, uint64_t* bytes)
+{
+    if (!bytes) return api_fail(SAM_ERR_INVALID_ARG, "bytes is null");
+    Plan p{};
+    Layout L;
+    const sam_status st = forward_layout(dtype, out, M, N, K, &p, &L);
+    if (st != SAM_OK) return st;
+    *bytes = L.total;
+    return api_ok();
+}
+
+sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const uint8_t* codes,
+                            const uint8_t* scales, sam_dtype out, void* Y, int64_t ldy, void* workspace,
+                            uint64_t workspace_bytes, void* stream)
+{
+    Plan p{};
+    Layout L;
+    sam_status st = forward_layout(dtype, out, M, N, K, &p, &L);
+    if (st != SAM_OK) return st;
+    if (M == 0) return api_ok();
+    if (M > 1 && (ldx < K || ldy < N || ldx > (1ll << 40) || ldy > (1ll << 40)))
+        return api_fail(SAM_ERR_INVALID_ARG, "row stride ldx=%lld (rows of %lld) or ldy=%lld (rows of %lld)", (long long)ldx,
+                        (long long)K, (long long)ldy, (long long)N);
+    const long long kb = blocks_of(K);
+    const int es = elem(dtype), eo = elem(out);
+    const Buf bufs[] = {
+        {X, span(M, ldx, K, es), "X", es, false},
+        {codes, 16ull * N * kb, "codes", 16, false},
+        {scales, (unsigned long long)N * kb, "scales", 1, false},
+        {Y, span(M, ldy, N, eo), "Y", eo, true},
+        {workspace, workspace ? L.total : 0, "workspace", 16, true},
+    };
+    st = check_buffers(bufs, 5);
+    if (st != SAM_OK) return st;
+    if (L.total && (!workspace || workspace_bytes < L.total))
+        return api_fail(SAM_ERR_WORKSPACE, "the call needs %llu workspace bytes, got %llu", L.total,
+                        (unsigned long long)(workspace ? workspace_bytes : 0));
+    st = api_device_check();
+    if (st != SAM_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const Quant4Args q{X, M > 1 ? ldx : K, M, (int)K, (int)kb, (unsigned char*)ws + L.codes.off, (unsigned char*)ws + L.scales.off};
+    const hipError_t e = launch_quant4(dtype, false, q, s);
+    if (e != hipSuccess) return done(e);
+    float* result = reinterpret_cast<float*>(ws + L.result.off);
+    st = sam_gemm_mxfp4(q.codes, q.scales, codes, scales, result, M, N, 32 * kb, L.inner.bytes ? ws + L.inner.off : nullptr,
+                        L.inner.bytes, stream);
+    if (st != SAM_OK) return st;
+    return done(launch_convert4(out, {result, Y, M > 1 ? ldy : N, M, (int)N}, s));
+}
+
+sam_status sam_linear_mxfp4_backward_workspace(sam_dtype dtype, sam_dtype out, int64_t M, int64_t N, int64_t K, uint64_t* bytes)
+{
+    if (!bytes) return api_fail(SAM_ERR_INVALID_ARG, "bytes is null");
+    Layout L;
+    const sam_status st = backward_layout(dtype, out, M, N, K, &L);
+    if (st != SAM_OK) return st;
+    *bytes = L.total;
+    return api_ok();
+}
+
+sam_status sam_linear_mxfp4_backward(sam_dtype dtype, int64_t M, int64_t N, int64_t K, const void* dY, int64_t lddy,
+                                     const uint8_t* codes, const uint8_t* scales, sam_dtype out, void* dX, int64_t lddx,
+                                     void* workspace, uint64_t workspace_bytes, void* stream)
+{
+    Layout L;
+    sam_status st = backward_layout(dtype, out, M, N, K, &L);
+    if (st != SAM_OK) return st;
+    if (M == 0) return api_ok();
+    if (M > 1 && (lddy < N || lddx < K || lddy > kMostRow || lddx > kMostRow))
+        return api_fail(SAM_ERR_INVALID_ARG, "row stride lddy=%lld (rows of %lld) or lddx=%lld (rows of %lld)", (long long)lddy,
+                        (long long)N, (long long)lddx, (long long)K);
+    if (M == 1) lddy = N, lddx = K;
+    const long long kb = blocks_of(K);
+    const int es = elem(dtype), eo = elem(out);
+    const Buf bufs[] = {
+        {dY, span(M, lddy, N, es), "dY", 16, false},
+        {codes, 16ull * N * kb, "codes", 16, false},
+        {scales, (unsigned long long)N * kb, "scales", 1, false},
+        {dX, span(M, lddx, K, eo), "dX", 16, true},
+        {workspace, workspace ? L.total : 0, "workspace", 16, true},
+    };
+    st = check_buffers(bufs, 5);
+    if (st != SAM_OK) return st;
+    if (!workspace || workspace_bytes < L.total)
+        return api_fail(SAM_ERR_WORKSPACE, "the call needs %llu workspace bytes, got %llu", L.total,
+                        (unsigned long long)(workspace ? workspace_bytes : 0));
+    st = api_device_check();
+    if (st != SAM_OK) return st;
+    char* ws = static_cast<char*>(workspace);
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    void* w = ws + L.w.off;
+    const long long row = dtype == SAM_F32 ? (K + 3) / 4 * 4 : (K + 7) / 8 * 8;
+    const hipError_t e = launch_dequant4(dtype, {codes, scales, N, (int)K, (int)kb, w, row}, s);
+    if (e != hipSuccess) return done(e);
+    void* inner = L.inner.bytes ? ws + L.inner.off : nullptr;
+    if (dtype == SAM_F32)
+        return sam_gemm_ex(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, 1.0f, dY, lddy, w, row, 0.0f, static_cast<float*>(dX), lddx,
+                           inner, L.inner.bytes, stream);
+    // The adapters' projection without adapters; ids that it does not look up.
+    return sam_adapter_gemm(dtype, SAM_OP_N, M, K, N, 0, 1, dY, lddy, w, row, nullptr, nullptr,
+                            reinterpret_cast<const int32_t*>(ws + L.ids.off), nullptr, out, dX, lddx, inner, L.inner.bytes, stream);
+}
+
+}  // extern "C"
