@@ -478,6 +478,61 @@ sam_status sam_linear_mxfp4_backward_workspace(sam_dtype dtype, sam_dtype out,
                                                int64_t M, int64_t N, int64_t K,
                                                uint64_t* bytes);
 
+/* Log probabilities of given tokens, with the entropy and the most likely
+ * entries of every row of logits z at temperature T:
+ *   m = max z,  L = log sum_j exp((z_j - m) / T)
+ *   log p_j = (z_j - m) / T - L
+ *   logprob = log p[token],  entropy = - sum_j p_j log p_j
+ *   dtype    SAM_F32, SAM_BF16 or SAM_F16: the logits.
+ *   logits   device, `rows` rows of V values, row stride ldz >= V, aligned to
+ *            one value (rows that start on 16 bytes cost nothing extra).
+ *   tokens   device, `rows` int32; a value outside 0 .. V - 1 names none: that
+ *            row's logprob is 0.
+ *   logprob, entropy  device, `rows` floats.
+ *   norm     device, rows x 2 floats: m and L (log sum exp(z / T) = m / T + L;
+ *            kept apart, so that nothing is lost far from zero).
+ *   top      0 .. 128 and at most V: how many of the row's most likely entries
+ *            are wanted.
+ *   top_logprob, top_index  device, rows x top, compact: log p and index of
+ *            those, the largest logit first, the lowest index first among
+ *            equal ones (the two zeros are equal). NULL with top 0.
+ * Logits of -inf are masked entries: probability 0, log probability -inf,
+ * nothing in the entropy; as most likely entries they come last. A row
+ * without any other has entropy 0, m = L = -inf and log probabilities -inf. A row that
+ * holds NaN or +inf has NaN results, but its top_index are entries all the
+ * same (NaN counts as the largest). V up to 2^31 - 65536, T from 2^-40 to
+ * 2^40; rows == 0 is a no-op. Sums are FP32; no atomics on results, a fixed order. Results
+ * overlap nothing else. Workspace: sam_token_logprobs_workspace() bytes,
+ * SAM_ERR_WORKSPACE when short. Asynchronous on `stream`. */
+sam_status sam_token_logprobs(sam_dtype dtype, int64_t rows, int64_t V,
+                              int64_t top, const void* logits, int64_t ldz,
+                              const int32_t* tokens, float temperature,
+                              float* logprob, float* entropy, float* norm,
+                              float* top_logprob, int32_t* top_index,
+                              void* workspace, uint64_t workspace_bytes,
+                              void* stream);
+
+/* Workspace bytes sam_token_logprobs needs for these arguments (host only). */
+sam_status sam_token_logprobs_workspace(sam_dtype dtype, int64_t rows, int64_t V,
+                                        int64_t top, uint64_t* bytes);
+
+/* Gradient with respect to the logits for given gradients u of logprob and v
+ * of entropy:
+ *   dz_j = (u (1[j = token] - p_j) - v p_j (log p_j + entropy)) / T
+ * norm and entropy are what sam_token_logprobs wrote for the same logits and
+ * temperature; dlogprob and dentropy are `rows` floats or NULL for 0 (entropy
+ * may be NULL where dentropy is). A row without a token takes no u. Masked
+ * entries get 0 (a masked token u / T), and so do the rows of two zero gradients, whatever
+ * their logits hold, and rows of -inf. grad: `rows` rows of V, of the logits'
+ * type, row stride ldg >= V; the logits themselves (same pointer and stride)
+ * or no part of them. */
+sam_status sam_token_logprobs_grad(sam_dtype dtype, int64_t rows, int64_t V,
+                                   const void* logits, int64_t ldz,
+                                   const int32_t* tokens, float temperature,
+                                   const float* norm, const float* entropy,
+                                   const float* dlogprob, const float* dentropy,
+                                   void* grad, int64_t ldg, void* stream);
+
 /* Number of entries in the variant table (ids 0 .. count-1). */
 int32_t sam_variant_count(void);
 

@@ -133,6 +133,11 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_int),
         "sam_linear_mxfp4_backward_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, ctypes.POINTER(u64)],
                                                 ctypes.c_int),
+        "sam_token_logprobs": ([ctypes.c_int, i64, i64, i64, vp, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, u64, vp],
+                               ctypes.c_int),
+        "sam_token_logprobs_workspace": ([ctypes.c_int, i64, i64, i64, ctypes.POINTER(u64)], ctypes.c_int),
+        "sam_token_logprobs_grad": ([ctypes.c_int, i64, i64, vp, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp, i64, vp],
+                                    ctypes.c_int),
         "sam_device_check": ([], ctypes.c_int),
         "sam_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "sam_last_error": ([], ctypes.c_char_p),
@@ -906,3 +911,85 @@ def linear_mxfp4_backward(dY, codes, scales, K=None, dX=None, out_dtype=None, wo
     _check(lib().sam_linear_mxfp4_backward(code, M, N, K, _address(dY), lddy, _address(codes), _address(scales), out,
                                            _address(dX), lddx, _address(workspace), need, _stream_address(stream)))
     return dX
+
+
+# -- log probabilities of given tokens ----------------------------------------------
+def _logits_and_tokens(logits, tokens):
+    import torch
+    code = _value_code(logits, "logits")
+    rows, V, ldz = _matrix(logits, "logits")
+    if tokens.dtype != torch.int32 or tokens.dim() != 1 or tokens.numel() != rows or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous int32 tensor of {rows} (got {tokens.dtype} {tuple(tokens.shape)})")
+    return code, rows, V, ldz
+
+
+def _result(t, shape, dtype, like, name, stream):
+    """t, checked, or (None) a new tensor of this shape beside `like`."""
+    import torch
+    if t is None:
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=like.device)
+        return _new(shape, dtype, like.device, stream)
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor (got {t.dtype} {tuple(t.shape)})")
+    return t
+
+
+@_on_its_gpu
+def token_logprobs(logits, tokens, temperature=1.0, top=0, logprob=None, entropy=None, norm=None, top_logprob=None,
+                   top_index=None, workspace=None, stream=None):
+    """Log probability of every row's token, the row's entropy and its norm
+    (largest logit, log of the sum of exp((z - largest) / temperature)), and
+    with `top` its most likely entries (sam_token_logprobs): (logprob [rows],
+    entropy [rows], norm [rows, 2]), and with top also top_logprob and
+    top_index (int32) [rows, top], most likely first, the lowest index first
+    among equals.
+
+    logits [rows, V] float32, bfloat16 or float16 (a view with padded rows is
+    fine), tokens int32 [rows] (outside 0 .. V-1: none, logprob 0). top_index
+    with top_logprob is what the distillation calls take from a teacher."""
+    import torch
+    code, rows, V, ldz = _logits_and_tokens(logits, tokens)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _one_gpu(("logits", "tokens", "logprob", "entropy", "norm", "top_logprob", "top_index", "workspace"),
+             (logits, tokens, logprob, entropy, norm, top_logprob, top_index, workspace))
+    f32 = torch.float32
+    if workspace is None:
+        need = _adapter_workspace_bytes("sam_token_logprobs_workspace", code, rows, V, top)
+        workspace = _adapter_workspace(need, logits, stream)
+    else:
+        need = _workspace_bytes(workspace)
+    logprob = _result(logprob, (rows,), f32, logits, "logprob", stream)
+    entropy = _result(entropy, (rows,), f32, logits, "entropy", stream)
+    norm = _result(norm, (rows, 2), f32, logits, "norm", stream)
+    if top:
+        top_logprob = _result(top_logprob, (rows, top), f32, logits, "top_logprob", stream)
+        top_index = _result(top_index, (rows, top), torch.int32, logits, "top_index", stream)
+    _check(lib().sam_token_logprobs(code, rows, V, top, _address(logits), ldz, _address(tokens), float(temperature),
+                                    _address(logprob), _address(entropy), _address(norm), _address(top_logprob),
+                                    _address(top_index), _address(workspace), need, _stream_address(stream)))
+    return (logprob, entropy, norm, top_logprob, top_index) if top else (logprob, entropy, norm)
+
+
+@_on_its_gpu
+def token_logprobs_grad(logits, tokens, norm, entropy=None, dlogprob=None, dentropy=None, temperature=1.0, grad=None,
+                        stream=None):
+    """Gradient with respect to the logits for the gradients dlogprob and
+    dentropy (float32 [rows], None: 0) of token_logprobs' results, from its
+    norm and entropy (sam_token_logprobs_grad). grad may be logits itself."""
+    code, rows, V, ldz = _logits_and_tokens(logits, tokens)
+    _one_gpu(("logits", "tokens", "norm", "entropy", "dlogprob", "dentropy", "grad"),
+             (logits, tokens, norm, entropy, dlogprob, dentropy, grad))
+    import torch
+    if norm is None or (dentropy is not None and entropy is None):
+        raise ValueError("norm, and with dentropy entropy, are what token_logprobs returned")
+    _result(norm, (rows, 2), torch.float32, logits, "norm", stream)
+    for t, name in ((entropy, "entropy"), (dlogprob, "dlogprob"), (dentropy, "dentropy")):
+        if t is not None:
+            _result(t, (rows,), torch.float32, logits, name, stream)
+    grad, ldg = _distill_result(grad, logits, V, stream)
+    _check(lib().sam_token_logprobs_grad(code, rows, V, _address(logits), ldz, _address(tokens), float(temperature),
+                                         _address(norm), _address(entropy), _address(dlogprob), _address(dentropy),
+                                         _address(grad), ldg, _stream_address(stream)))
+    return grad
