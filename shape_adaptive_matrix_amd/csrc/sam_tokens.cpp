@@ -66,7 +66,8 @@ sam_status sam_token_logprobs_workspace(sam_dtype dtype, int64_t rows, int64_t V
     if (st != SAM_OK) return st;
     if (top < 0 || top > kMaxAlternatives || top > V)
         return api_fail(SAM_ERR_INVALID_ARG, "top=%lld outside 0 .. %d or over V", (long long)top, kMaxAlternatives);
-    *bytes = 0;
+    const int parts = rows > 0 ? tokens_parts(dtype, rows, V) : 1;
+    *bytes = parts > 1 ? align256(16ull * rows * parts) + 8ull * rows * parts * top : 0;
     return api_ok();
 }
 
@@ -115,6 +116,9 @@ sam_status sam_token_logprobs(sam_dtype dtype, int64_t rows, int64_t V, int64_t 
     a.norm = norm;
     a.top_logprob = top_logprob;
     a.top_index = top_index;
+    a.parts = tokens_parts(dtype, rows, V);
+    if (a.parts > 1) a.part = static_cast<float4*>(workspace);
+    if (a.parts > 1) a.list = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + align256(16ull * rows * a.parts));
     return done(launch_tokens(dtype, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -27,7 +27,16 @@ struct TokenArgs {
     float* norm;           // [rows][2]: m, L
     float* top_logprob;    // [rows][top]
     int* top_index;        // [rows][top]
+    // Rows cut over workgroups: what each leaves of its part of a row, and
+    // then `top` candidates of each, the best first.
+    int parts;
+    float4* part;          // [rows][parts]: m, sum exp, sum of exp times exponent, number of candidates
+    unsigned long long* list;   // [rows][parts][top]
 };
+
+// Workgroups that a row is cut over.
+int tokens_parts(int dtype, long long rows, long long V);
+constexpr int kMaxParts = 64;
 
 struct TokenGradArgs {
     const void* z;
