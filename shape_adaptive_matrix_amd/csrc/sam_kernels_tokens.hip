@@ -5,18 +5,18 @@
 // exponentials and the sum of these times their exponents (for the entropy),
 // and finds the most likely entries on the way:
 //
-//  * Of the first segment of a row (what the workgroup's registers hold) each
-//    thread has its largest value. The top-th largest of these, found by one
-//    wave bit by bit while the others add up exponentials, is a lower bound
-//    for the row's top-th largest value, and few values reach it.
-//  * Those go to a list in LDS, later segments' too. A list that fills up
-//    (more alternatives than a segment gives, many equal values) is cut to its
-//    best `top` and the bound with it; a segment that does not fit in one go
-//    is taken again, a value a thread at a time.
-//  * Entries are compared as 64-bit numbers, the value's order above the
-//    index's complement: all different, so that the order in which they
-//    reached the list does not matter. An entry's place among the results is
+//  * Every thread keeps, in 16 bits each, the largest value of its 16-byte
+//    pieces (of rows too long for that, of four pieces). Behind the row the
+//    top-th largest of the threads' own largest values, found bit by bit, is a
+//    lower bound of the row's top-th largest value that few pieces reach.
+//  * Those pieces are read again (of 32768 values and 64 alternatives about 75
+//    of 4096) and their values over the bound compared as 64-bit numbers, the
+//    value's order above the index's complement: all different, so that their
+//    order in the list does not matter. An entry's place among the results is
 //    how many are larger.
+//  * Rows with more such pieces or values than fit (equal values) are taken
+//    again from the front, a piece a thread at a time, through a list that is
+//    cut to its best whenever it could not take the next.
 #include "sam_rows.h"
 #include "sam_tokens.h"
 
@@ -27,7 +27,8 @@ namespace {
 using namespace rows;
 typedef unsigned long long u64;
 
-constexpr int kList = 1536;             // candidates of a workgroup
+constexpr int kEntries = 512;           // entries whose places are found by comparing all with all
+constexpr float kLowest = -3.402823466e38f;
 constexpr float kLn2 = 0.693147180559945f;
 
 // Whole numbers that order values: NaN above all, the two zeros equal.
@@ -61,6 +62,11 @@ __device__ __forceinline__ float max_of(const float (&v)[E], float m)
     for (int i = 0; i < E; i += 2) m = max3(m, v[i], v[i + 1]);
     return m;
 }
+
+// The register as it is, not what an earlier use made of it: without it the
+// compiler keeps 16-bit rows as floats from one use to the next, twice the
+// registers.
+__device__ __forceinline__ void as_read(u4& x) { asm volatile("" : "+v"(x)); }
 
 // Sums over some values relative to their largest, m: s of 2^d and h of d
 // 2^d, d = (z - m) log2(e) / T.
@@ -103,49 +109,63 @@ __device__ __forceinline__ void write_row(const TokenArgs& a, long long row, con
     a.norm[2 * row + 1] = L;
 }
 
-// The workgroup's list in LDS cut to its `top` best: the bits of the top-th
-// largest entry are found one by one, until exactly `top` are as large.
-// Returns a bound that the kept entries reach. n > top entries; every thread
-// calls it, and the list's last use lies behind a barrier.
-template <int NT, int CAP>
-__device__ u64 cut_list(u64* list, int* count, int n, int top)
+// An LDS barrier that leaves global loads under way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ int lanes_below(u64 who)
 {
-    __shared__ int more[NT / 64];
-    constexpr int EACH = (CAP + NT - 1) / NT;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    u64 own[EACH];
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) own[i] = (int)threadIdx.x + i * NT < n ? list[threadIdx.x + i * NT] : 0;
+    return __builtin_amdgcn_mbcnt_hi((unsigned)(who >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)who, 0));
+}
+
+// The top-th largest of the numbers that the workgroup's threads hold, G each
+// (zero: none): bit by bit, until exactly `top` are as large; zero with fewer.
+// `count`: LDS for a number a wave.
+template <int NT, int G>
+__device__ __forceinline__ u64 bound_together(const u64 (&own)[G], int top, int* count)
+{
     u64 bound = 0;
     for (int bit = 63; bit >= 0; --bit) {
         const u64 t = bound | 1ull << bit;
         int c = 0;
 #pragma unroll
-        for (int i = 0; i < EACH; ++i) c += __popcll(__ballot(own[i] >= t));
-        if (lane == 0) more[wave] = c;
-        __syncthreads();
-        int total = 0;
+        for (int i = 0; i < G; ++i) c += __popcll(__ballot(own[i] >= t));
+        lds_barrier();
+        if ((threadIdx.x & 63) == 0) count[threadIdx.x >> 6] = c;
+        lds_barrier();
+        c = 0;
 #pragma unroll
-        for (int w = 0; w < NT / 64; ++w) total += more[w];
-        if (total >= top) bound = t;
-        __syncthreads();
-        if (total == top) break;
+        for (int w = 0; w < NT / 64; ++w) c += count[w];
+        if (c >= top) bound = t;
+        if (c == top) break;
     }
-    if (threadIdx.x == 0) *count = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < EACH; ++i)
-        if (own[i] && own[i] >= bound) list[atomicAdd(count, 1)] = own[i];
-    __syncthreads();
     return bound;
 }
 
-// How many of a list's n entries are larger than e.
+// How many of a list's n entries are larger than e. What lies behind them, up
+// to a multiple of eight, is read and dropped.
 __device__ __forceinline__ int larger(const u64* list, int n, u64 e)
 {
     int r = 0;
-    for (int j = 0; j < n; ++j) r += list[j] > e;
+    for (int j = 0; j < n; j += 8) {
+        u64 o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = list[j + i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r += o[i] > e && j + i < n;
+    }
     return r;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int sum_up_to(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // from 1, 2, 4, 8 lanes below
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // lane 15 of the row below
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31
+    return v;
 }
 
 __device__ __forceinline__ void write_entry(const TokenArgs& a, long long row, int place, u64 e, float m, float L)
@@ -171,17 +191,48 @@ __device__ __forceinline__ void write_masked(const TokenArgs& a, long long row, 
     }
 }
 
-// A row, or a part of one (a.parts > 1), on NT threads that hold P pieces each.
+// A lower bound of the top-th largest of 64 G values, by the upper 16 bits of
+// numbers that order them (G a lane; zero: none), found by one wave.
+template <int G>
+__device__ __forceinline__ float bound_of(const unsigned (&k)[G], int top)
+{
+    unsigned hi = k[0], lo = k[0];
+#pragma unroll
+    for (int i = 1; i < G; ++i) {
+        hi = max(hi, k[i]);
+        lo = min(lo, k[i]);
+    }
+    // The bits that all have in common need no search.
+    hi = (unsigned)wave_max((float)hi);
+    lo = (unsigned)-wave_max(-(float)lo);
+    unsigned bit = hi == lo ? 0 : 1u << (31 - __builtin_clz(hi ^ lo));
+    unsigned t = bit ? hi & ~(2 * bit - 1) : hi;
+    for (; bit; bit >>= 1) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i) c += __popcll(__ballot(k[i] >= (t | bit)));
+        t = c >= top ? t | bit : t;
+    }
+    return t <= 0x7F ? kLowest : value_of(t << 16);   // values of -inf are no candidates
+}
+
+// A row, or a part of one (a.parts > 1), on NT threads that hold P pieces
+// each of it, and the next P on the way.
 template <int DT, int NT, int P, bool TOP>
-__global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6 : 8))) tokens_kernel(TokenArgs a)
 {
     typedef Piece<DT> Pc;
     typedef typename Pc::T T;
-    constexpr int E = Pc::E, NW = NT / 64;
-    __shared__ u64 list[TOP ? kList : 1];
-    __shared__ unsigned short best[TOP ? NT : 1];
-    __shared__ int count;
-    __shared__ float bound_s;
+    constexpr int E = Pc::E, NW = NT / 64, FINE = 32 / P;   // segments whose pieces each have a bit of 32
+    static_assert(P == 4 && FINE * P == 32, "a thread's pieces, or groups of segments, are 32 bits");
+    // The pieces' largest values, [segment][thread][P], or those of `step`
+    // segments, [.][thread];
+    // entries; and in the place of both the list of the long way.
+    constexpr int KEYS = 32 * NT / 4, LIST = NT * E + kEntries;
+    constexpr int ROOM = KEYS + kEntries > LIST ? KEYS + kEntries : LIST;
+    __shared__ __attribute__((aligned(16))) u64 room[TOP ? ROOM + 8 : 1];
+    __shared__ unsigned short ids[TOP ? kEntries : 1], best[TOP ? NT : 1];
+    __shared__ int counts[NW], pieces_found, entries;
     __shared__ Sums wave_sums[NW];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -190,8 +241,19 @@ __global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
     const T* z = static_cast<const T*>(a.z) + row * a.ldz;
     const Span sp = span_of<DT>(z, a.V);
     const u4* zb = reinterpret_cast<const u4*>(z + sp.head);
-    const int each = a.parts == 1 ? sp.pieces : (sp.pieces / a.parts + 64) & ~63;
+    const int each = (sp.pieces + a.parts - 1) / a.parts;
     const int p0 = min(part * each, sp.pieces), p1 = min(p0 + each, sp.pieces);
+    const int segments = (p1 - p0 + NT * P - 1) / (NT * P);
+    const bool fine = segments <= FINE;
+    const int step = fine ? 1 : (segments + 31) / 32;   // segments that share a bit
+
+    u4 r[2][P];
+    auto fetch = [&](u4 (&x)[P], int seg) {   // past the part's end: zeros, and no traffic
+        const __amdgpu_buffer_rsrc_t rs = dma::make_rsrc(zb + seg, seg < p1 ? 16ll * (p1 - seg) : 0);
+#pragma unroll
+        for (int q = 0; q < P; ++q) x[q] = __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, q * NT * 16, kOnce);
+    };
+    fetch(r[0], p0);
 
     // The first part takes the values outside the pieces, one a thread, and
     // the row's token.
@@ -202,29 +264,16 @@ __global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
     }
     const float edge = edge_at >= 0 ? (float)z[edge_at] : -INFINITY;
     float z_token = 0.0f;
-    if (a.parts == 1 && tid == 0) {
+    if (part == 0 && tid == 0) {
         const int t = a.token[row];
         z_token = (float)z[(unsigned)t < (unsigned)a.V ? t : 0];
     }
     Sums x = {edge, edge == -INFINITY ? 0.0f : 1.0f + (edge - edge), 0.0f};   // NaN for an Inf or NaN
 
-    int n = 0;             // candidates
-    u64 least = 0;         // entries under it are out
-    float bound = 0.0f;    // ... and values
-    if (TOP && tid == 0) count = 0;
-    auto push = [&](float v, int index) {
-        const u64 e = entry_of(v, index);
-        if (e >= least) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kList) list[at] = e;
-        }
-    };
-
-    for (int seg = p0; seg < p1 || seg == p0; seg += NT * P) {
-        u4 r[P];
-        const __amdgpu_buffer_rsrc_t rs = dma::make_rsrc(zb + seg, 16ll * (p1 - seg));
-#pragma unroll
-        for (int q = 0; q < P; ++q) r[q] = __builtin_amdgcn_raw_buffer_load_b128(rs, tid * 16, q * NT * 16, kOnce);
+    float so_far = -INFINITY;   // of the segments that share a bit
+    auto segment = [&](u4 (&r)[P], u4 (&next)[P], int at) {
+        const int seg = p0 + at * (NT * P);
+        fetch(next, seg + NT * P);
         if (seg + NT * P > p1) {   // the part's end: nothing there
 #pragma unroll
             for (int q = 0; q < P; ++q)
@@ -236,53 +285,37 @@ __global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
             float v[E];
             Pc::get(r[q], v);
             pm[q] = max_of(v, -INFINITY);
-            tm = fmaxf(tm, pm[q]);
         }
-        const bool select = TOP && n < a.top;
-        if (select) {
-            best[tid] = (unsigned short)(order_of(fmaxf(tm, seg == p0 ? edge : -INFINITY)) >> 16);
-            __syncthreads();
-            if (wave == 0) {
-                unsigned k[NW], t = 0;
+        tm = max3(max3(pm[0], pm[1], pm[2]), pm[3], tm);
 #pragma unroll
-                for (int i = 0; i < NW; ++i) k[i] = best[lane + 64 * i];
-#pragma unroll
-                for (int bit = 15; bit >= 0; --bit) {
-                    int c = 0;
-#pragma unroll
-                    for (int i = 0; i < NW; ++i) c += __popcll(__ballot(k[i] >= (t | 1u << bit)));
-                    if (c >= a.top) t |= 1u << bit;
-                }
-                // Values of -inf are no candidates.
-                if (lane == 0) bound_s = t <= 0x7F ? -3.402823466e38f : value_of(t << 16);
-            }
-        }
+        for (int q = 0; q < P; ++q) as_read(r[q]);
 
         // The segment's sums, relative to the thread's largest value so far.
-        if (tm > x.m || x.s == 0.0f) {
-            const float M = fmaxf(tm, x.m);
-            to_largest(x, M, a.scale);
-        }
+        if (tm > x.m || x.s == 0.0f) to_largest(x, fmaxf(tm, x.m), a.scale);
         const float pivot = x.m == -INFINITY ? 0.0f : x.m, c = pivot * a.scale;
         float s = 0.0f, h = 0.0f;
-        if (!__any(!(fabsf(c) <= 16384.0f))) {
-            // d = z scale - c in one operation. c is rounded: all exponents
-            // are off by the same, which is taken out of the sums.
+        // d = z scale - c in one operation. c is rounded: all exponents are
+        // off by the same, which is taken out of the sums.
 #pragma unroll
-            for (int q = 0; q < P; ++q) {
-                float v[E];
-                Pc::get(r[q], v);
+        for (int q = 0; q < P; ++q) {
+            float v[E];
+            Pc::get(r[q], v);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float d = __fmaf_rn(v[i], a.scale, -c), e = pow2(d);
-                    s += e;
-                    h = __fmaf_rn(e, fmaxf(d, -1000.0f), h);
-                }
+            for (int i = 0; i < E; ++i) {
+                const float d = __fmaf_rn(v[i], a.scale, -c), e = pow2(d);
+                s += e;
+                h = __fmaf_rn(e, d, h);
             }
-            const float off = __fmaf_rn(pivot, a.scale, -c), g = pow2(-off);
-            h = g * (h - off * s);
-            s *= g;
-        } else {
+        }
+        const float off = __fmaf_rn(pivot, a.scale, -c), g = pow2(-off);
+        h = g * (h - off * s);
+        s *= g;
+        // Not so with values of -inf (whose 0 times -inf should be 0) and far
+        // from zero: once more.
+        if (__any(h != h || !(fabsf(c) <= 16384.0f))) {
+#pragma unroll
+            for (int q = 0; q < P; ++q) as_read(r[q]);
+            s = h = 0.0f;
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 float v[E];
@@ -297,61 +330,38 @@ __global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
         }
         x.s += s;
         x.h += h;
-
         if constexpr (TOP) {
-            if (select) {
-                __syncthreads();
-                bound = fmaxf(bound_s, n ? bound : bound_s);
-            }
-            const bool odd = x.s != x.s;   // NaN among the values: pieces' largest do not show it
-            if (seg == p0 && edge_at >= 0 && edge != -INFINITY && !(edge < bound)) push(edge, edge_at);
+            // NaN among the values does not show in their largest: a NaN.
+            const bool odd = x.s != x.s;
+            unsigned k[P];
 #pragma unroll
-            for (int q = 0; q < P; ++q) {
-                if (pm[q] < bound && !odd) continue;
-                float v[E];
-                Pc::get(r[q], v);
-#pragma unroll
-                for (int i = 0; i < E; ++i)
-                    if (!(v[i] < bound)) push(v[i], sp.head + (seg + q * NT + tid) * E + i);
+            for (int q = 0; q < P; ++q) k[q] = odd ? 0x7FC00000u : __float_as_uint(pm[q]);
+            if (fine) {
+                reinterpret_cast<uint2*>(room)[at * NT + tid] = make_uint2(__builtin_amdgcn_perm(k[1], k[0], 0x07060302u),
+                                                                           __builtin_amdgcn_perm(k[3], k[2], 0x07060302u));
+            } else {
+                const int group = at / step;
+                so_far = group * step == at ? tm : fmaxf(so_far, tm);
+                reinterpret_cast<unsigned short*>(room)[group * NT + tid] = odd ? 0x7FC0 : (unsigned short)(__float_as_uint(so_far) >> 16);
             }
-            __syncthreads();
-            int now = count;
-            __syncthreads();
-            if (now > kList) {
-                // Too many at once: the segment again, a value a thread at a
-                // time, and the list cut whenever it could not take the next.
-                if (tid == 0) count = n;
-                __syncthreads();
-                if (seg == p0 && edge_at >= 0 && edge != -INFINITY) push(edge, edge_at);
-                for (int i = 0; i < P * E; ++i) {
-                    const int piece = seg + i / E * NT + tid;
-                    if (piece < p1) {
-                        const int index = sp.head + piece * E + i % E;
-                        const float v = (float)z[index];
-                        if (v != -INFINITY) push(v, index);
-                    }
-                    __syncthreads();
-                    now = count;
-                    __syncthreads();
-                    if (now + NT > kList) {
-                        least = cut_list<NT, kList>(list, &count, now, a.top);
-                        now = a.top;
-                    }
-                }
-            }
-            n = now;
-            if (n > kList / 2) {
-                least = cut_list<NT, kList>(list, &count, n, a.top);
-                n = a.top;
-            }
-            if (least) bound = fmaxf(bound, value_of((unsigned)(least >> 32)));
         }
+    };
+    int at = 0;
+#pragma clang loop unroll(disable)
+    for (; at + 2 <= segments; at += 2) {
+        segment(r[0], r[1], at);
+        segment(r[1], r[0], at + 1);
     }
+    if (at < segments) segment(r[0], r[1], at);
 
+    if constexpr (TOP) {
+        best[tid] = x.s != x.s ? 0xFFFF : (unsigned short)(order_of(x.m) >> 16);
+        if (tid == 0) pieces_found = entries = 0;
+    }
     x = wave_total(x, a.scale);
-    if (NW > 1) {
+    if (NW > 1 || TOP) {
         if (lane == 0) wave_sums[wave] = x;
-        __syncthreads();
+        lds_barrier();
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, wave_sums[w].m);
@@ -365,29 +375,132 @@ __global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
         }
         x = all;
     }
-    if (TOP && n > kList / 4) {
-        cut_list<NT, kList>(list, &count, n, a.top);
-        n = a.top;
-    }
-    if (a.parts > 1) {
-        const long long at = row * a.parts + part;
-        if (tid == 0) a.part[at] = make_float4(x.m, x.s, x.h, __int_as_float(min(n, a.top)));
-        if constexpr (TOP) {
-            for (int i = tid; i < n; i += NT) {
-                const int place = larger(list, n, list[i]);
-                if (place < a.top) a.list[at * a.top + place] = list[i];
+    const float L = logf(x.s);
+    int total = 0;
+    if constexpr (TOP) {
+        u64* list = room + KEYS;
+        float bound;
+        {
+            unsigned k[NW];
+#pragma unroll
+            for (int i = 0; i < NW; ++i) k[i] = best[lane + 64 * i];
+            bound = bound_of(k, a.top);   // every wave the same
+        }
+        // A bit for each of the thread's pieces (segments) that reach it.
+        unsigned mine = 0;
+        for (int s = 0; s * step < segments; ++s) {
+            auto reaches = [&](unsigned upper) { return !(__uint_as_float(upper) < bound) ? 1u : 0u; };
+            if (fine) {
+                const uint2 k = reinterpret_cast<const uint2*>(room)[s * NT + tid];
+                mine |= (reaches(k.x << 16) | reaches(k.x & 0xFFFF0000u) << 1 | reaches(k.y << 16) << 2 |
+                         reaches(k.y & 0xFFFF0000u) << 3) << (4 * s);
+            } else {
+                mine |= reaches((unsigned)reinterpret_cast<const unsigned short*>(room)[s * NT + tid] << 16) << s;
             }
         }
-        return;
-    }
-    const float L = logf(x.s);
-    if (tid == 0) write_row(a, row, x, L, z_token);
-    if constexpr (TOP) {
-        for (int i = tid; i < n; i += NT) {
-            const int place = larger(list, n, list[i]);
-            if (place < a.top) write_entry(a, row, place, list[i], x.m, L);
+        // A place for each of `n` of every lane, counted in `count`.
+        auto places = [&](int n, int* count) {
+            const int up = sum_up_to(n);
+            int to = 0;
+            if (lane == 63 && up) to = atomicAdd(count, up);
+            return __builtin_amdgcn_readlane(to, 63) + up - n;
+        };
+        {
+            int to = places(__popc(mine), &pieces_found);
+            for (; mine; mine &= mine - 1, ++to)
+                if (to < kEntries) ids[to] = (unsigned short)((__ffs(mine) - 1) * NT + tid);
         }
-        if (n < a.top && wave == 0) write_masked<DT>(a, row, n, x.m, L);
+        lds_barrier();
+        const int found = pieces_found;
+        auto taken = [&](float v) { return v != -INFINITY && !(v < bound); };
+        if (found <= kEntries) {
+            const int per = fine ? 1 : P * step, items = found * per;
+            for (int i0 = 0; i0 < items || i0 == 0; i0 += NT) {
+                const int i = i0 + tid;
+                u4 d = Pc::masked();
+                int index = 0;
+                if (i < items) {
+                    const int id = ids[i / per], bit = id / NT, rest = i % per;
+                    const int at = fine ? bit / P : bit * step + rest / P, q = fine ? bit % P : rest % P;
+                    const int piece = p0 + at * (NT * P) + q * NT + id % NT;
+                    if (piece < p1) {
+                        d = zb[piece];
+                        index = sp.head + piece * E;
+                    }
+                }
+                float v[E];
+                Pc::get(d, v);
+                int n = i0 == 0 && edge_at >= 0 && taken(edge) ? 1 : 0;
+                const int edges = n;
+#pragma unroll
+                for (int j = 0; j < E; ++j) n += taken(v[j]);
+                int to = places(n, &entries);
+                if (n) {
+                    if (edges && to < kEntries) list[to] = entry_of(edge, edge_at);
+                    to += edges;
+#pragma unroll
+                    for (int j = 0; j < E; ++j) {
+                        if (taken(v[j]) && to < kEntries) list[to] = entry_of(v[j], index + j);
+                        to += taken(v[j]);
+                    }
+                }
+            }
+            lds_barrier();
+            total = entries;
+        }
+        if (found > kEntries || total > kEntries) {
+            list = room;
+            u64 least = 0;
+            lds_barrier();
+            if (tid == 0) entries = 0;
+            lds_barrier();
+            auto push = [&](float v, int index) {
+                const u64 e = entry_of(v, index);
+                if (v != -INFINITY && e >= least) list[atomicAdd(&entries, 1)] = e;
+            };
+            if (edge_at >= 0) push(edge, edge_at);
+            for (int p = p0; p < p1; p += NT) {
+                if (p + tid < p1) {
+                    float v[E];
+                    Pc::get(zb[p + tid], v);
+#pragma unroll
+                    for (int j = 0; j < E; ++j) push(v[j], sp.head + (p + tid) * E + j);
+                }
+                lds_barrier();
+                total = entries;
+                lds_barrier();
+                if (total <= kEntries - 2 * E) continue;   // room for a step's and the edges'
+                constexpr int G = (LIST + NT - 1) / NT;
+                u64 own[G];
+#pragma unroll
+                for (int i = 0; i < G; ++i) own[i] = tid + i * NT < total ? list[tid + i * NT] : 0;
+                least = bound_together<NT>(own, a.top, counts);
+                if (tid == 0) entries = 0;
+                lds_barrier();
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    if (own[i] && own[i] >= least) list[atomicAdd(&entries, 1)] = own[i];
+                lds_barrier();
+                total = entries;
+            }
+        }
+        const long long out = row * a.parts + part;
+        for (int i = tid; i < total; i += NT) {
+            const u64 e = list[i];
+            const int place = larger(list, total, e);
+            if (place >= a.top) continue;
+            if (a.parts > 1) a.list[out * a.top + place] = e;
+            else write_entry(a, row, place, e, x.m, L);
+        }
+        if (a.parts == 1 && total < a.top && wave == 0) write_masked<DT>(a, row, total, x.m, L);
+    }
+    if (tid == 0) {
+        if (a.parts == 1) {
+            write_row(a, row, x, L, z_token);
+        } else {
+            a.part[row * a.parts + part] = make_float4(x.m, x.s, x.h, __int_as_float(min(total, a.top)));
+            if (part == 0) a.z_token[row] = z_token;
+        }
     }
 }
 
@@ -397,26 +510,23 @@ __global__ void __launch_bounds__(NT) tokens_kernel(TokenArgs a)
 template <int DT, bool TOP>
 __global__ void __launch_bounds__(256) tokens_join_kernel(TokenArgs a)
 {
-    typedef typename Ty<DT>::T T;
-    constexpr int NT = 256, CAP = TOP ? kMaxParts * kMaxAlternatives : 1;
-    __shared__ u64 list[CAP];
+    constexpr int CAP = TOP ? kMaxParts * kMaxAlternatives : 1;
+    __shared__ __attribute__((aligned(16))) u64 list[CAP + 8];
     __shared__ int count, held[kMaxParts];
     const int tid = threadIdx.x, lane = tid & 63;
     const long long row = blockIdx.x;
-    const int t = a.token[row];
-    const float z_token = (float)(static_cast<const T*>(a.z) + row * a.ldz)[(unsigned)t < (unsigned)a.V ? t : 0];
     const float4 mine = lane < a.parts ? a.part[row * a.parts + lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    const float z_token = a.z_token[row];
+    const int have = __float_as_int(mine.w);
+    const u64* from = a.list + row * a.parts * a.top;
     const Sums x = wave_total({mine.x, mine.y, mine.z}, a.scale);   // every wave the same
     const float L = logf(x.s);
-    if (tid == 0) write_row(a, row, x, L, z_token);
     if constexpr (TOP) {
-        const int have = __float_as_int(mine.w);
-        const u64* from = a.list + row * a.parts * a.top;
-        const int full = __popcll(__ballot(lane < a.parts && have == a.top));
+        const bool is_full = lane < a.parts && have == a.top;
+        const int full = __popcll(__ballot(is_full));
         u64 least = 0;
         if (full) {
-            const int at = (a.top + full - 1) / full - 1;
-            u64 e = lane < a.parts && have == a.top ? from[lane * a.top + at] : ~0ull;
+            u64 e = is_full ? from[lane * a.top + (a.top + full - 1) / full - 1] : ~0ull;
 #pragma unroll
             for (int d = 32; d; d >>= 1) {
                 const u64 o = __shfl_xor(e, d);
@@ -426,25 +536,41 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(TokenArgs a)
         }
         if (tid == 0) count = 0;
         if (tid < 64) held[lane] = have;
-        __syncthreads();
-        for (int i = tid; i < a.parts * a.top; i += NT) {
-            const int s = i / a.top, k = i - s * a.top;
-            const u64 e = k < held[s] ? from[i] : 0;
-            if (e && e >= least) list[atomicAdd(&count, 1)] = e;
+        lds_barrier();
+        for (int i = tid; i < a.parts * a.top; i += 256) {
+            const int s = i / a.top;
+            const u64 e = i - s * a.top < held[s] ? from[i] : 0;
+            const u64 who = __ballot(e && e >= least);
+            int at = 0;
+            if (lane == __ffsll(who) - 1) at = atomicAdd(&count, __popcll(who));
+            at = __shfl(at, __ffsll(who) - 1);
+            if (e && e >= least) list[at + lanes_below(who)] = e;
         }
-        __syncthreads();
+        lds_barrier();
         int n = count;
-        __syncthreads();
-        if (n > kList / 4) {
-            cut_list<NT, CAP>(list, &count, n, a.top);
-            n = min(n, a.top);
+        if (n > kEntries) {   // the best lie in few parts
+            __shared__ int counts[4];
+            constexpr int G = (CAP + 255) / 256;
+            u64 own[G];
+#pragma unroll
+            for (int i = 0; i < G; ++i) own[i] = tid + 256 * i < n ? list[tid + 256 * i] : 0;
+            const u64 last = bound_together<256>(own, a.top, counts);
+            if (tid == 0) count = 0;
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (own[i] && own[i] >= last) list[atomicAdd(&count, 1)] = own[i];
+            lds_barrier();
+            n = count;
         }
-        for (int i = tid; i < n; i += NT) {
-            const int place = larger(list, n, list[i]);
-            if (place < a.top) write_entry(a, row, place, list[i], x.m, L);
+        for (int i = tid; i < n; i += 256) {
+            const u64 e = list[i];
+            const int place = larger(list, n, e);
+            if (place < a.top) write_entry(a, row, place, e, x.m, L);
         }
         if (n < a.top && tid < 64) write_masked<DT>(a, row, n, x.m, L);
     }
+    if (tid == 0) write_row(a, row, x, L, z_token);
 }
 
 // A strip of a row on a workgroup. Pieces are whole in the gradient's memory;
@@ -527,21 +653,18 @@ __global__ void __launch_bounds__(kStripThreads) tokens_grad_kernel(TokenGradArg
     }
 }
 
-struct Form {
-    int nt, p;
-};
-
 template <int DT, bool TOP>
 hipError_t run(const TokenArgs& a, hipStream_t s)
 {
     const unsigned grid = (unsigned)(a.rows * a.parts);
     const long long bytes = (long long)a.V * (DT == DT_F32 ? 4 : 2) / a.parts;
-    if (!TOP && bytes <= 4096)
-        hipLaunchKernelGGL((tokens_kernel<DT, 64, 4, TOP>), dim3(grid), dim3(64), 0, s, a);
-    else if (bytes <= 32768)
-        hipLaunchKernelGGL((tokens_kernel<DT, 256, 8, TOP>), dim3(grid), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((tokens_kernel<DT, 512, 8, TOP>), dim3(grid), dim3(512), 0, s, a);
+    if constexpr (!TOP) {
+        if (bytes <= 4096) {
+            hipLaunchKernelGGL((tokens_kernel<DT, 64, 4, TOP>), dim3(grid), dim3(64), 0, s, a);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((tokens_kernel<DT, 256, 4, TOP>), dim3(grid), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     hipLaunchKernelGGL((tokens_join_kernel<DT, TOP>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
@@ -550,12 +673,13 @@ hipError_t run(const TokenArgs& a, hipStream_t s)
 
 }  // namespace
 
-// Rows for fewer than two workgroups a CU are cut, into parts of 16 KB at least.
+// Rows for fewer than two workgroups a CU are cut, into parts of 16 KB at
+// least.
 int tokens_parts(int dtype, long long rows, long long V)
 {
     const long long bytes = V * (dtype == DT_F32 ? 4 : 2);
-    long long p = 512 / rows;
     const long long most = bytes / 16384;
+    long long p = 512 / rows;
     p = p > most ? most : p;
     p = p > kMaxParts ? kMaxParts : p;
     return p < 2 ? 1 : (int)p;

@@ -67,7 +67,7 @@ sam_status sam_token_logprobs_workspace(sam_dtype dtype, int64_t rows, int64_t V
     if (top < 0 || top > kMaxAlternatives || top > V)
         return api_fail(SAM_ERR_INVALID_ARG, "top=%lld outside 0 .. %d or over V", (long long)top, kMaxAlternatives);
     const int parts = rows > 0 ? tokens_parts(dtype, rows, V) : 1;
-    *bytes = parts > 1 ? align256(16ull * rows * parts) + 8ull * rows * parts * top : 0;
+    *bytes = parts > 1 ? align256(16ull * rows * parts) + align256(4ull * rows) + 8ull * rows * parts * top : 0;
     return api_ok();
 }
 
@@ -117,8 +117,13 @@ sam_status sam_token_logprobs(sam_dtype dtype, int64_t rows, int64_t V, int64_t 
     a.top_logprob = top_logprob;
     a.top_index = top_index;
     a.parts = tokens_parts(dtype, rows, V);
-    if (a.parts > 1) a.part = static_cast<float4*>(workspace);
-    if (a.parts > 1) a.list = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + align256(16ull * rows * a.parts));
+    if (a.parts > 1) {
+        char* ws = static_cast<char*>(workspace);
+        a.part = reinterpret_cast<float4*>(ws);
+        ws += align256(16ull * rows * a.parts);
+        a.z_token = reinterpret_cast<float*>(ws);
+        a.list = reinterpret_cast<unsigned long long*>(ws + align256(4ull * rows));
+    }
     return done(launch_tokens(dtype, a, static_cast<hipStream_t>(stream)));
 }
 

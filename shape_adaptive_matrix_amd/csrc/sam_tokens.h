@@ -31,6 +31,7 @@ struct TokenArgs {
     // then `top` candidates of each, the best first.
     int parts;
     float4* part;          // [rows][parts]: m, sum exp, sum of exp times exponent, number of candidates
+    float* z_token;        // [rows]: the token's logit
     unsigned long long* list;   // [rows][parts][top]
 };
 
