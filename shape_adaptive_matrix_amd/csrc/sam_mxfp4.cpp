@@ -97,6 +97,13 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
     *L = Layout{};
     if (M == 0) return SAM_OK;
     const long long kb = blocks_of(K);
+    if (stream4_takes(M, kb)) {
+        if (!stream4_rounds(M, kb)) {
+            L->take(L->codes, 16ull * M * kb);
+            L->take(L->scales, (unsigned long long)M * kb);
+        }
+        return SAM_OK;
+    }
     if (!plan_auto(M, N, 32 * kb, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
     L->take(L->codes, 16ull * M * kb);
     L->take(L->scales, (unsigned long long)M * kb);
@@ -220,9 +227,28 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     if (st != SAM_OK) return st;
     char* ws = static_cast<char*>(workspace);
     const hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool few = stream4_takes(M, kb), rounds = few && L.codes.bytes == 0;
     const Quant4Args q{X, M > 1 ? ldx : K, M, (int)K, (int)kb, (unsigned char*)ws + L.codes.off, (unsigned char*)ws + L.scales.off};
-    const hipError_t e = launch_quant4(dtype, false, q, s);
-    if (e != hipSuccess) return done(e);
+    if (!rounds) {
+        const hipError_t e = launch_quant4(dtype, false, q, s);
+        if (e != hipSuccess) return done(e);
+    }
+    if (few) {
+        Stream4Args a{};
+        a.x = q.x;
+        a.ldx = q.ldx;
+        if (!rounds) a.xc = q.codes, a.xs = q.scales;
+        a.codes = codes;
+        a.scales = scales;
+        a.M = (int)M;
+        a.N = (int)N;
+        a.K = (int)K;
+        a.kb = (int)kb;
+        a.y = Y;
+        a.ldy = M > 1 ? ldy : N;
+        a.out = out;
+        return done(launch_stream4(dtype, a, s));
+    }
     float* result = reinterpret_cast<float*>(ws + L.result.off);
     st = sam_gemm_mxfp4(q.codes, q.scales, codes, scales, result, M, N, 32 * kb, L.inner.bytes ? ws + L.inner.off : nullptr,
                         L.inner.bytes, stream);

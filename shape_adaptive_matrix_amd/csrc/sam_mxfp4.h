@@ -39,6 +39,28 @@ struct Convert4Args {
     int cols;
 };
 
+// Y = q(X) Wq^T for few rows, W streamed past them.
+struct Stream4Args {
+    const void* x;                  // M rows of K, stride ldx, rounded on the way; or
+    long long ldx;
+    const unsigned char* xc;        // ... their codes (M x kb x 16)
+    const unsigned char* xs;        // and scales (M x kb)
+    const unsigned char* codes;     // N x kb x 16
+    const unsigned char* scales;    // N x kb
+    int M, N, K, kb;
+    void* y;                        // M rows of N, stride ldy
+    long long ldy;
+    int out;                        // type of y
+};
+
+// Whether the streaming kernels take M rows of kb blocks: up to 32, or 64
+// whose codes fit into LDS (read from memory, 48 rows of 11008 values take as
+// long as through the tiles).
+bool stream4_takes(long long M, long long kb);
+// Whether the rows are rounded in the product's own launch (xc, xs unused).
+bool stream4_rounds(long long M, long long kb);
+hipError_t launch_stream4(int dtype, const Stream4Args& a, hipStream_t s);
+
 hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t s);
 hipError_t launch_dequant4(int dtype, const Dequant4Args& a, hipStream_t s);
 hipError_t launch_convert4(int dtype, const Convert4Args& a, hipStream_t s);
