@@ -443,8 +443,8 @@ sam_status sam_dequantize_mxfp4(sam_dtype dtype, int64_t rows, int64_t K,
  *   out     the type of Y: SAM_F32 or dtype.
  *   Y       device, M rows of N values, row stride ldy >= N; write-only.
  * X and Y are aligned to one value. A block of X or of the weight that stands
- * for NaN makes the results of its row (of its column) NaN. N, K >= 1 and up
- * to 2.08 M; M == 0 is a no-op; a single row's stride may be any. Y overlaps
+ * for NaN makes the results of its row (of its column) NaN. N, K >= 1, they
+ * and ldy up to 2.08 M; M == 0 is a no-op; a single row's stride may be any. Y overlaps
  * nothing else. Workspace: sam_linear_mxfp4_workspace() bytes,
  * SAM_ERR_WORKSPACE when short. Asynchronous on `stream`, no atomics, a fixed
  * order. */

@@ -207,14 +207,22 @@ __global__ void __launch_bounds__(kQuantThreads) dequant4_kernel(Dequant4Args a)
     }
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256) convert4_kernel(Convert4Args a)
+// Four values a lane where the results' rows allow one store for them.
+template <int DT, int E>
+__global__ void __launch_bounds__(256) join4_kernel(Join4Args a)
 {
     typedef typename Ty<DT>::T T;
+    typedef float Fe __attribute__((ext_vector_type(E)));
+    typedef T Te __attribute__((ext_vector_type(E)));
     const long long n = a.rows * a.cols;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    for (long long i = (blockIdx.x * 256ll + threadIdx.x) * E; i < n; i += gridDim.x * 256ll * E) {
+        Fe v = *reinterpret_cast<const Fe*>(a.src + i);
+        for (int p = 1; p < a.parts; ++p) v += *reinterpret_cast<const Fe*>(a.src + p * n + i);
         const long long row = i / a.cols;
-        static_cast<T*>(a.dst)[row * a.ldd + (i - row * a.cols)] = (T)a.src[i];
+        Te r;
+#pragma unroll
+        for (int e = 0; e < E; ++e) r[e] = (T)v[e];
+        *reinterpret_cast<Te*>(static_cast<T*>(a.dst) + row * a.ldd + (i - row * a.cols)) = r;
     }
 }
 
@@ -257,12 +265,15 @@ hipError_t launch_dequant4(int dtype, const Dequant4Args& a, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_convert4(int dtype, const Convert4Args& a, hipStream_t s)
+hipError_t launch_join4(int dtype, const Join4Args& a, hipStream_t s)
 {
-    const long long n = (a.rows * a.cols + 255) / 256;
-    typedef void (*Fn)(Convert4Args);
-    static const Fn fn[3] = {convert4_kernel<DT_F32>, convert4_kernel<DT_BF16>, convert4_kernel<DT_F16>};
-    hipLaunchKernelGGL(fn[dtype], dim3((unsigned)(n < 8192 ? n : 8192)), dim3(256), 0, s, a);
+    const int es = dtype == DT_F32 ? 4 : 2;
+    const bool four = a.cols % 4 == 0 && a.ldd % 4 == 0 && (unsigned long long)a.dst % (4 * es) == 0;
+    const long long n = (a.rows * a.cols / (four ? 4 : 1) + 255) / 256;
+    typedef void (*Fn)(Join4Args);
+    static const Fn fn[3][2] = {{join4_kernel<DT_F32, 1>, join4_kernel<DT_F32, 4>}, {join4_kernel<DT_BF16, 1>, join4_kernel<DT_BF16, 4>},
+                                {join4_kernel<DT_F16, 1>, join4_kernel<DT_F16, 4>}};
+    hipLaunchKernelGGL(fn[dtype][four], dim3((unsigned)(n < 8192 ? n : 8192)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -66,8 +66,8 @@ struct Region {
 };
 
 struct Layout {
-    Region codes, scales, result, inner;   // forward
-    Region w, ids;                         // backward
+    Region codes, scales, parts;   // forward
+    Region w, ids, inner;          // backward
     unsigned long long total = 0;
     void take(Region& r, unsigned long long bytes)
     {
@@ -107,8 +107,7 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
     if (!plan_auto(M, N, 32 * kb, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
     L->take(L->codes, 16ull * M * kb);
     L->take(L->scales, (unsigned long long)M * kb);
-    L->take(L->result, 4ull * M * N);
-    L->take(L->inner, p->ws_bytes);
+    if (p->split > 1) L->take(L->parts, 4ull * p->split * M * N);
     return SAM_OK;
 }
 
@@ -206,7 +205,7 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     sam_status st = forward_layout(dtype, out, M, N, K, &p, &L);
     if (st != SAM_OK) return st;
     if (M == 0) return api_ok();
-    if (M > 1 && (ldx < K || ldy < N || ldx > (1ll << 40) || ldy > (1ll << 40)))
+    if (M > 1 && (ldx < K || ldy < N || ldx > (1ll << 40) || ldy > kMostRow))
         return api_fail(SAM_ERR_INVALID_ARG, "row stride ldx=%lld (rows of %lld) or ldy=%lld (rows of %lld)", (long long)ldx,
                         (long long)K, (long long)ldy, (long long)N);
     const long long kb = blocks_of(K);
@@ -249,11 +248,34 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
         a.out = out;
         return done(launch_stream4(dtype, a, s));
     }
-    float* result = reinterpret_cast<float*>(ws + L.result.off);
-    st = sam_gemm_mxfp4(q.codes, q.scales, codes, scales, result, M, N, 32 * kb, L.inner.bytes ? ws + L.inner.off : nullptr,
-                        L.inner.bytes, stream);
-    if (st != SAM_OK) return st;
-    return done(launch_convert4(out, {result, Y, M > 1 ? ldy : N, M, (int)N}, s));
+    GemmArgs g{};
+    g.A = q.codes;
+    g.sa = q.scales;
+    g.B = codes;
+    g.sb = scales;
+    g.fmt_a = g.fmt_b = 4;
+    g.M = (int)M;
+    g.N = (int)N;
+    g.K = (int)(32 * kb);
+    g.lda = g.ldb = g.K;
+    g.k_chunk = p.k_chunk;
+    g.split = p.split;
+    g.tiles_m = p.tiles_m;
+    g.tiles_n = p.tiles_n;
+    g.group_m = p.group_m;
+    g.xcd_remap = p.xcd_remap;
+    g.raster_n = p.raster_n;
+    g.part_stride = M * N;
+    if (p.split == 1) {
+        g.out = static_cast<float*>(Y);
+        g.ldc = (int)(M > 1 ? ldy : N);
+        return done(launch_tile4(p, g, out, s));
+    }
+    float* parts = reinterpret_cast<float*>(ws + L.parts.off);
+    g.out = parts;
+    g.ldc = g.N;
+    const hipError_t e = launch_mx8(p, g, s);
+    return done(e != hipSuccess ? e : launch_join4(out, {parts, p.split, Y, M > 1 ? ldy : N, M, (int)N}, s));
 }
 
 sam_status sam_linear_mxfp4_backward_workspace(sam_dtype dtype, sam_dtype out, int64_t M, int64_t N, int64_t K, uint64_t* bytes)

@@ -30,9 +30,10 @@ struct Dequant4Args {
     long long ldx;
 };
 
-// FP32 rows into rows of another type or stride.
-struct Convert4Args {
-    const float* src;        // rows x cols, compact
+// Partial sums added in their order, into rows of the result's type and stride.
+struct Join4Args {
+    const float* src;        // [parts][rows][cols]
+    int parts;
     void* dst;               // stride ldd
     long long ldd;
     long long rows;
@@ -63,6 +64,9 @@ hipError_t launch_stream4(int dtype, const Stream4Args& a, hipStream_t s);
 
 hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t s);
 hipError_t launch_dequant4(int dtype, const Dequant4Args& a, hipStream_t s);
-hipError_t launch_convert4(int dtype, const Convert4Args& a, hipStream_t s);
+hipError_t launch_join4(int dtype, const Join4Args& a, hipStream_t s);
+// A product of E2M1 operands by its plan (one split): C of type `out` at a.out
+// with row stride a.ldc.
+hipError_t launch_tile4(const Plan& p, const GemmArgs& a, int out, hipStream_t s);
 
 }  // namespace sam
