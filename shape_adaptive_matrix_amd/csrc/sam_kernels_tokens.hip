@@ -141,19 +141,28 @@ __device__ __forceinline__ u64 bound_together(const u64 (&own)[G], int top, int*
     return bound;
 }
 
-// How many of a list's n entries are larger than e. What lies behind them, up
-// to a multiple of eight, is read and dropped.
-__device__ __forceinline__ int larger(const u64* list, int n, u64 e)
+// Calls f(entry, its place) for the list's n entries, by the workgroup: a
+// place is how many are larger. Lists of up to 64 (128) have four (two) lanes
+// to an entry. Zeros follow the last entry up to a multiple of eight.
+template <int NT, class F>
+__device__ __forceinline__ void for_places(const u64* list, int n, F f)
 {
-    int r = 0;
-    for (int j = 0; j < n; j += 8) {
-        u64 o[8];
+    const int split = n <= NT / 4 ? 2 : (n <= NT / 2 ? 1 : 0);
+    const int sub = threadIdx.x & ((1 << split) - 1);
+    for (int i = threadIdx.x >> split; i < n; i += NT >> split) {
+        const u64 e = list[i];
+        int r = 0;
+        for (int j = 8 * sub; j < n; j += 8 << split) {
+            u64 o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = list[j + i];
+            for (int k = 0; k < 8; ++k) o[k] = list[j + k];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r += o[i] > e && j + i < n;
+            for (int k = 0; k < 8; ++k) r += o[k] > e;
+        }
+        if (split) r += __builtin_amdgcn_update_dpp(0, r, 0xB1, 0xF, 0xF, true);       // lanes 1 0 3 2
+        if (split == 2) r += __builtin_amdgcn_update_dpp(0, r, 0x4E, 0xF, 0xF, true);  // lanes 2 3 0 1
+        if (sub == 0) f(e, r);
     }
-    return r;
 }
 
 // Sum over the lanes up to this one.
@@ -271,6 +280,9 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
     Sums x = {edge, edge == -INFINITY ? 0.0f : 1.0f + (edge - edge), 0.0f};   // NaN for an Inf or NaN
 
     float so_far = -INFINITY;   // of the segments that share a bit
+    bool plain = true;          // the wave's values so far are finite and near enough to zero
+    if constexpr (TOP)
+        for (int i = tid; i < kEntries + 8; i += NT) room[KEYS + i] = 0;
     auto segment = [&](u4 (&r)[P], u4 (&next)[P], int at) {
         const int seg = p0 + at * (NT * P);
         fetch(next, seg + NT * P);
@@ -294,28 +306,32 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
         if (tm > x.m || x.s == 0.0f) to_largest(x, fmaxf(tm, x.m), a.scale);
         const float pivot = x.m == -INFINITY ? 0.0f : x.m, c = pivot * a.scale;
         float s = 0.0f, h = 0.0f;
-        // d = z scale - c in one operation. c is rounded: all exponents are
-        // off by the same, which is taken out of the sums.
+        plain = plain && !__any(!(fabsf(c) <= 16384.0f));
+        if (plain) {
+            // d = z scale - c in one operation. c is rounded: all exponents
+            // are off by the same, which is taken out of the sums.
 #pragma unroll
-        for (int q = 0; q < P; ++q) {
-            float v[E];
-            Pc::get(r[q], v);
+            for (int q = 0; q < P; ++q) {
+                float v[E];
+                Pc::get(r[q], v);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float d = __fmaf_rn(v[i], a.scale, -c), e = pow2(d);
-                s += e;
-                h = __fmaf_rn(e, d, h);
+                for (int i = 0; i < E; ++i) {
+                    const float d = __fmaf_rn(v[i], a.scale, -c), e = pow2(d);
+                    s += e;
+                    h = __fmaf_rn(e, d, h);
+                }
             }
+            const float off = __fmaf_rn(pivot, a.scale, -c), g = pow2(-off);
+            h = g * (h - off * s);
+            s *= g;
+            plain = !__any(h != h);
         }
-        const float off = __fmaf_rn(pivot, a.scale, -c), g = pow2(-off);
-        h = g * (h - off * s);
-        s *= g;
-        // Not so with values of -inf (whose 0 times -inf should be 0) and far
-        // from zero: once more.
-        if (__any(h != h || !(fabsf(c) <= 16384.0f))) {
+        // Values of -inf (their 0 times -inf should be 0), and far from zero:
+        // here, and for the rest of the row.
+        if (!plain) {
+            s = h = 0.0f;
 #pragma unroll
             for (int q = 0; q < P; ++q) as_read(r[q]);
-            s = h = 0.0f;
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 float v[E];
@@ -386,6 +402,44 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
             for (int i = 0; i < NW; ++i) k[i] = best[lane + 64 * i];
             bound = bound_of(k, a.top);   // every wave the same
         }
+        // A place for each of `n` of every lane, counted in `count`.
+        auto places = [&](int n, int* count) {
+            const int up = sum_up_to(n);
+            int to = 0;
+            if (lane == 63 && up) to = atomicAdd(count, up);
+            return __builtin_amdgcn_readlane(to, 63) + up - n;
+        };
+        auto taken = [&](float v) { return v != -INFINITY && !(v < bound); };
+        // The values of a thread's pieces (d[q] at index[q]), and at the edge
+        // of the row, that reach the bound.
+        auto gather = [&](auto& d, auto& index, unsigned look, bool with_edge) {   // look: a bit for each piece
+            constexpr int Q = sizeof(index) / sizeof(index[0]);
+            const int edges = with_edge && edge_at >= 0 && taken(edge) ? 1 : 0;
+            int n = edges;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (!__any(look >> q & 1)) continue;
+                float v[E];
+                Pc::get(d[q], v);
+#pragma unroll
+                for (int j = 0; j < E; ++j) n += taken(v[j]);
+            }
+            int to = places(n, &entries);
+            if (n == 0) return;
+            if (edges && to < kEntries) list[to] = entry_of(edge, edge_at);
+            to += edges;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (!(look >> q & 1)) continue;
+                float v[E];
+                Pc::get(d[q], v);
+#pragma unroll
+                for (int j = 0; j < E; ++j) {
+                    if (taken(v[j]) && to < kEntries) list[to] = entry_of(v[j], index[q] + j);
+                    to += taken(v[j]);
+                }
+            }
+        };
         // A bit for each of the thread's pieces (segments) that reach it.
         unsigned mine = 0;
         for (int s = 0; s * step < segments; ++s) {
@@ -398,55 +452,40 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
                 mine |= reaches((unsigned)reinterpret_cast<const unsigned short*>(room)[s * NT + tid] << 16) << s;
             }
         }
-        // A place for each of `n` of every lane, counted in `count`.
-        auto places = [&](int n, int* count) {
-            const int up = sum_up_to(n);
-            int to = 0;
-            if (lane == 63 && up) to = atomicAdd(count, up);
-            return __builtin_amdgcn_readlane(to, 63) + up - n;
-        };
-        {
+        int found = 0;
+        if (segments <= 1) {   // the pieces are still there
+            int index[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) index[q] = sp.head + (p0 + q * NT + tid) * E;
+            gather(r[0], index, mine, true);
+            lds_barrier();
+            total = entries;
+        } else {
             int to = places(__popc(mine), &pieces_found);
             for (; mine; mine &= mine - 1, ++to)
                 if (to < kEntries) ids[to] = (unsigned short)((__ffs(mine) - 1) * NT + tid);
-        }
-        lds_barrier();
-        const int found = pieces_found;
-        auto taken = [&](float v) { return v != -INFINITY && !(v < bound); };
-        if (found <= kEntries) {
-            const int per = fine ? 1 : P * step, items = found * per;
-            for (int i0 = 0; i0 < items || i0 == 0; i0 += NT) {
-                const int i = i0 + tid;
-                u4 d = Pc::masked();
-                int index = 0;
-                if (i < items) {
-                    const int id = ids[i / per], bit = id / NT, rest = i % per;
-                    const int at = fine ? bit / P : bit * step + rest / P, q = fine ? bit % P : rest % P;
-                    const int piece = p0 + at * (NT * P) + q * NT + id % NT;
-                    if (piece < p1) {
-                        d = zb[piece];
-                        index = sp.head + piece * E;
-                    }
-                }
-                float v[E];
-                Pc::get(d, v);
-                int n = i0 == 0 && edge_at >= 0 && taken(edge) ? 1 : 0;
-                const int edges = n;
-#pragma unroll
-                for (int j = 0; j < E; ++j) n += taken(v[j]);
-                int to = places(n, &entries);
-                if (n) {
-                    if (edges && to < kEntries) list[to] = entry_of(edge, edge_at);
-                    to += edges;
-#pragma unroll
-                    for (int j = 0; j < E; ++j) {
-                        if (taken(v[j]) && to < kEntries) list[to] = entry_of(v[j], index + j);
-                        to += taken(v[j]);
-                    }
-                }
-            }
             lds_barrier();
-            total = entries;
+            found = pieces_found;
+            if (found <= kEntries) {
+                const int per = fine ? 1 : P * step, items = found * per;
+                for (int i0 = 0; i0 < items || i0 == 0; i0 += NT) {
+                    const int i = i0 + tid;
+                    u4 d[1] = {Pc::masked()};
+                    int index[1] = {0};
+                    if (i < items) {
+                        const int id = ids[i / per], bit = id / NT, rest = i % per;
+                        const int at = fine ? bit / P : bit * step + rest / P, q = fine ? bit % P : rest % P;
+                        const int piece = p0 + at * (NT * P) + q * NT + id % NT;
+                        if (piece < p1) {
+                            d[0] = zb[piece];
+                            index[0] = sp.head + piece * E;
+                        }
+                    }
+                    gather(d, index, 1, i0 == 0);
+                }
+                lds_barrier();
+                total = entries;
+            }
         }
         if (found > kEntries || total > kEntries) {
             list = room;
@@ -483,15 +522,15 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
                 lds_barrier();
                 total = entries;
             }
+            if (tid < (-total & 7)) list[total + tid] = 0;
+            lds_barrier();
         }
         const long long out = row * a.parts + part;
-        for (int i = tid; i < total; i += NT) {
-            const u64 e = list[i];
-            const int place = larger(list, total, e);
-            if (place >= a.top) continue;
+        for_places<NT>(list, total, [&](u64 e, int place) {
+            if (place >= a.top) return;
             if (a.parts > 1) a.list[out * a.top + place] = e;
             else write_entry(a, row, place, e, x.m, L);
-        }
+        });
         if (a.parts == 1 && total < a.top && wave == 0) write_masked<DT>(a, row, total, x.m, L);
     }
     if (tid == 0) {
@@ -513,12 +552,22 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(TokenArgs a)
     constexpr int CAP = TOP ? kMaxParts * kMaxAlternatives : 1;
     __shared__ __attribute__((aligned(16))) u64 list[CAP + 8];
     __shared__ int count, held[kMaxParts];
+    constexpr int EARLY = 4;
     const int tid = threadIdx.x, lane = tid & 63;
     const long long row = blockIdx.x;
+    const u64* from = a.list + row * a.parts * a.top;
+    // Everything that most calls need is asked for at once; what a list holds
+    // past its end is dropped later.
     const float4 mine = lane < a.parts ? a.part[row * a.parts + lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
     const float z_token = a.z_token[row];
+    const int all = a.parts * a.top;
+    u64 own[EARLY], low = 0;
+    if constexpr (TOP) {
+        low = from[min(lane, a.parts - 1) * a.top + (a.top + a.parts - 1) / a.parts - 1];
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) own[i] = from[min(tid + 256 * i, all - 1)];
+    }
     const int have = __float_as_int(mine.w);
-    const u64* from = a.list + row * a.parts * a.top;
     const Sums x = wave_total({mine.x, mine.y, mine.z}, a.scale);   // every wave the same
     const float L = logf(x.s);
     if constexpr (TOP) {
@@ -526,48 +575,52 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(TokenArgs a)
         const int full = __popcll(__ballot(is_full));
         u64 least = 0;
         if (full) {
-            u64 e = is_full ? from[lane * a.top + (a.top + full - 1) / full - 1] : ~0ull;
+            if (full < a.parts && is_full) low = from[lane * a.top + (a.top + full - 1) / full - 1];
+            least = is_full ? low : ~0ull;
 #pragma unroll
             for (int d = 32; d; d >>= 1) {
-                const u64 o = __shfl_xor(e, d);
-                e = o < e ? o : e;
+                const u64 o = __shfl_xor(least, d);
+                least = o < least ? o : least;
             }
-            least = e;
         }
         if (tid == 0) count = 0;
         if (tid < 64) held[lane] = have;
+        for (int i = tid; i < min(all, kEntries) + 8; i += 256) list[i] = 0;
         lds_barrier();
-        for (int i = tid; i < a.parts * a.top; i += 256) {
+        auto add = [&](u64 e, int i) {
             const int s = i / a.top;
-            const u64 e = i - s * a.top < held[s] ? from[i] : 0;
-            const u64 who = __ballot(e && e >= least);
+            const bool in = i < all && i - s * a.top < held[min(s, a.parts - 1)] && e >= least;
+            const u64 who = __ballot(in);
             int at = 0;
-            if (lane == __ffsll(who) - 1) at = atomicAdd(&count, __popcll(who));
-            at = __shfl(at, __ffsll(who) - 1);
-            if (e && e >= least) list[at + lanes_below(who)] = e;
-        }
+            if (lane == 0 && who) at = atomicAdd(&count, __popcll(who));
+            at = __builtin_amdgcn_readfirstlane(at);
+            if (in) list[at + lanes_below(who)] = e;
+        };
+#pragma unroll
+        for (int i = 0; i < EARLY; ++i) add(own[i], tid + 256 * i);
+        for (int i = 256 * EARLY; i < all; i += 256) add(i + tid < all ? from[i + tid] : 0, i + tid);
         lds_barrier();
         int n = count;
         if (n > kEntries) {   // the best lie in few parts
             __shared__ int counts[4];
             constexpr int G = (CAP + 255) / 256;
-            u64 own[G];
+            u64 some[G];
 #pragma unroll
-            for (int i = 0; i < G; ++i) own[i] = tid + 256 * i < n ? list[tid + 256 * i] : 0;
-            const u64 last = bound_together<256>(own, a.top, counts);
+            for (int i = 0; i < G; ++i) some[i] = tid + 256 * i < n ? list[tid + 256 * i] : 0;
+            const u64 last = bound_together<256>(some, a.top, counts);
             if (tid == 0) count = 0;
             lds_barrier();
 #pragma unroll
             for (int i = 0; i < G; ++i)
-                if (own[i] && own[i] >= last) list[atomicAdd(&count, 1)] = own[i];
+                if (some[i] && some[i] >= last) list[atomicAdd(&count, 1)] = some[i];
             lds_barrier();
             n = count;
+            if (tid < (-n & 7)) list[n + tid] = 0;
+            lds_barrier();
         }
-        for (int i = tid; i < n; i += 256) {
-            const u64 e = list[i];
-            const int place = larger(list, n, e);
+        for_places<256>(list, n, [&](u64 e, int place) {
             if (place < a.top) write_entry(a, row, place, e, x.m, L);
-        }
+        });
         if (n < a.top && tid < 64) write_masked<DT>(a, row, n, x.m, L);
     }
     if (tid == 0) write_row(a, row, x, L, z_token);
