@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
     typedef Piece<DT> Pc;
     typedef typename Pc::T T;
     constexpr int E = Pc::E, NW = NT / 64, FINE = 32 / P;   // segments whose pieces each have a bit of 32
+    // top <= NT: that many threads' largest values bound it.
     static_assert(P == 4 && FINE * P == 32, "a thread's pieces, or groups of segments, are 32 bits");
     // The pieces' largest values, [segment][thread][P], or those of `step`
     // segments, [.][thread];
@@ -710,14 +711,15 @@ template <int DT, bool TOP>
 hipError_t run(const TokenArgs& a, hipStream_t s)
 {
     const unsigned grid = (unsigned)(a.rows * a.parts);
-    const long long bytes = (long long)a.V * (DT == DT_F32 ? 4 : 2) / a.parts;
-    if constexpr (!TOP) {
-        if (bytes <= 4096) {
-            hipLaunchKernelGGL((tokens_kernel<DT, 64, 4, TOP>), dim3(grid), dim3(64), 0, s, a);
-            return hipGetLastError();
-        }
-    }
-    hipLaunchKernelGGL((tokens_kernel<DT, 256, 4, TOP>), dim3(grid), dim3(256), 0, s, a);
+    const long long bytes = (long long)a.V * (DT == DT_F32 ? 4 : 2);
+    // Short rows: a wave each, which waits for no other (4096 x 2000 bf16, 5
+    // alternatives: 14 us, with four waves 29; 4096 x 8192: 20 and 26), as long
+    // as its 64 lanes' largest values make a close bound.
+    const bool wave = a.top <= 24 && a.parts == 1 && (bytes <= 4096 || (bytes <= 16384 && a.rows >= 512));
+    if (wave)
+        hipLaunchKernelGGL((tokens_kernel<DT, 64, 4, TOP>), dim3(grid), dim3(64), 0, s, a);
+    else
+        hipLaunchKernelGGL((tokens_kernel<DT, 256, 4, TOP>), dim3(grid), dim3(256), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     hipLaunchKernelGGL((tokens_join_kernel<DT, TOP>), dim3((unsigned)a.rows), dim3(256), 0, s, a);
@@ -727,11 +729,11 @@ hipError_t run(const TokenArgs& a, hipStream_t s)
 }  // namespace
 
 // Rows for fewer than two workgroups a CU are cut, into parts of 16 KB at
-// least.
-int tokens_parts(int dtype, long long rows, long long V)
+// least, with alternatives 32 KB (16 x 131072 FP32, 20 of them: 13.3 us, with
+// 16 KB 16 us, for twice the lists to join).
+int tokens_parts(int dtype, long long rows, long long V, long long top)
 {
-    const long long bytes = V * (dtype == DT_F32 ? 4 : 2);
-    const long long most = bytes / 16384;
+    const long long bytes = V * (dtype == DT_F32 ? 4 : 2), most = bytes / (top ? 32768 : 16384);
     long long p = 512 / rows;
     p = p > most ? most : p;
     p = p > kMaxParts ? kMaxParts : p;

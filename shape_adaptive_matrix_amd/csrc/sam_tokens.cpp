@@ -66,7 +66,7 @@ sam_status sam_token_logprobs_workspace(sam_dtype dtype, int64_t rows, int64_t V
     if (st != SAM_OK) return st;
     if (top < 0 || top > kMaxAlternatives || top > V)
         return api_fail(SAM_ERR_INVALID_ARG, "top=%lld outside 0 .. %d or over V", (long long)top, kMaxAlternatives);
-    const int parts = rows > 0 ? tokens_parts(dtype, rows, V) : 1;
+    const int parts = rows > 0 ? tokens_parts(dtype, rows, V, top) : 1;
     *bytes = parts > 1 ? align256(16ull * rows * parts) + align256(4ull * rows) + 8ull * rows * parts * top : 0;
     return api_ok();
 }
@@ -116,7 +116,7 @@ sam_status sam_token_logprobs(sam_dtype dtype, int64_t rows, int64_t V, int64_t 
     a.norm = norm;
     a.top_logprob = top_logprob;
     a.top_index = top_index;
-    a.parts = tokens_parts(dtype, rows, V);
+    a.parts = tokens_parts(dtype, rows, V, top);
     if (a.parts > 1) {
         char* ws = static_cast<char*>(workspace);
         a.part = reinterpret_cast<float4*>(ws);

@@ -36,7 +36,7 @@ struct TokenArgs {
 };
 
 // Workgroups that a row is cut over.
-int tokens_parts(int dtype, long long rows, long long V);
+int tokens_parts(int dtype, long long rows, long long V, long long top);
 constexpr int kMaxParts = 64;
 
 struct TokenGradArgs {
