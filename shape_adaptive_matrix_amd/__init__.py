@@ -773,34 +773,35 @@ def distill(logits, teacher, index, weight=None, temperature=1.0, loss=None, gra
 
 
 # -- MXFP4 tensors and the 4-bit projection -----------------------------------------
-def _on_its_gpu(call):
-    """A call on its first tensor's GPU, whichever is current."""
-    @functools.wraps(call)
-    def on_its_gpu(first, *args, **more):
-        import torch
-        d = first.get_device()
-        if d < 0 or d == torch.cuda.current_device():
-            return call(first, *args, **more)
-        with torch.cuda.device(d):
-            return call(first, *args, **more)
-    return on_its_gpu
+_CODES = {}   # torch's types to type codes
 
 
 def _value_code(t, name):
-    import torch
-    code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}.get(t.dtype)
+    code = _CODES.get(t.dtype)
     if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+        import torch
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+        code = _CODES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
     return code
+
+
+def _elsewhere(d):
+    """A context on GPU d, or None where it is the current one."""
+    import torch
+    current = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # without the first call's set-up around it
+    return None if d == current() else torch.cuda.device(d)
 
 
 def _mxfp4_tensor(codes, scales):
     """(rows, blocks) of a tensor's codes and scales."""
     import torch
-    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_contiguous() or codes.shape[1] % 16:
-        raise ValueError(f"codes must be a contiguous uint8 [rows, 16 blocks] tensor (got {codes.dtype} {tuple(codes.shape)})")
-    rows, blocks = codes.shape[0], codes.shape[1] // 16
-    if scales.dtype != torch.uint8 or scales.shape != (rows, blocks) or not scales.is_contiguous():
+    u8, shape = torch.uint8, codes.shape
+    if codes.dtype != u8 or len(shape) != 2 or shape[1] % 16 or not codes.is_contiguous():
+        raise ValueError(f"codes must be a contiguous uint8 [rows, 16 blocks] tensor (got {codes.dtype} {tuple(shape)})")
+    rows, blocks = shape[0], shape[1] // 16
+    if scales.dtype != u8 or scales.shape != (rows, blocks) or not scales.is_contiguous():
         raise ValueError(f"scales must be a contiguous uint8 [{rows}, {blocks}] tensor (got {scales.dtype} {tuple(scales.shape)})")
     return rows, blocks
 
@@ -817,7 +818,6 @@ def _columns(K, blocks, like=None):
     return K
 
 
-@_on_its_gpu
 def quantize_mxfp4(X, trans=False, codes=None, scales=None, stream=None):
     """MXFP4 codes and scales of X's rows (trans: of its columns, for a weight
     stored K x N): (codes, scales), uint8 [rows, 16 ceil(K / 32)] and [rows,
@@ -828,20 +828,23 @@ def quantize_mxfp4(X, trans=False, codes=None, scales=None, stream=None):
     rows, K, ldx = _matrix(X, "X")
     if trans:
         rows, K = K, rows
-    _one_gpu(("X", "codes", "scales"), (X, codes, scales))
+    there = _elsewhere(_one_gpu(("X", "codes", "scales"), (X, codes, scales)))
+    if there:
+        with there:
+            return quantize_mxfp4(X, trans, codes, scales, stream)
     blocks = (K + 31) // 32
+    given = codes is not None or scales is not None
     if codes is None:
         codes = _new((rows, 16 * blocks), torch.uint8, X.device, stream)
     if scales is None:
         scales = _new((rows, blocks), torch.uint8, X.device, stream)
-    if _mxfp4_tensor(codes, scales) != (rows, blocks):
+    if given and _mxfp4_tensor(codes, scales) != (rows, blocks):
         raise ValueError(f"codes and scales must be of {rows} rows and {blocks} blocks (got {tuple(scales.shape)})")
     _check(lib().sam_quantize_mxfp4(code, int(trans), rows, K, _address(X), ldx, _address(codes), _address(scales),
                                     _stream_address(stream)))
     return codes, scales
 
 
-@_on_its_gpu
 def dequantize_mxfp4(codes, scales, K=None, out_dtype=None, X=None, stream=None):
     """The values that codes and scales stand for (sam_dequantize_mxfp4): X
     [rows, K], bfloat16 unless out_dtype (or X) says otherwise. K: 32 a block
@@ -849,7 +852,10 @@ def dequantize_mxfp4(codes, scales, K=None, out_dtype=None, X=None, stream=None)
     import torch
     rows, blocks = _mxfp4_tensor(codes, scales)
     K = _columns(K, blocks, X)
-    _one_gpu(("codes", "scales", "X"), (codes, scales, X))
+    there = _elsewhere(_one_gpu(("codes", "scales", "X"), (codes, scales, X)))
+    if there:
+        with there:
+            return dequantize_mxfp4(codes, scales, K, out_dtype, X, stream)
     if X is None:
         X = _new((rows, K), torch.bfloat16 if out_dtype is None else out_dtype, codes.device, stream)
     elif out_dtype is not None and X.dtype != out_dtype:
@@ -863,7 +869,6 @@ def dequantize_mxfp4(codes, scales, K=None, out_dtype=None, X=None, stream=None)
     return X
 
 
-@_on_its_gpu
 def linear_mxfp4(X, codes, scales, Y=None, out_dtype=None, workspace=None, stream=None):
     """Y = q(X)·Wq^T: X's rows rounded to MXFP4 times a weight kept in it
     (sam_linear_mxfp4). X [M, K] float32, bfloat16 or float16, may be a view
@@ -876,7 +881,10 @@ def linear_mxfp4(X, codes, scales, Y=None, out_dtype=None, workspace=None, strea
     _columns(K, blocks)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _one_gpu(("X", "codes", "scales", "Y", "workspace"), (X, codes, scales, Y, workspace))
+    there = _elsewhere(_one_gpu(("X", "codes", "scales", "Y", "workspace"), (X, codes, scales, Y, workspace)))
+    if there:
+        with there:
+            return linear_mxfp4(X, codes, scales, Y, out_dtype, workspace, stream)
     Y, out, ldy = _adapter_result(Y, M, N, out_dtype, X, code, "Y", stream)
     if workspace is None:
         need = _adapter_workspace_bytes("sam_linear_mxfp4_workspace", code, out, M, N, K)
@@ -888,7 +896,6 @@ def linear_mxfp4(X, codes, scales, Y=None, out_dtype=None, workspace=None, strea
     return Y
 
 
-@_on_its_gpu
 def linear_mxfp4_backward(dY, codes, scales, K=None, dX=None, out_dtype=None, workspace=None, stream=None):
     """Gradient of linear_mxfp4 with respect to X for dY [M, N], X's rounding
     passed through (sam_linear_mxfp4_backward): dX = dY·Wq [M, K], float32
@@ -901,7 +908,10 @@ def linear_mxfp4_backward(dY, codes, scales, K=None, dX=None, out_dtype=None, wo
         raise ValueError(f"dY has rows of {n}, the weight {N} rows")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _one_gpu(("dY", "codes", "scales", "dX", "workspace"), (dY, codes, scales, dX, workspace))
+    there = _elsewhere(_one_gpu(("dY", "codes", "scales", "dX", "workspace"), (dY, codes, scales, dX, workspace)))
+    if there:
+        with there:
+            return linear_mxfp4_backward(dY, codes, scales, K, dX, out_dtype, workspace, stream)
     dX, out, lddx = _adapter_result(dX, M, K, out_dtype, dY, code, "dX", stream)
     if workspace is None:
         need = _adapter_workspace_bytes("sam_linear_mxfp4_backward_workspace", code, out, M, N, K)
@@ -925,17 +935,13 @@ def _logits_and_tokens(logits, tokens):
 
 def _result(t, shape, dtype, like, name, stream):
     """t, checked, or (None) a new tensor of this shape beside `like`."""
-    import torch
     if t is None:
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=like.device)
-        return _new(shape, dtype, like.device, stream)
+        return like.new_empty(shape, dtype=dtype) if stream is None else _new(shape, dtype, like.device, stream)
     if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {shape} tensor (got {t.dtype} {tuple(t.shape)})")
     return t
 
 
-@_on_its_gpu
 def token_logprobs(logits, tokens, temperature=1.0, top=0, logprob=None, entropy=None, norm=None, top_logprob=None,
                    top_index=None, workspace=None, stream=None):
     """Log probability of every row's token, the row's entropy and its norm
@@ -952,8 +958,12 @@ def token_logprobs(logits, tokens, temperature=1.0, top=0, logprob=None, entropy
     code, rows, V, ldz = _logits_and_tokens(logits, tokens)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _one_gpu(("logits", "tokens", "logprob", "entropy", "norm", "top_logprob", "top_index", "workspace"),
-             (logits, tokens, logprob, entropy, norm, top_logprob, top_index, workspace))
+    there = _elsewhere(_one_gpu(("logits", "tokens", "logprob", "entropy", "norm", "top_logprob", "top_index", "workspace"),
+                                (logits, tokens, logprob, entropy, norm, top_logprob, top_index, workspace)))
+    if there:
+        with there:
+            return token_logprobs(logits, tokens, temperature, top, logprob, entropy, norm, top_logprob, top_index,
+                                  workspace, stream)
     f32 = torch.float32
     if workspace is None:
         need = _adapter_workspace_bytes("sam_token_logprobs_workspace", code, rows, V, top)
@@ -972,16 +982,18 @@ def token_logprobs(logits, tokens, temperature=1.0, top=0, logprob=None, entropy
     return (logprob, entropy, norm, top_logprob, top_index) if top else (logprob, entropy, norm)
 
 
-@_on_its_gpu
 def token_logprobs_grad(logits, tokens, norm, entropy=None, dlogprob=None, dentropy=None, temperature=1.0, grad=None,
                         stream=None):
     """Gradient with respect to the logits for the gradients dlogprob and
     dentropy (float32 [rows], None: 0) of token_logprobs' results, from its
     norm and entropy (sam_token_logprobs_grad). grad may be logits itself."""
     code, rows, V, ldz = _logits_and_tokens(logits, tokens)
-    _one_gpu(("logits", "tokens", "norm", "entropy", "dlogprob", "dentropy", "grad"),
-             (logits, tokens, norm, entropy, dlogprob, dentropy, grad))
     import torch
+    there = _elsewhere(_one_gpu(("logits", "tokens", "norm", "entropy", "dlogprob", "dentropy", "grad"),
+                                (logits, tokens, norm, entropy, dlogprob, dentropy, grad)))
+    if there:
+        with there:
+            return token_logprobs_grad(logits, tokens, norm, entropy, dlogprob, dentropy, temperature, grad, stream)
     if norm is None or (dentropy is not None and entropy is None):
         raise ValueError("norm, and with dentropy entropy, are what token_logprobs returned")
     _result(norm, (rows, 2), torch.float32, logits, "norm", stream)

@@ -20,12 +20,12 @@ def dequant(dtype=sam.BF16, rows=4, K=100, X=P, ldx=100, codes=2 * P, scales=3 *
     return L.sam_dequantize_mxfp4(dtype, rows, K, codes, scales, X, ldx, None)
 
 
-def linear(dtype=sam.BF16, M=4, N=60, K=100, X=P, ldx=100, codes=2 * P, scales=3 * P, out=sam.F32, Y=4 * P, ldy=60,
+def linear(dtype=sam.BF16, M=100, N=60, K=100, X=P, ldx=100, codes=2 * P, scales=3 * P, out=sam.F32, Y=4 * P, ldy=60,
            ws=5 * P, n=1 << 23):
     return L.sam_linear_mxfp4(dtype, M, N, K, X, ldx, codes, scales, out, Y, ldy, ws, n, None)
 
 
-def back(dtype=sam.BF16, M=4, N=60, K=100, X=P, ldx=60, codes=2 * P, scales=3 * P, out=sam.F32, Y=4 * P, ldy=100,
+def back(dtype=sam.BF16, M=100, N=60, K=100, X=P, ldx=60, codes=2 * P, scales=3 * P, out=sam.F32, Y=4 * P, ldy=100,
          ws=5 * P, n=1 << 23):
     return L.sam_linear_mxfp4_backward(dtype, M, N, K, X, ldx, codes, scales, out, Y, ldy, ws, n, None)
 

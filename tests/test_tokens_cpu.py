@@ -88,7 +88,8 @@ def test_binding_refuses(change):
 
 
 def test_gradient_needs_what_the_forward_pass_gave(monkeypatch):
-    monkeypatch.setattr(sam, "_one_gpu", lambda *a: 0)
+    monkeypatch.setattr(sam, "_one_gpu", lambda *a: 0)   # host tensors, for these are looked at behind that check
+    monkeypatch.setattr(sam, "_elsewhere", lambda d: None)
     z, t = torch.zeros(4, 50), torch.zeros(4, dtype=torch.int32)
     for more in (dict(norm=None), dict(norm=torch.zeros(4, 2), dentropy=torch.zeros(4)), dict(norm=torch.zeros(4)),
                  dict(norm=torch.zeros(4, 2), dlogprob=torch.zeros(3)), dict(norm=torch.zeros(4, 2).double())):
