@@ -19,10 +19,20 @@ using namespace quant4;
 constexpr int kQuantThreads = 256, kQuantEach = 2;
 
 // A quarter of a block a lane: 16 (FP32: 32) bytes in, 4 out, both whole
-// lines a wave.
+// lines a wave. Workgroups from `blocks` on copy scales.
 template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a)
+__global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a, unsigned blocks)
 {
+    if (blockIdx.x >= blocks) {
+        const long long n = a.pack_rows * a.kb;
+        for (long long i = (long long)(blockIdx.x - blocks) * kQuantThreads + threadIdx.x; i < n;
+             i += (long long)(gridDim.x - blocks) * kQuantThreads) {
+            const long long row = i / a.kb;
+            const int k = (int)(i - row * a.kb);
+            a.to[i] = k < a.from_kb ? a.from[row * a.from_kb + k] : 0;
+        }
+        return;
+    }
     typedef typename Ty<DT>::T T;
     constexpr int W = DT == DT_F32 ? 8 : 4;
     const unsigned per_row = 4u * a.kb;
@@ -245,11 +255,13 @@ hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t
         return hipGetLastError();
     }
     const long long pieces = a.rows * a.kb * 4, each = kQuantThreads * kQuantEach;
-    typedef void (*Fn)(Quant4Args);
+    const long long blocks = (pieces + each - 1) / each, copies = (a.pack_rows * a.kb + kQuantThreads - 1) / kQuantThreads;
+    typedef void (*Fn)(Quant4Args, unsigned);
     static const Fn fn[3][2] = {{quant4_rows_kernel<DT_F32, false>, quant4_rows_kernel<DT_F32, true>},
                                 {quant4_rows_kernel<DT_BF16, false>, quant4_rows_kernel<DT_BF16, true>},
                                 {quant4_rows_kernel<DT_F16, false>, quant4_rows_kernel<DT_F16, true>}};
-    hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)((pieces + each - 1) / each)), dim3(kQuantThreads), 0, s, a);
+    hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)(blocks + (copies < 1024 ? copies : 1024))), dim3(kQuantThreads), 0, s, a,
+                       (unsigned)blocks);
     return hipGetLastError();
 }
 

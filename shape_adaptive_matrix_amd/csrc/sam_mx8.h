@@ -56,8 +56,10 @@ typedef unsigned u8v __attribute__((ext_vector_type(8)));
 
 // EB: element bits, 8 (FA, FB: 0 E4M3, 1 E5M2) or 4 (FA = FB = 4, E2M1 packed
 // two per byte, element 2 i in the low nibble). BK counts values of K.
-// OUT: -1 C (or a split's partial sums) as compact FP32 rows; otherwise C of that type
-// (DT_F32, DT_BF16, DT_F16) with row stride ldc.
+// OUT: -1 C (or a split's partial sums) as compact FP32 rows; otherwise C (or a
+// split's) of that type (DT_F32, DT_BF16, DT_F16) with row stride ldc, and Bt's
+// rows of ldb values: K may be rounded up past them, for what A holds there
+// are zeros and what Bt's next row holds are finite E2M1 values.
 template <int FA, int FB, int BM, int BN, int WM, int WN, int BK, bool SDMA, int EB, int OUT = -1>
 __global__ void __launch_bounds__(WM * WN * 64)
 __attribute__((amdgpu_waves_per_eu(1, (160 * 1024 / (2 * (BM + BN) * (BK + 8))) * WM * WN / 4 > 0
@@ -106,6 +108,7 @@ gemm_mx8_kernel(GemmArgs args)
     const int M = args.M, N = args.N, K = args.K;
     const int KB = K / 32;                             // scale codes per row
     const int RB = K * EB / 8;                         // bytes per operand row
+    const int RBB = OUT >= 0 ? args.ldb * EB / 8 : RB; // of Bt: rows may be shorter than K (see OUT)
     const int m0 = tm * BM, n0 = tn * BN;
     const int kbeg = s * args.k_chunk;
     const int kend = min(K, kbeg + args.k_chunk);
@@ -114,7 +117,7 @@ gemm_mx8_kernel(GemmArgs args)
     const int wn0 = (wave % WN) * WTN;
 
     const i4 rA = rsrc_words(static_cast<const char*>(args.A) + (long long)m0 * RB, (long long)(M - m0) * RB);
-    const i4 rB = rsrc_words(static_cast<const char*>(args.B) + (long long)n0 * RB, (long long)(N - n0) * RB);
+    const i4 rB = rsrc_words(static_cast<const char*>(args.B) + (long long)n0 * RBB, (long long)(N - n0) * RBB);
     const __amdgpu_buffer_rsrc_t rSA = make_rsrc(args.sa + (long long)m0 * KB, (long long)(M - m0) * KB);
     const __amdgpu_buffer_rsrc_t rSB = make_rsrc(args.sb + (long long)n0 * KB, (long long)(N - n0) * KB);
     const i4 rSAw = rsrc_words(args.sa + (long long)m0 * KB, (long long)(M - m0) * KB);
@@ -151,7 +154,7 @@ gemm_mx8_kernel(GemmArgs args)
         const int row = I * RPL + lane / CPR;
         const int c = (lane % CPR) ^ ((row / RSW) % CPR);
         const int gk = k0 + c * VPC;                   // first value of K in the chunk
-        const int off = gk < kend ? row * RB + gk * EB / 8 : kOOB;
+        const int off = gk < kend ? row * (is_a ? RB : RBB) + gk * EB / 8 : kOOB;
         if (is_a)
             lds_load16(rA, lds_addr(buf + I * 1024), off);
         else
@@ -342,7 +345,7 @@ gemm_mx8_kernel(GemmArgs args)
         // bytes of one store.
         constexpr int ES = OUT == DT_F32 ? 4 : 2;
         const int ld = args.ldc;
-        char* outp = reinterpret_cast<char*>(args.out) + ((long long)m0 * ld + n0) * ES;
+        char* outp = reinterpret_cast<char*>(args.out) + (s * args.part_stride + (long long)m0 * ld + n0) * ES;
         const __amdgpu_buffer_rsrc_t rC = make_rsrc(outp, ((long long)(M - m0 - 1) * ld + N - n0) * ES);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {

@@ -66,8 +66,8 @@ struct Region {
 };
 
 struct Layout {
-    Region codes, scales, parts;   // forward
-    Region w, ids, inner;          // backward
+    Region codes, scales, wscales, parts;   // forward
+    Region w, ids, inner;                   // backward
     unsigned long long total = 0;
     void take(Region& r, unsigned long long bytes)
     {
@@ -104,9 +104,14 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
         }
         return SAM_OK;
     }
-    if (!plan_auto(M, N, 32 * kb, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
-    L->take(L->codes, 16ull * M * kb);
-    L->take(L->scales, (unsigned long long)M * kb);
+    // The tiles move scales four at a time: rows that are not so many get
+    // zeros behind them, X's where they are made and W's scales in a copy
+    // (its codes stay; 4096 x 11040 x 4096: 398 us with a byte load a scale).
+    const long long kp = (kb + 3) / 4 * 4;
+    if (!plan_auto(M, N, 32 * kp, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
+    L->take(L->codes, 16ull * M * kp);
+    L->take(L->scales, (unsigned long long)M * kp);
+    if (kp != kb) L->take(L->wscales, (unsigned long long)N * kp);
     if (p->split > 1) L->take(L->parts, 4ull * p->split * M * N);
     return SAM_OK;
 }
@@ -160,7 +165,14 @@ sam_status sam_quantize_mxfp4(sam_dtype dtype, sam_op trans, int64_t rows, int64
     if (rows == 0) return api_ok();
     st = api_device_check();
     if (st != SAM_OK) return st;
-    const Quant4Args a{X, lines > 1 ? ldx : line, rows, (int)K, (int)kb, codes, scales};
+    Quant4Args a{};
+    a.x = X;
+    a.ldx = lines > 1 ? ldx : line;
+    a.rows = rows;
+    a.K = (int)K;
+    a.kb = (int)kb;
+    a.codes = codes;
+    a.scales = scales;
     return done(launch_quant4(dtype, trans == SAM_OP_T, a, static_cast<hipStream_t>(stream)));
 }
 
@@ -227,7 +239,21 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     char* ws = static_cast<char*>(workspace);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const bool few = stream4_takes(M, kb), rounds = few && L.codes.bytes == 0;
-    const Quant4Args q{X, M > 1 ? ldx : K, M, (int)K, (int)kb, (unsigned char*)ws + L.codes.off, (unsigned char*)ws + L.scales.off};
+    const long long kp = few ? kb : (kb + 3) / 4 * 4;
+    Quant4Args q{};
+    q.x = X;
+    q.ldx = M > 1 ? ldx : K;
+    q.rows = M;
+    q.K = (int)K;
+    q.kb = (int)kp;
+    q.codes = (unsigned char*)ws + L.codes.off;
+    q.scales = (unsigned char*)ws + L.scales.off;
+    if (L.wscales.bytes) {
+        q.from = scales;
+        q.to = (unsigned char*)ws + L.wscales.off;
+        q.pack_rows = N;
+        q.from_kb = (int)kb;
+    }
     if (!rounds) {
         const hipError_t e = launch_quant4(dtype, false, q, s);
         if (e != hipSuccess) return done(e);
@@ -252,12 +278,13 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     g.A = q.codes;
     g.sa = q.scales;
     g.B = codes;
-    g.sb = scales;
+    g.sb = L.wscales.bytes ? q.to : scales;
     g.fmt_a = g.fmt_b = 4;
     g.M = (int)M;
     g.N = (int)N;
-    g.K = (int)(32 * kb);
-    g.lda = g.ldb = g.K;
+    g.K = (int)(32 * kp);
+    g.lda = g.K;
+    g.ldb = (int)(32 * kb);
     g.k_chunk = p.k_chunk;
     g.split = p.split;
     g.tiles_m = p.tiles_m;
@@ -274,7 +301,7 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     float* parts = reinterpret_cast<float*>(ws + L.parts.off);
     g.out = parts;
     g.ldc = g.N;
-    const hipError_t e = launch_mx8(p, g, s);
+    const hipError_t e = launch_tile4(p, g, SAM_F32, s);
     return done(e != hipSuccess ? e : launch_join4(out, {parts, p.split, Y, M > 1 ? ldy : N, M, (int)N}, s));
 }
 

@@ -19,6 +19,12 @@ struct Quant4Args {
     int K, kb;               // values and blocks a row
     unsigned char* codes;    // rows x kb x 16
     unsigned char* scales;   // rows x kb
+    // Beside it (rows' form): a copy of other scales, pack_rows of from_kb to
+    // rows of kb with zeros behind.
+    const unsigned char* from;
+    unsigned char* to;
+    long long pack_rows;
+    int from_kb;
 };
 
 struct Dequant4Args {
@@ -65,8 +71,8 @@ hipError_t launch_stream4(int dtype, const Stream4Args& a, hipStream_t s);
 hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t s);
 hipError_t launch_dequant4(int dtype, const Dequant4Args& a, hipStream_t s);
 hipError_t launch_join4(int dtype, const Join4Args& a, hipStream_t s);
-// A product of E2M1 operands by its plan (one split): C of type `out` at a.out
-// with row stride a.ldc.
+// A product of E2M1 operands by its plan: C (or the partial sums) of type
+// `out` at a.out with row stride a.ldc, Bt's rows of a.ldb values.
 hipError_t launch_tile4(const Plan& p, const GemmArgs& a, int out, hipStream_t s);
 
 }  // namespace sam
