@@ -18,25 +18,48 @@ using namespace quant4;
 
 constexpr int kQuantThreads = 256, kQuantEach = 2;
 
-// A quarter of a block a lane: 16 (FP32: 32) bytes in, 4 out, both whole
-// lines a wave. Workgroups from `blocks` on copy scales.
-template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a, unsigned blocks)
+constexpr int kPlanesEach = 4;
+
+// 256 rows of scales, kPlanesEach dwords of each, to their planes: a lane
+// reads neighbours in a row, a wave writes lines.
+__device__ __forceinline__ void to_planes(const Quant4Args& a, unsigned wg)
 {
-    if (blockIdx.x >= blocks) {
-        const long long n = a.pack_rows * a.kb;
-        for (long long i = (long long)(blockIdx.x - blocks) * kQuantThreads + threadIdx.x; i < n;
-             i += (long long)(gridDim.x - blocks) * kQuantThreads) {
-            const long long row = i / a.kb;
-            const int k = (int)(i - row * a.kb);
-            a.to[i] = k < a.from_kb ? a.from[row * a.from_kb + k] : 0;
-        }
+    const unsigned groups = (a.kb / 4 + kPlanesEach - 1) / kPlanesEach;
+    const long long row = (long long)(wg / groups) * kQuantThreads + threadIdx.x;
+    const int p0 = wg % groups * kPlanesEach;
+    if (row >= a.plane_rows) return;
+    // Whole words around the row's bytes, shifted into place; words past the
+    // row's last byte are its last word, and dropped.
+    const unsigned long long at = reinterpret_cast<unsigned long long>(a.from + row * a.from_kb);
+    const unsigned* from = reinterpret_cast<const unsigned*>(at & ~3ull);
+    const int skew = (int)(at & 3), last = (skew + a.from_kb - 1) >> 2;
+    unsigned w[kPlanesEach + 1], d[kPlanesEach];
+#pragma unroll
+    for (int i = 0; i <= kPlanesEach; ++i) w[i] = from[min(p0 + i, last)];
+#pragma unroll
+    for (int i = 0; i < kPlanesEach; ++i) {
+        const int left = a.from_kb - 4 * (p0 + i);
+        const unsigned v = __builtin_amdgcn_alignbit(w[i + 1], w[i], 8 * skew);
+        d[i] = left >= 4 ? v : (left > 0 ? v & ((1u << (8 * left)) - 1) : 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanesEach; ++i)
+        if (p0 + i < a.kb / 4) reinterpret_cast<unsigned*>(a.to)[(p0 + i) * a.plane_rows + row] = d[i];
+}
+
+// A quarter of a block a lane: 16 (FP32: 32) bytes in, 4 out, both whole
+// lines a wave. The first `copies` workgroups bring other scales into planes.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a, unsigned copies)
+{
+    if (blockIdx.x < copies) {
+        to_planes(a, blockIdx.x);
         return;
     }
     typedef typename Ty<DT>::T T;
     constexpr int W = DT == DT_F32 ? 8 : 4;
     const unsigned per_row = 4u * a.kb;
-    const long long first = (long long)blockIdx.x * (kQuantThreads * kQuantEach);
+    const long long first = (long long)(blockIdx.x - copies) * (kQuantThreads * kQuantEach);
     const long long row0 = first / per_row;
     const unsigned rem0 = (unsigned)(first - row0 * per_row);
     unsigned x[kQuantEach][W];
@@ -62,9 +85,15 @@ __global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a
         m = max(m, quad<0x4E>(m));   // lanes 2 3 0 1
         const unsigned code = scale_code<DT>(m);
         const unsigned c = to_codes<DT>(x[i], code);
+        if (a.planes) {   // a dword of four blocks: 16 lanes of one row
+            unsigned d = code << (8 * (q[i] >> 2 & 3));
+            d |= __builtin_amdgcn_update_dpp(0u, d, 0x124, 0xF, 0xF, true);   // of 4, then 8 lanes round
+            d |= __builtin_amdgcn_update_dpp(0u, d, 0x128, 0xF, 0xF, true);
+            if ((q[i] & 15) == 0 && row[i] < a.rows) reinterpret_cast<unsigned*>(a.scales)[(q[i] >> 4) * a.rows + row[i]] = d;
+        }
         if (row[i] < a.rows) {
             reinterpret_cast<unsigned*>(a.codes)[row[i] * per_row + q[i]] = c;
-            if ((q[i] & 3) == 0) a.scales[row[i] * a.kb + (q[i] >> 2)] = (unsigned char)code;
+            if (!a.planes && (q[i] & 3) == 0) a.scales[row[i] * a.kb + (q[i] >> 2)] = (unsigned char)code;
         }
     }
 }
@@ -255,13 +284,14 @@ hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t
         return hipGetLastError();
     }
     const long long pieces = a.rows * a.kb * 4, each = kQuantThreads * kQuantEach;
-    const long long blocks = (pieces + each - 1) / each, copies = (a.pack_rows * a.kb + kQuantThreads - 1) / kQuantThreads;
+    const long long blocks = (pieces + each - 1) / each;
+    const long long copies = (a.plane_rows + kQuantThreads - 1) / kQuantThreads * ((a.kb / 4 + kPlanesEach - 1) / kPlanesEach);
     typedef void (*Fn)(Quant4Args, unsigned);
     static const Fn fn[3][2] = {{quant4_rows_kernel<DT_F32, false>, quant4_rows_kernel<DT_F32, true>},
                                 {quant4_rows_kernel<DT_BF16, false>, quant4_rows_kernel<DT_BF16, true>},
                                 {quant4_rows_kernel<DT_F16, false>, quant4_rows_kernel<DT_F16, true>}};
-    hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)(blocks + (copies < 1024 ? copies : 1024))), dim3(kQuantThreads), 0, s, a,
-                       (unsigned)blocks);
+    hipLaunchKernelGGL(fn[dtype][al], dim3((unsigned)(blocks + copies)), dim3(kQuantThreads), 0, s, a,
+                       (unsigned)copies);
     return hipGetLastError();
 }
 

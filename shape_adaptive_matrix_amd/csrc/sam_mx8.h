@@ -54,12 +54,17 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef unsigned u4 __attribute__((ext_vector_type(4)));
 typedef unsigned u8v __attribute__((ext_vector_type(8)));
 
+template <int DT> struct Half;
+template <> struct Half<DT_BF16> { typedef __bf16 T; };
+template <> struct Half<DT_F16> { typedef _Float16 T; };
+
 // EB: element bits, 8 (FA, FB: 0 E4M3, 1 E5M2) or 4 (FA = FB = 4, E2M1 packed
 // two per byte, element 2 i in the low nibble). BK counts values of K.
 // OUT: -1 C (or a split's partial sums) as compact FP32 rows; otherwise C (or a
 // split's) of that type (DT_F32, DT_BF16, DT_F16) with row stride ldc, and Bt's
 // rows of ldb values: K may be rounded up past them, for what A holds there
-// are zeros and what Bt's next row holds are finite E2M1 values.
+// are zeros and what Bt's next row holds are finite E2M1 values. The scales
+// are K / 128 planes then, of a dword for every row.
 template <int FA, int FB, int BM, int BN, int WM, int WN, int BK, bool SDMA, int EB, int OUT = -1>
 __global__ void __launch_bounds__(WM * WN * 64)
 __attribute__((amdgpu_waves_per_eu(1, (160 * 1024 / (2 * (BM + BN) * (BK + 8))) * WM * WN / 4 > 0
@@ -89,6 +94,7 @@ gemm_mx8_kernel(GemmArgs args)
     constexpr int NSB = TM + TN;                       // MFMA blocks whose scales a lane uses
     constexpr int NSR = SDMA ? SDW : KSTEPS;           // raw scale registers per block
     static_assert(EB == 8 || (EB == 4 && FA == 4 && FB == 4), "8-bit formats or E2M1");
+    static_assert(OUT < 0 || SDMA, "planes of scale dwords");
     static_assert(ROW == 128 || ROW == 256, "K per stage: 128- or 256-byte rows");
     static_assert(BK % 128 == 0, "whole scale dwords per stage");
     static_assert(WTM % 32 == 0 && WTN % 32 == 0, "wave tile must be whole 32x32 blocks");
@@ -151,9 +157,19 @@ gemm_mx8_kernel(GemmArgs args)
             const bool is_a = grp * 64 < BM;
             const int r = grp * 64 - (is_a ? 0 : BM);      // first row of A or of Bt
             const int kb = k0 / 32 + 4 * d;
-            const int first = kb * 32 < kend ? r * KB + kb : kOOB;
-            lds_load4(is_a ? rSAw : rSBw, lds_addr(buf + A_BYTES + B_BYTES + (d * (BM + BN) + grp * 64) * 4),
-                      (int)((unsigned)first + (unsigned)(lane * KB)));   // rows past M / N: past the record count
+            const unsigned dst = lds_addr(buf + A_BYTES + B_BYTES + (d * (BM + BN) + grp * 64) * 4);
+            if constexpr (OUT >= 0) {
+                // Scales by dwords, each a plane of all rows: a load is 256
+                // contiguous bytes. From rows of scales every lane's dword
+                // lies in a line of its own, of which the L1 keeps nothing
+                // until the next stage: three times the operands' traffic.
+                const long long rows = is_a ? M : N, row0 = (is_a ? m0 : n0) + r;
+                lds_load4(rsrc_words((is_a ? args.sa : args.sb) + (kb / 4 * rows + row0) * 4, kb * 32 < kend ? (rows - row0) * 4 : 0), dst,
+                          lane * 4);
+            } else {
+                const int first = kb * 32 < kend ? r * KB + kb : kOOB;
+                lds_load4(is_a ? rSAw : rSBw, dst, (int)((unsigned)first + (unsigned)(lane * KB)));   // rows past M / N: past the record count
+            }
             return;
         }
         // Rows past M (N) need no test: the panel's record count ends at row
@@ -253,7 +269,18 @@ gemm_mx8_kernel(GemmArgs args)
 #pragma unroll
         for (int m = 0; m < NMF; ++m) {
             const int i = m / TN, j = m % TN;
-            if constexpr (SDMA) {
+            if constexpr (OUT >= 0) {
+                // Operands exchanged: the block comes transposed, a lane's
+                // values are four neighbours of a row of C each.
+                if (t & 1)
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        __builtin_bit_cast(v8i, fb[j]), __builtin_bit_cast(v8i, fa[i]), acc[i][j], FB, FA, 2,
+                        (int)sc[TM + j][t >> 1], 2, (int)sc[i][t >> 1]);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                        __builtin_bit_cast(v8i, fb[j]), __builtin_bit_cast(v8i, fa[i]), acc[i][j], FB, FA, 0,
+                        (int)sc[TM + j][t >> 1], 0, (int)sc[i][t >> 1]);
+            } else if constexpr (SDMA) {
                 if (t & 1)
                     acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
                         __builtin_bit_cast(v8i, fa[i]), __builtin_bit_cast(v8i, fb[j]), acc[i][j], FA, FB, 2,
@@ -350,27 +377,67 @@ gemm_mx8_kernel(GemmArgs args)
 
     const int lrow = lane & 31, lgrp = lane >> 5;
     if constexpr (OUT >= 0) {
-        // Values to nearest even; a row's 32 columns of a block are 64 or 128
-        // bytes of one store.
+        // Values to nearest even. Lane l holds row l % 32 of a block, columns
+        // 8 g + 4 (l / 32) .. + 3 in registers 4 g .. 4 g + 3. Through LDS (an
+        // eighth of the wave's rows at a time, in the ring's place) to stores
+        // of 16 bytes, WTN columns of a row next to each other.
         constexpr int ES = OUT == DT_F32 ? 4 : 2;
+        constexpr int ROWB = WTN * ES + 16;                // a row in LDS, on banks of its own
+        constexpr int LPR = WTN * ES / 16, RPI = 64 / LPR; // lanes to a row, rows an instruction
+        static_assert(NW * 32 * ROWB <= NBUF * STAGE && LPR <= 64 && 64 % LPR == 0 && 32 % RPI == 0, "a block's rows of all waves in LDS");
         const int ld = args.ldc;
         char* outp = reinterpret_cast<char*>(args.out) + (s * args.part_stride + (long long)m0 * ld + n0) * ES;
         const __amdgpu_buffer_rsrc_t rC = make_rsrc(outp, ((long long)(M - m0 - 1) * ld + N - n0) * ES);
+        // Rows on whole words are stored 16 bytes at a time, but for the last
+        // columns.
+        const bool words = ((long long)ld * ES % 4 == 0) && (reinterpret_cast<unsigned long long>(outp) & 3) == 0;
+        unsigned char* mine = lds + wave * 32 * ROWB;
+        barrier();   // all waves' last fragments are read
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int col = wn0 + 32 * j + lrow;
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = wm0 + 32 * i + ((r >> 2) << 3) + (lgrp << 2) + (r & 3);
-                    const int at = m0 + row < M && n0 + col < N ? (row * ld + col) * ES : kOOB;
-                    if constexpr (OUT == DT_F32)
-                        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][r]), rC, at, 0, 0);
-                    else if constexpr (OUT == DT_BF16)
-                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (__bf16)acc[i][j][r]), rC, at, 0, 0);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (_Float16)acc[i][j][r]), rC, at, 0, 0);
+                for (int g = 0; g < 4; ++g) {
+                    unsigned char* p = mine + lrow * ROWB + (32 * j + 8 * g + 4 * lgrp) * ES;
+                    if constexpr (OUT == DT_F32) {
+                        *reinterpret_cast<u4*>(p) = u4{__float_as_uint(acc[i][j][4 * g]), __float_as_uint(acc[i][j][4 * g + 1]),
+                                                       __float_as_uint(acc[i][j][4 * g + 2]), __float_as_uint(acc[i][j][4 * g + 3])};
+                    } else {
+                        typedef typename Half<OUT>::T T;
+                        typedef T T4 __attribute__((ext_vector_type(4)));
+                        *reinterpret_cast<T4*>(p) = T4{(T)acc[i][j][4 * g], (T)acc[i][j][4 * g + 1], (T)acc[i][j][4 * g + 2],
+                                                       (T)acc[i][j][4 * g + 3]};
+                    }
+                }
+            // The wave's own rows: no barrier, its LDS accesses are in order.
+            if (ES == 4 || words) {
+#pragma unroll
+                for (int t = 0; t < 32 / RPI; ++t) {
+                    const int r = t * RPI + lane / LPR, c = lane % LPR * (16 / ES);
+                    const u4 v = *reinterpret_cast<const u4*>(mine + r * ROWB + lane % LPR * 16);
+                    const int row = wm0 + 32 * i + r, col = wn0 + c, left = N - n0 - col;
+                    const int at = m0 + row < M ? (row * ld + col) * ES : kOOB;
+                    __builtin_amdgcn_raw_buffer_store_b128(v, rC, left >= 16 / ES ? at : kOOB, 0, 0);
+                    if (left > 0 && left < 16 / ES && at != kOOB) {
+#pragma unroll
+                        for (int e = 0; e < 16 / ES; ++e) {
+                            if (e >= left) continue;
+                            if constexpr (ES == 4)
+                                __builtin_amdgcn_raw_buffer_store_b32(v[e], rC, at + 4 * e, 0, 0);
+                            else
+                                __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(v[e / 2] >> (16 * (e % 2))), rC, at + 2 * e, 0, 0);
+                        }
+                    }
+                }
+            } else if constexpr (ES == 2) {   // rows that start inside a word: a value a lane
+                constexpr int SPAN = WTN < 64 ? WTN : 64, RPV = 64 / SPAN;
+#pragma unroll 8
+                for (int t = 0; t < 32 / RPV * (WTN / SPAN); ++t) {
+                    const int r = t / (WTN / SPAN) * RPV + lane / SPAN, c = t % (WTN / SPAN) * SPAN + lane % SPAN;
+                    const int row = wm0 + 32 * i + r, col = wn0 + c;
+                    __builtin_amdgcn_raw_buffer_store_b16(*reinterpret_cast<const unsigned short*>(mine + r * ROWB + c * 2), rC,
+                                                          m0 + row < M && n0 + col < N ? (row * ld + col) * 2 : kOOB, 0, 0);
                 }
             }
         }

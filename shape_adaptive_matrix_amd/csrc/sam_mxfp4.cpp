@@ -104,14 +104,15 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
         }
         return SAM_OK;
     }
-    // The tiles move scales four at a time: rows that are not so many get
-    // zeros behind them, X's where they are made and W's scales in a copy
-    // (its codes stay; 4096 x 11040 x 4096: 398 us with a byte load a scale).
+    // The tiles read scales as planes of dwords, X's and a copy of W's; rows
+    // that are no whole dwords get zeros behind them. (From rows of scales
+    // 4096 x 11008 x 4096 took 122 us, with a byte load a scale, as odd rows
+    // need there, 4096 x 11040 x 4096 398 us.)
     const long long kp = (kb + 3) / 4 * 4;
     if (!plan_auto(M, N, 32 * kp, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
     L->take(L->codes, 16ull * M * kp);
     L->take(L->scales, (unsigned long long)M * kp);
-    if (kp != kb) L->take(L->wscales, (unsigned long long)N * kp);
+    L->take(L->wscales, (unsigned long long)N * kp);
     if (p->split > 1) L->take(L->parts, 4ull * p->split * M * N);
     return SAM_OK;
 }
@@ -248,10 +249,11 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     q.kb = (int)kp;
     q.codes = (unsigned char*)ws + L.codes.off;
     q.scales = (unsigned char*)ws + L.scales.off;
-    if (L.wscales.bytes) {
+    if (!few) {
+        q.planes = 1;
         q.from = scales;
         q.to = (unsigned char*)ws + L.wscales.off;
-        q.pack_rows = N;
+        q.plane_rows = N;
         q.from_kb = (int)kb;
     }
     if (!rounds) {
@@ -278,7 +280,7 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
     g.A = q.codes;
     g.sa = q.scales;
     g.B = codes;
-    g.sb = L.wscales.bytes ? q.to : scales;
+    g.sb = q.to;
     g.fmt_a = g.fmt_b = 4;
     g.M = (int)M;
     g.N = (int)N;

@@ -19,11 +19,13 @@ struct Quant4Args {
     int K, kb;               // values and blocks a row
     unsigned char* codes;    // rows x kb x 16
     unsigned char* scales;   // rows x kb
-    // Beside it (rows' form): a copy of other scales, pack_rows of from_kb to
-    // rows of kb with zeros behind.
+    // For the tiles (rows' form; kb is a multiple of four then): scales as kb / 4
+    // planes of a dword for every row, and beside it those of another tensor,
+    // plane_rows of from_kb, zeros behind.
+    int planes;
     const unsigned char* from;
     unsigned char* to;
-    long long pack_rows;
+    long long plane_rows;
     int from_kb;
 };
 
@@ -72,7 +74,8 @@ hipError_t launch_quant4(int dtype, bool trans, const Quant4Args& a, hipStream_t
 hipError_t launch_dequant4(int dtype, const Dequant4Args& a, hipStream_t s);
 hipError_t launch_join4(int dtype, const Join4Args& a, hipStream_t s);
 // A product of E2M1 operands by its plan: C (or the partial sums) of type
-// `out` at a.out with row stride a.ldc, Bt's rows of a.ldb values.
+// `out` at a.out with row stride a.ldc, Bt's rows of a.ldb values, scales in
+// planes.
 hipError_t launch_tile4(const Plan& p, const GemmArgs& a, int out, hipStream_t s);
 
 }  // namespace sam
