@@ -415,7 +415,8 @@ sam_status sam_distill(sam_dtype dtype, int64_t rows, int64_t V, int64_t top,
  *           element k of a row in the low half of its byte k / 2 for even k.
  *   scales  device, rows x ceil(K / 32) bytes, compact, any alignment.
  * codes and scales overlap neither X nor each other. K >= 1, rows *
- * ceil(K / 32) below 2^31; rows == 0 is a no-op. Asynchronous on `stream`. */
+ * ceil(K / 32) up to 2^31 - 4096; rows == 0 is a no-op. Asynchronous on
+ * `stream`. */
 sam_status sam_quantize_mxfp4(sam_dtype dtype, sam_op trans, int64_t rows,
                               int64_t K, const void* X, int64_t ldx,
                               uint8_t* codes, uint8_t* scales, void* stream);
@@ -444,7 +445,8 @@ sam_status sam_dequantize_mxfp4(sam_dtype dtype, int64_t rows, int64_t K,
  *   Y       device, M rows of N values, row stride ldy >= N; write-only.
  * X and Y are aligned to one value. A block of X or of the weight that stands
  * for NaN makes the results of its row (of its column) NaN. N, K >= 1, they
- * and ldy up to 2.08 M; M == 0 is a no-op; a single row's stride may be any. Y overlaps
+ * and ldy up to 2.08 M, M * ceil(max(N, K) / 128) and N * ceil(K / 128) up to
+ * 2^29 - 2^26; M == 0 is a no-op; a single row's stride may be any. Y overlaps
  * nothing else. Workspace: sam_linear_mxfp4_workspace() bytes,
  * SAM_ERR_WORKSPACE when short. Asynchronous on `stream`, no atomics, a fixed
  * order. */

@@ -161,8 +161,8 @@ gemm_mx8_kernel(GemmArgs args)
             if constexpr (OUT >= 0) {
                 // Scales by dwords, each a plane of all rows: a load is 256
                 // contiguous bytes. From rows of scales every lane's dword
-                // lies in a line of its own, of which the L1 keeps nothing
-                // until the next stage: three times the operands' traffic.
+                // lies in a line of its own, 64 of them a load (4096 x 11008 x
+                // 4096 without the rounding: 99 us here, from rows 105).
                 const long long rows = is_a ? M : N, row0 = (is_a ? m0 : n0) + r;
                 lds_load4(rsrc_words((is_a ? args.sa : args.sb) + (kb / 4 * rows + row0) * 4, kb * 32 < kend ? (rows - row0) * 4 : 0), dst,
                           lane * 4);
@@ -378,9 +378,10 @@ gemm_mx8_kernel(GemmArgs args)
     const int lrow = lane & 31, lgrp = lane >> 5;
     if constexpr (OUT >= 0) {
         // Values to nearest even. Lane l holds row l % 32 of a block, columns
-        // 8 g + 4 (l / 32) .. + 3 in registers 4 g .. 4 g + 3. Through LDS (an
-        // eighth of the wave's rows at a time, in the ring's place) to stores
-        // of 16 bytes, WTN columns of a row next to each other.
+        // 8 g + 4 (l / 32) .. + 3 in registers 4 g .. 4 g + 3. Through LDS (32
+        // of the wave's rows at a time, in the ring's place) to stores of 16
+        // bytes, WTN columns of a row next to each other. (Stored from the
+        // registers, 8 bytes a lane: 4096 x 11008 x 4096 99 us, so 92.)
         constexpr int ES = OUT == DT_F32 ? 4 : 2;
         constexpr int ROWB = WTN * ES + 16;                // a row in LDS, on banks of its own
         constexpr int LPR = WTN * ES / 16, RPI = 64 / LPR; // lanes to a row, rows an instruction

@@ -9,6 +9,9 @@ using namespace sam;
 namespace {
 
 constexpr long long kMostRow = 0x7FFFFFF0ll / (257 * 4);   // the products' offset range
+// Blocks of a tensor, and those of a product's operands in whole 128 values: a
+// launch has up to 2^32 threads, two a block (and the copies of the scales).
+constexpr long long kMostBlocks = (1ll << 31) - 4096, kMostOperand = (1ll << 31) - (1ll << 28);
 
 int elem(int dtype) { return dtype == SAM_F32 ? 4 : 2; }
 
@@ -49,7 +52,7 @@ long long blocks_of(long long K) { return (K + 31) / 32; }
 sam_status check_tensor(int dtype, long long rows, long long K, long long lines, long long line, long long ldx)
 {
     if (!value_type(dtype)) return api_fail(SAM_ERR_INVALID_ARG, "bad dtype %d", dtype);
-    if (rows < 0 || K < 1 || rows > (1ll << 30) || K > (1ll << 31) - 64 || rows > ((1ll << 31) - 1) / blocks_of(K))
+    if (rows < 0 || K < 1 || rows > (1ll << 30) || K > (1ll << 31) - 64 || rows > kMostBlocks / blocks_of(K))
         return api_fail(SAM_ERR_INVALID_ARG, "bad sizes rows=%lld K=%lld", rows, K);
     if (lines > 1 && (ldx < line || ldx > (1ll << 40)))
         return api_fail(SAM_ERR_INVALID_ARG, "row stride %lld (rows of %lld)", ldx, line);
@@ -85,8 +88,9 @@ sam_status check_linear(int dtype, int out, long long M, long long N, long long 
     if (M < 0 || N < 1 || K < 1 || N > kMostRow || K > kMostRow)
         return api_fail(SAM_ERR_INVALID_ARG, "bad sizes M=%lld N=%lld K=%lld", M, N, K);
     const long long wide = N > K ? N : K;
-    if (M > (1ll << 30) || M > ((1ll << 31) - 1) / blocks_of(wide))
+    if (M > (1ll << 30) || M > kMostOperand / ((wide + 127) / 128 * 4))
         return api_fail(SAM_ERR_INVALID_ARG, "M=%lld too many rows", M);
+    if (N > kMostOperand / ((K + 127) / 128 * 4)) return api_fail(SAM_ERR_INVALID_ARG, "weight N=%lld K=%lld too large", N, K);
     return SAM_OK;
 }
 
@@ -105,9 +109,9 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
         return SAM_OK;
     }
     // The tiles read scales as planes of dwords, X's and a copy of W's; rows
-    // that are no whole dwords get zeros behind them. (From rows of scales
-    // 4096 x 11008 x 4096 took 122 us, with a byte load a scale, as odd rows
-    // need there, 4096 x 11040 x 4096 398 us.)
+    // that are no whole dwords get zeros behind them. (4096 x 11008 x 4096, the
+    // first size N: 107 us, from rows of scales 122. 4096 x 11040 x 4096 with
+    // K = 11040 117, with the byte loads that odd rows need there 398.)
     const long long kp = (kb + 3) / 4 * 4;
     if (!plan_auto(M, N, 32 * kp, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
     L->take(L->codes, 16ull * M * kp);

@@ -166,6 +166,27 @@ def test_linear_strides(shape, dtype):
             assert (y[M] == -7).all() and (y[:, :at] == -7).all() and (y[:, at + N:] == -7).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 77, 500), (40, 130, 2080), (70, 333, 4000), (150, 2051, 1500), (300, 515, 225)], ids=str)
+def test_linear_places(M, N, K):
+    """Scales at every byte of a word, results that start inside one, neighbours left alone."""
+    codes, scales, w = weight(N, K, 41)
+    x = normal((M, K), "bf16", 42)
+    want = sam.linear_mxfp4(x, codes, scales)
+    xq = ref.values(*ref.quantize(x), K)
+    ref.close(want, xq @ w.t(), product_bound(xq, w))
+    room = torch.full((scales.numel() + 8,), 255, device="cuda", dtype=torch.uint8)
+    for at in (1, 2, 3):
+        moved = room[at:at + scales.numel()].view_as(scales)
+        moved.copy_(scales)
+        assert torch.equal(sam.linear_mxfp4(x, codes, moved), want)
+        for out in (torch.float32, torch.bfloat16):
+            y = torch.full((M * N + 8,), 3.0, device="cuda", dtype=out)
+            sam.linear_mxfp4(x, codes, moved, Y=y[at:at + M * N].view(M, N))
+            assert torch.equal(y[at:at + M * N].view(M, N), want.to(out))
+            assert (y[:at] == 3).all() and (y[at + M * N:] == 3).all()
+        room.fill_(255)
+
+
 @pytest.mark.parametrize("M", [1, 4, 20, 70, 300])
 def test_linear_nan_stays_in_its_row_and_column(M):
     N, K = 200, 160

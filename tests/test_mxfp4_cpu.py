@@ -32,7 +32,7 @@ def back(dtype=sam.BF16, M=100, N=60, K=100, X=P, ldx=60, codes=2 * P, scales=3 
 
 @pytest.mark.parametrize("change,status", [
     (dict(dtype=sam.MXFP4), INVALID), (dict(dtype=-1), INVALID), (dict(rows=-1), INVALID), (dict(K=0), INVALID),
-    (dict(K=1 << 31), INVALID), (dict(rows=1 << 30, K=65), INVALID), (dict(ldx=99), INVALID), (dict(X=None), INVALID),
+    (dict(K=1 << 31), INVALID), (dict(rows=1 << 30, K=65), INVALID), (dict(rows=(1 << 30) - 1, K=64, ldx=64), INVALID), (dict(ldx=99), INVALID), (dict(X=None), INVALID),
     (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(X=P + 1), MISALIGNED),
     (dict(dtype=sam.F32, X=P + 2), MISALIGNED), (dict(codes=2 * P + 8), MISALIGNED)], ids=str)
 def test_tensors_refuse(change, status):
@@ -52,7 +52,8 @@ def test_tensors_more():
 @pytest.mark.parametrize("change,status", [
     (dict(dtype=sam.MXFP8), INVALID), (dict(out=sam.F16), INVALID), (dict(M=-1), INVALID), (dict(N=0), INVALID),
     (dict(K=0), INVALID), (dict(N=3 << 20), INVALID), (dict(K=3 << 20), INVALID), (dict(M=1 << 31), INVALID),
-    (dict(M=1 << 30, K=128), INVALID), (dict(ldx=59), INVALID), (dict(ldy=59), INVALID), (dict(X=None), INVALID),
+    (dict(M=1 << 30, K=128), INVALID), (dict(M=1 << 29, N=32, K=32), INVALID), (dict(N=1 << 20, K=1 << 16), INVALID),
+    (dict(ldx=59), INVALID), (dict(ldy=59), INVALID), (dict(X=None), INVALID),
     (dict(codes=None), INVALID), (dict(scales=None), INVALID), (dict(Y=None), INVALID), (dict(X=P + 1), MISALIGNED),
     (dict(codes=2 * P + 4), MISALIGNED), (dict(Y=4 * P + 2), MISALIGNED), (dict(ws=5 * P + 8), MISALIGNED),
     (dict(Y=P), INVALID), (dict(Y=2 * P), INVALID), (dict(Y=3 * P + 16), INVALID), (dict(ws=4 * P + 256), INVALID),
