@@ -289,7 +289,11 @@ hipError_t from_codes(const Stream4Args& a, hipStream_t s)
     if (bytes <= kHoldThree) return run<kCopy, DT_F32, true, MB, 1, kAhead, kHoldThree>(a, s);
     if (bytes <= kHoldTwo) return run<kCopy, DT_F32, true, MB, 1, kAhead, kHoldTwo>(a, s);
     if (bytes <= kHoldOne) return run<kCopy, DT_F32, true, MB, 1, kAhead, kHoldOne>(a, s);
-    if constexpr (MB <= 2) return run<kDirect, DT_F32, true, MB, 2, kAhead, 16>(a, s);
+    // From memory two blocks of W share X's loads, where that leaves every CU a
+    // workgroup (32 rows of 11008: N = 4096 18.4 us by two blocks, 15.0 by one;
+    // N = 8192 22.4 and 26.6).
+    if constexpr (MB <= 2)
+        return a.N <= 16 * 256 ? run<kDirect, DT_F32, true, MB, 1, kAhead, 16>(a, s) : run<kDirect, DT_F32, true, MB, 2, kAhead, 16>(a, s);
     return hipErrorInvalidValue;
 }
 

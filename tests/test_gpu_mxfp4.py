@@ -166,6 +166,25 @@ def test_linear_strides(shape, dtype):
             assert (y[M] == -7).all() and (y[:, :at] == -7).all() and (y[:, at + N:] == -7).all()
 
 
+# Few rows by what their codes take of LDS, up to none: one and two blocks of the weight, whole lines and not.
+HELD = [(16, 90, 6000), (5, 40, 16384), (24, 50, 8192), (31, 48, 8000), (64, 130, 4000), (9, 33, 33000), (16, 4200, 32768),
+        (32, 100, 11008), (17, 4128, 16401), (32, 4200, 9216)]
+
+
+@pytest.mark.parametrize("shape", HELD, ids=str)
+def test_linear_of_long_rows(shape):
+    M, N, K = shape
+    x = normal((M, K), "f16", 43)
+    codes, scales, w = weight(N, K, 44)
+    xq = ref.values(*ref.quantize(x), K)
+    want, bound = xq @ w.t(), product_bound(xq, w)
+    y = torch.full((M + 1, N), -7.0, device="cuda", dtype=torch.float16)
+    sam.linear_mxfp4(x, codes, scales, Y=y[:M])
+    ref.close(y[:M], want, bound)
+    assert (y[M] == -7).all()
+    ref.close(sam.linear_mxfp4(x, codes, scales), want, bound)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 77, 500), (40, 130, 2080), (70, 333, 4000), (150, 2051, 1500), (300, 515, 225)], ids=str)
 def test_linear_places(M, N, K):
     """Scales at every byte of a word, results that start inside one, neighbours left alone."""
