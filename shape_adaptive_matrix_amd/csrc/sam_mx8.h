@@ -333,18 +333,23 @@ gemm_mx8_kernel(GemmArgs args)
 #pragma unroll
         for (int j = 0; j < TN; ++j) fb[0][j].hi = fb[1][j].hi = u4{0, 0, 0, 0};
     }
-    // Stage 0 and its scales, drained completely (so that no scale load is
-    // still counted as pending when the loop starts), then stage 1.
+    // Stages 0 and 1; stage 0 and its scales have landed when as many loads as
+    // stage 1 has at least are left (some waves have one more). Byte form:
+    // stage 0 is drained completely, so that no scale load is still counted as
+    // pending when the loop starts.
     if constexpr (!SDMA) {
 #pragma unroll
         for (int b = 0; b < NSB; ++b) issue_scales(0, b);
     }
 #pragma unroll
     for (int q = 0; q < LPS; ++q) issue_one(0, q);
-    wait_cnt<0, 15>();
-    if constexpr (!SDMA) take_scales();
+    if constexpr (!SDMA) {
+        wait_cnt<0, 15>();
+        take_scales();
+    }
 #pragma unroll
     for (int q = 0; q < LPS; ++q) issue_one(1, q);
+    if constexpr (SDMA) wait_cnt<A_PW + B_PW + SPL / NW, 15>();
     barrier();
     if constexpr (SDMA) {
 #pragma unroll
