@@ -91,6 +91,14 @@ gemm_mx8_kernel(GemmArgs args)
     constexpr int SPL = SDMA ? (BM + BN) / 64 * SDW : 0;      // 64-row scale loads per stage
     constexpr int SPW = (SPL + NW - 1) / NW;           // ... per wave, at most
     constexpr int LPS = A_PW + B_PW + SPW;             // wave loads per stage (a wave may skip its last)
+    // Stage loads by k-steps: the last of a stage issues loads 0 .. LATE - 1 of
+    // the stage after next, the next stage's first LATE .. LATER - 1, its second
+    // the rest. All of them in the last one (68 KB a k-step of a 256 x 256
+    // E2M1 tile) take twice as long as its MFMAs, which wait behind them: E2M1
+    // 4096 x 4096 x 11008 with the rounding 119 us, so 108; E4M3 8192^3 513
+    // and 502.
+    constexpr int LATE = !SDMA ? LPS : (EB == 4 ? LPS / 2 : LPS * 3 / 4);
+    constexpr int LATER = KSTEPS > 2 && SDMA ? LATE + (LPS - LATE) / 2 : LPS;
     constexpr int NSB = TM + TN;                       // MFMA blocks whose scales a lane uses
     constexpr int NSR = SDMA ? SDW : KSTEPS;           // raw scale registers per block
     static_assert(EB == 8 || (EB == 4 && FA == 4 && FB == 4), "8-bit formats or E2M1");
@@ -103,6 +111,7 @@ gemm_mx8_kernel(GemmArgs args)
     static_assert(LPS + (SDMA ? 0 : NSB * KSTEPS) < 64, "vmcnt range");
     static_assert(BM % 64 == 0 && BN % 64 == 0, "scale loads cover 64 rows");
     static_assert(NBUF == 2, "the prologue fills two stages");
+    static_assert(!SDMA || LATE <= A_PW + B_PW, "loads that every wave has");
 
     __shared__ __attribute__((aligned(1024))) unsigned char lds[NBUF * STAGE];
 
@@ -261,11 +270,11 @@ gemm_mx8_kernel(GemmArgs args)
     // then, after the last MFMA of A block i, the next k-step's reads of A
     // block i into the same registers (A fragments are single-buffered: each
     // is dead once its row of MFMAs has issued), then its share of the stage
-    // loads (last k-step) or of the next stage's scales (first k-step:
+    // loads q0 .. q1 - 1 or of the next stage's scales (first k-step:
     // global byte loads; last k-step, SDMA: LDS reads), evenly spread over
     // the slots.
     auto kstep = [&](u8v (&fa)[TM], const u8v (&fb)[TN], int t, const unsigned char* rbuf, int rt,
-                     u8v (&nb)[TN], int load_stage, int scale_stage, int sread_stage) {
+                     u8v (&nb)[TN], int load_stage, int q0, int q1, int scale_stage, int sread_stage) {
 #pragma unroll
         for (int m = 0; m < NMF; ++m) {
             const int i = m / TN, j = m % TN;
@@ -303,8 +312,8 @@ gemm_mx8_kernel(GemmArgs args)
             }
             if (load_stage >= 0) {
 #pragma unroll
-                for (int q = (m * LPS + NMF - 1) / NMF; q < ((m + 1) * LPS + NMF - 1) / NMF; ++q)
-                    if (q < LPS) issue_one(load_stage, q);
+                for (int q = q0 + (m * (q1 - q0) + NMF - 1) / NMF; q < q0 + ((m + 1) * (q1 - q0) + NMF - 1) / NMF; ++q)
+                    if (q < q1) issue_one(load_stage, q);
             }
             if (scale_stage >= 0) {
 #pragma unroll
@@ -333,8 +342,8 @@ gemm_mx8_kernel(GemmArgs args)
 #pragma unroll
         for (int j = 0; j < TN; ++j) fb[0][j].hi = fb[1][j].hi = u4{0, 0, 0, 0};
     }
-    // Stages 0 and 1; stage 0 and its scales have landed when as many loads as
-    // stage 1 has at least are left (some waves have one more). Byte form:
+    // Stage 0 and what the loop does not load of stage 1; stage 0 and its
+    // scales have landed when as many loads as that are left. Byte form:
     // stage 0 is drained completely, so that no scale load is still counted as
     // pending when the loop starts.
     if constexpr (!SDMA) {
@@ -348,8 +357,8 @@ gemm_mx8_kernel(GemmArgs args)
         take_scales();
     }
 #pragma unroll
-    for (int q = 0; q < LPS; ++q) issue_one(1, q);
-    if constexpr (SDMA) wait_cnt<A_PW + B_PW + SPL / NW, 15>();
+    for (int q = 0; q < LATE; ++q) issue_one(1, q);
+    if constexpr (SDMA) wait_cnt<LATE, 15>();
     barrier();
     if constexpr (SDMA) {
 #pragma unroll
@@ -364,17 +373,18 @@ gemm_mx8_kernel(GemmArgs args)
         const unsigned char* cur = lds + (k % NBUF) * STAGE;
         const unsigned char* nxt = lds + ((k + 1) % NBUF) * STAGE;
         // k-steps 0 .. KSTEPS-2 of stage k, each reading the next k-step; the
-        // first also loads stage k+1's scales.
+        // first also loads stage k+1's scales (byte form), the first two the
+        // rest of its operands (SDMA).
 #pragma unroll
         for (int t = 0; t + 1 < KSTEPS; ++t)
-            kstep(fa, fb[t & 1], t, cur, t + 1, fb[(t + 1) & 1], -1, (!SDMA && t == 0) ? k + 1 : -1, -1);
+            kstep(fa, fb[t & 1], t, cur, t + 1, fb[(t + 1) & 1], t < 2 && LATE < LPS ? k + 1 : -1, t ? LATER : LATE, t ? LPS : LATER, (!SDMA && t == 0) ? k + 1 : -1, -1);
         // Stage k fully read by this wave; stage k+1 and its scales landed.
         wait_cnt<0, 0>();
         barrier();
         // Last k-step of stage k: read k-step 0 of stage k+1 (and, SDMA, its
-        // scales) and refill the slot stage k leaves with stage k + 2.
+        // scales) and start to refill the slot stage k leaves with stage k + 2.
         constexpr int L = (KSTEPS - 1) & 1;
-        kstep(fa, fb[L], KSTEPS - 1, nxt, 0, fb[L ^ 1], k + NBUF, -1, SDMA ? k + 1 : -1);
+        kstep(fa, fb[L], KSTEPS - 1, nxt, 0, fb[L ^ 1], k + NBUF, 0, LATE, -1, SDMA ? k + 1 : -1);
         static_assert(L == 1, "an even number of k-steps per stage");
         take_scales();
     }
