@@ -59,6 +59,10 @@ struct Variant {
 int variant_count();
 const Variant* variant_get(int id);
 
+// Dwords of a plane of block scales (four blocks of every row in a dword), so
+// that each plane starts on 16 bytes.
+constexpr long long scale_rows(long long rows) { return (rows + 3) / 4 * 4; }
+
 // Arguments of one main-kernel launch.
 struct GemmArgs {
     const void* A;

@@ -44,7 +44,7 @@ __device__ __forceinline__ void to_planes(const Quant4Args& a, unsigned wg)
     }
 #pragma unroll
     for (int i = 0; i < kPlanesEach; ++i)
-        if (p0 + i < a.kb / 4) reinterpret_cast<unsigned*>(a.to)[(p0 + i) * a.plane_rows + row] = d[i];
+        if (p0 + i < a.kb / 4) reinterpret_cast<unsigned*>(a.to)[(p0 + i) * scale_rows(a.plane_rows) + row] = d[i];
 }
 
 // A quarter of a block a lane: 16 (FP32: 32) bytes in, 4 out, both whole
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kQuantThreads) quant4_rows_kernel(Quant4Args a
             unsigned d = code << (8 * (q[i] >> 2 & 3));
             d |= __builtin_amdgcn_update_dpp(0u, d, 0x124, 0xF, 0xF, true);   // of 4, then 8 lanes round
             d |= __builtin_amdgcn_update_dpp(0u, d, 0x128, 0xF, 0xF, true);
-            if ((q[i] & 15) == 0 && row[i] < a.rows) reinterpret_cast<unsigned*>(a.scales)[(q[i] >> 4) * a.rows + row[i]] = d;
+            if ((q[i] & 15) == 0 && row[i] < a.rows) reinterpret_cast<unsigned*>(a.scales)[(q[i] >> 4) * scale_rows(a.rows) + row[i]] = d;
         }
         if (row[i] < a.rows) {
             reinterpret_cast<unsigned*>(a.codes)[row[i] * per_row + q[i]] = c;

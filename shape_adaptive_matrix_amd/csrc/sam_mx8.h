@@ -64,7 +64,8 @@ template <> struct Half<DT_F16> { typedef _Float16 T; };
 // split's) of that type (DT_F32, DT_BF16, DT_F16) with row stride ldc, and Bt's
 // rows of ldb values: K may be rounded up past them, for what A holds there
 // are zeros and what Bt's next row holds are finite E2M1 values. The scales
-// are K / 128 planes then, of a dword for every row.
+// are K / 128 planes then, of a dword for every row (scale_rows, so that a
+// plane starts on 16 bytes).
 template <int FA, int FB, int BM, int BN, int WM, int WN, int BK, bool SDMA, int EB, int OUT = -1>
 __global__ void __launch_bounds__(WM * WN * 64)
 __attribute__((amdgpu_waves_per_eu(1, (160 * 1024 / (2 * (BM + BN) * (BK + 8))) * WM * WN / 4 > 0
@@ -85,10 +86,12 @@ gemm_mx8_kernel(GemmArgs args)
     constexpr int KSTEPS = BK / 64;                    // MFMA k-steps per stage
     constexpr int A_BYTES = BM * ROW, B_BYTES = BN * ROW;
     constexpr int SDW = BK / 128;                      // scale dwords per row per stage (SDMA)
-    constexpr int S_BYTES = SDMA ? (BM + BN) * SDW * 4 : 0;   // [dword d][A rows, then Bt rows]
+    constexpr int S_BYTES = SDMA ? (BM + BN) * SDW * 4 : 0;   // [dword d][A rows, then Bt rows]; OUT: A's dwords, then Bt's
     constexpr int STAGE = A_BYTES + B_BYTES + S_BYTES;
     constexpr int A_PW = A_BYTES / 1024 / NW, B_PW = B_BYTES / 1024 / NW;
-    constexpr int SPL = SDMA ? (BM + BN) / 64 * SDW : 0;      // 64-row scale loads per stage
+    // Scale loads per stage: a dword of 64 rows each (OUT: four rows a lane).
+    constexpr int SPA = BM * SDW / 256;                // of A (OUT)
+    constexpr int SPL = SDMA ? (OUT >= 0 ? SPA + BN * SDW / 256 : (BM + BN) / 64 * SDW) : 0;
     constexpr int SPW = (SPL + NW - 1) / NW;           // ... per wave, at most
     constexpr int LPS = A_PW + B_PW + SPW;             // wave loads per stage (a wave may skip its last)
     // Stage loads by k-steps: the last of a stage issues loads 0 .. LATE - 1 of
@@ -110,6 +113,7 @@ gemm_mx8_kernel(GemmArgs args)
     static_assert(NBUF * STAGE <= 160 * 1024, "LDS");
     static_assert(LPS + (SDMA ? 0 : NSB * KSTEPS) < 64, "vmcnt range");
     static_assert(BM % 64 == 0 && BN % 64 == 0, "scale loads cover 64 rows");
+    static_assert(OUT < 0 || (BM * SDW % 256 == 0 && BN * SDW % 256 == 0), "1 KB scale loads");
     static_assert(NBUF == 2, "the prologue fills two stages");
     static_assert(!SDMA || LATE <= A_PW + B_PW, "loads that every wave has");
 
@@ -161,21 +165,29 @@ gemm_mx8_kernel(GemmArgs args)
             // zero.
             const int sq = wave + (q - A_PW - B_PW) * NW;
             if (SPL % NW != 0 && sq >= SPL) return;
-            constexpr int G = (BM + BN) / 64;              // 64-row groups
-            const int d = sq / G, grp = sq % G;
-            const bool is_a = grp * 64 < BM;
-            const int r = grp * 64 - (is_a ? 0 : BM);      // first row of A or of Bt
-            const int kb = k0 / 32 + 4 * d;
-            const unsigned dst = lds_addr(buf + A_BYTES + B_BYTES + (d * (BM + BN) + grp * 64) * 4);
             if constexpr (OUT >= 0) {
-                // Scales by dwords, each a plane of all rows: a load is 256
-                // contiguous bytes. From rows of scales every lane's dword
-                // lies in a line of its own, 64 of them a load (4096 x 11008 x
-                // 4096 without the rounding: 99 us here, from rows 105).
-                const long long rows = is_a ? M : N, row0 = (is_a ? m0 : n0) + r;
-                lds_load4(rsrc_words((is_a ? args.sa : args.sb) + (kb / 4 * rows + row0) * 4, kb * 32 < kend ? (rows - row0) * 4 : 0), dst,
-                          lane * 4);
+                // Scales by dwords, each a plane of all rows: a lane takes
+                // those of four. (From rows of scales every lane's dword lies
+                // in a line of its own, 64 of them a load of 256 bytes: 4096 x
+                // 11008 x 4096 without the rounding 105 us, from planes 99.)
+                // Rows past M / N have any scales, for zeros.
+                const bool is_a = sq < SPA;
+                const int u = is_a ? sq : sq - SPA;
+                const int at = u * 256 + lane * 4;               // row d R + r of the operand's R rows
+                const int d = is_a ? at / BM : at / BN, r = is_a ? at % BM : at % BN;
+                const long long rows = scale_rows(is_a ? M : N);
+                const unsigned char* base = (is_a ? args.sa : args.sb) + (k0 / 128 * rows + (is_a ? m0 : n0)) * 4;
+                const unsigned off = ((unsigned)d * (unsigned)rows + (unsigned)r) * 4;
+                lds_load16(rsrc_words(base, ((K / 128 - k0 / 128) * rows - (is_a ? m0 : n0)) * 4),
+                           lds_addr(buf + A_BYTES + B_BYTES + (is_a ? 0 : BM * SDW * 4) + u * 1024),
+                           k0 + 128 * d < kend ? (int)off : kOOB);
             } else {
+                constexpr int G = (BM + BN) / 64;              // 64-row groups
+                const int d = sq / G, grp = sq % G;
+                const bool is_a = grp * 64 < BM;
+                const int r = grp * 64 - (is_a ? 0 : BM);      // first row of A or of Bt
+                const int kb = k0 / 32 + 4 * d;
+                const unsigned dst = lds_addr(buf + A_BYTES + B_BYTES + (d * (BM + BN) + grp * 64) * 4);
                 const int first = kb * 32 < kend ? r * KB + kb : kOOB;
                 lds_load4(is_a ? rSAw : rSBw, dst, (int)((unsigned)first + (unsigned)(lane * KB)));   // rows past M / N: past the record count
             }
@@ -223,10 +235,12 @@ gemm_mx8_kernel(GemmArgs args)
 
     // SDMA: the scale dwords of block b's rows for the stage in `buf`.
     auto read_scales = [&](const unsigned char* buf, int b) {
-        const int r = (b < TM ? wm0 + 32 * b : BM + wn0 + 32 * (b - TM)) + (lane & 31);
+        const int r = (b < TM ? wm0 + 32 * b : wn0 + 32 * (b - TM)) + (lane & 31);
 #pragma unroll
-        for (int d = 0; d < NSR; ++d)
-            sn[b][d] = *reinterpret_cast<const unsigned*>(buf + A_BYTES + B_BYTES + (d * (BM + BN) + r) * 4);
+        for (int d = 0; d < NSR; ++d) {
+            const int at = OUT >= 0 ? (b < TM ? d * BM : SDW * BM + d * BN) : d * (BM + BN) + (b < TM ? 0 : BM);
+            sn[b][d] = *reinterpret_cast<const unsigned*>(buf + A_BYTES + B_BYTES + (at + r) * 4);
+        }
     };
 
     // Fragment reads, one 128-bit LDS read each; RPB per MFMA block: read

@@ -115,8 +115,8 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
     const long long kp = (kb + 3) / 4 * 4;
     if (!plan_auto(M, N, 32 * kp, DT_MX4, p)) return api_fail(SAM_ERR_INTERNAL, "no admissible plan");
     L->take(L->codes, 16ull * M * kp);
-    L->take(L->scales, (unsigned long long)M * kp);
-    L->take(L->wscales, (unsigned long long)N * kp);
+    L->take(L->scales, (unsigned long long)scale_rows(M) * kp);
+    L->take(L->wscales, (unsigned long long)scale_rows(N) * kp);
     if (p->split > 1) L->take(L->parts, 4ull * p->split * M * N);
     return SAM_OK;
 }

@@ -20,8 +20,8 @@ struct Quant4Args {
     unsigned char* codes;    // rows x kb x 16
     unsigned char* scales;   // rows x kb
     // For the tiles (rows' form; kb is a multiple of four then): scales as kb / 4
-    // planes of a dword for every row, and beside it those of another tensor,
-    // plane_rows of from_kb, zeros behind.
+    // planes of scale_rows() dwords, and beside it those of another tensor,
+    // plane_rows of from_kb, zeros behind a row.
     int planes;
     const unsigned char* from;
     unsigned char* to;

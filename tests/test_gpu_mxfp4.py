@@ -185,6 +185,19 @@ def test_linear_of_long_rows(shape):
     ref.close(sam.linear_mxfp4(x, codes, scales), want, bound)
 
 
+@pytest.mark.parametrize("M,N,K", [(70, 333, 4000), (150, 2051, 1500), (301, 515, 225), (1025, 130, 700)], ids=str)
+def test_what_a_workspace_held(M, N, K):
+    """Scales of NaN left behind in a workspace, also beside the last rows, reach no result."""
+    codes, scales, w = weight(N, K, 45)
+    x = normal((M, K), "bf16", 46)
+    want = sam.linear_mxfp4(x, codes, scales)
+    xq = ref.values(*ref.quantize(x), K)
+    ref.close(want, xq @ w.t(), product_bound(xq, w))
+    for left in (0, 255):
+        workspace = torch.full((32 << 20,), left, device="cuda", dtype=torch.uint8)
+        assert torch.equal(sam.linear_mxfp4(x, codes, scales, workspace=workspace), want)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 77, 500), (40, 130, 2080), (70, 333, 4000), (150, 2051, 1500), (300, 515, 225)], ids=str)
 def test_linear_places(M, N, K):
     """Scales at every byte of a word, results that start inside one, neighbours left alone."""
