@@ -27,7 +27,7 @@ const Form kForms[] = {SAM_MX8_VARIANTS(SAM_TILE4_ENTRY)};
 
 }  // namespace
 
-// K is a multiple of 128: scales travel as 4-byte words.
+// K is a multiple of 128: scales come as planes of dwords.
 hipError_t launch_tile4(const Plan& p, const GemmArgs& a, int out, hipStream_t s)
 {
     for (const Form& f : kForms) {
