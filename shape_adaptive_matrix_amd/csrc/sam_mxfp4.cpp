@@ -131,16 +131,15 @@ sam_status backward_layout(int dtype, int out, long long M, long long N, long lo
     L->take(L->w, (unsigned long long)N * row * elem(dtype));
     uint64_t inner = 0;
     sam_status e;
-    // Strides do not change what the products' own workspace holds beyond a
-    // copy of dY, for which the largest is taken.
+    // The products copy operands and results whose rows are no whole 16-byte
+    // pieces: room for both copies, by strides of that kind, serves every
+    // stride.
     if (dtype == SAM_F32) {
-        uint64_t other = 0;
-        e = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, N + 1, row, K + 1, 1.0f, 0.0f, &inner);
-        if (e == SAM_OK) e = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, N, row, K, 1.0f, 0.0f, &other);
-        if (other > inner) inner = other;
+        auto odd = [](long long n) { return n % 4 == 3 ? n + 2 : n + 1; };   // neither n nor whole pieces
+        e = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, odd(N), row, odd(K), 1.0f, 0.0f, &inner);
     } else {
         L->take(L->ids, 4ull * M);
-        e = sam_adapter_gemm_workspace((sam_dtype)dtype, SAM_OP_N, M, K, N, 0, 1, N + 1, row, &inner);
+        e = sam_adapter_gemm_workspace((sam_dtype)dtype, SAM_OP_N, M, K, N, 0, 1, N % 8 ? N : N + 1, row, &inner);
     }
     if (e != SAM_OK) return e;
     L->take(L->inner, inner);
