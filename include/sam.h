@@ -467,7 +467,7 @@ sam_status sam_linear_mxfp4_workspace(sam_dtype dtype, sam_dtype out, int64_t M,
  * dtype, as sam_dequantize_mxfp4 gives it. dX (type `out`: SAM_F32 or dtype, row stride
  * lddx >= K) is written whole. dY and dX must be 16-byte aligned; strides up
  * to 2.08 M values (a single row's may be any). Everything else as for
- * sam_linear_mxfp4. */
+ * sam_linear_mxfp4, the workspace by sam_linear_mxfp4_backward_workspace(). */
 sam_status sam_linear_mxfp4_backward(sam_dtype dtype, int64_t M, int64_t N,
                                      int64_t K, const void* dY, int64_t lddy,
                                      const uint8_t* codes,
@@ -475,10 +475,16 @@ sam_status sam_linear_mxfp4_backward(sam_dtype dtype, int64_t M, int64_t N,
                                      void* dX, int64_t lddx, void* workspace,
                                      uint64_t workspace_bytes, void* stream);
 
-/* Workspace bytes sam_linear_mxfp4_backward needs (host only). */
+/* Workspace bytes sam_linear_mxfp4_backward needs (host only): for any
+ * strides, or (_strided) for these. In it lies the weight in dtype, N rows of K
+ * values; beside it what the product takes, with strides that are no whole 16
+ * bytes also a copy of dY and (FP32) one of dX. */
 sam_status sam_linear_mxfp4_backward_workspace(sam_dtype dtype, sam_dtype out,
                                                int64_t M, int64_t N, int64_t K,
                                                uint64_t* bytes);
+sam_status sam_linear_mxfp4_backward_workspace_strided(
+    sam_dtype dtype, sam_dtype out, int64_t M, int64_t N, int64_t K,
+    int64_t lddy, int64_t lddx, uint64_t* bytes);
 
 /* Log probabilities of given tokens, with the entropy and the most likely
  * entries of every row of logits z at temperature T:

@@ -133,6 +133,8 @@ def lib() -> ctypes.CDLL:
                                       ctypes.c_int),
         "sam_linear_mxfp4_backward_workspace": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, ctypes.POINTER(u64)],
                                                 ctypes.c_int),
+        "sam_linear_mxfp4_backward_workspace_strided": ([ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, i64,
+                                                         ctypes.POINTER(u64)], ctypes.c_int),
         "sam_token_logprobs": ([ctypes.c_int, i64, i64, i64, vp, i64, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, u64, vp],
                                ctypes.c_int),
         "sam_token_logprobs_workspace": ([ctypes.c_int, i64, i64, i64, ctypes.POINTER(u64)], ctypes.c_int),
@@ -914,7 +916,7 @@ def linear_mxfp4_backward(dY, codes, scales, K=None, dX=None, out_dtype=None, wo
             return linear_mxfp4_backward(dY, codes, scales, K, dX, out_dtype, workspace, stream)
     dX, out, lddx = _adapter_result(dX, M, K, out_dtype, dY, code, "dX", stream)
     if workspace is None:
-        need = _adapter_workspace_bytes("sam_linear_mxfp4_backward_workspace", code, out, M, N, K)
+        need = _adapter_workspace_bytes("sam_linear_mxfp4_backward_workspace_strided", code, out, M, N, K, lddy, lddx)
         workspace = _adapter_workspace(need, dY, stream)
     else:
         need = _workspace_bytes(workspace)

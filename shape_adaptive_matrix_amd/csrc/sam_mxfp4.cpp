@@ -121,29 +121,36 @@ sam_status forward_layout(int dtype, int out, long long M, long long N, long lon
     return SAM_OK;
 }
 
-sam_status backward_layout(int dtype, int out, long long M, long long N, long long K, Layout* L)
+// The products copy operands and results whose rows are no whole 16-byte
+// pieces, so what they take depends on the strides.
+sam_status backward_layout(int dtype, int out, long long M, long long N, long long K, long long lddy, long long lddx, Layout* L)
 {
-    const sam_status st = check_linear(dtype, out, M, N, K);
+    sam_status st = check_linear(dtype, out, M, N, K);
     if (st != SAM_OK) return st;
     *L = Layout{};
     if (M == 0) return SAM_OK;
+    if (lddy < N || lddx < K || lddy > kMostRow || lddx > kMostRow)
+        return api_fail(SAM_ERR_INVALID_ARG, "row stride lddy=%lld (rows of %lld) or lddx=%lld (rows of %lld)", lddy, N, lddx, K);
     const long long row = dtype == SAM_F32 ? (K + 3) / 4 * 4 : (K + 7) / 8 * 8;
     L->take(L->w, (unsigned long long)N * row * elem(dtype));
     uint64_t inner = 0;
-    sam_status e;
-    // The products copy operands and results whose rows are no whole 16-byte
-    // pieces: room for both copies, by strides of that kind, serves every
-    // stride.
     if (dtype == SAM_F32) {
-        auto odd = [](long long n) { return n % 4 == 3 ? n + 2 : n + 1; };   // neither n nor whole pieces
-        e = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, odd(N), row, odd(K), 1.0f, 0.0f, &inner);
+        st = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, lddy, row, lddx, 1.0f, 0.0f, &inner);
     } else {
         L->take(L->ids, 4ull * M);
-        e = sam_adapter_gemm_workspace((sam_dtype)dtype, SAM_OP_N, M, K, N, 0, 1, N % 8 ? N : N + 1, row, &inner);
+        st = sam_adapter_gemm_workspace((sam_dtype)dtype, SAM_OP_N, M, K, N, 0, 1, lddy, row, &inner);
     }
-    if (e != SAM_OK) return e;
+    if (st != SAM_OK) return st;
     L->take(L->inner, inner);
     return SAM_OK;
+}
+
+// A stride for rows of n values that takes the most: neither n nor whole
+// 16-byte pieces.
+long long worst_stride(long long n, int es)
+{
+    const long long ld = (n + 1) * es % 16 ? n + 1 : n + 2;
+    return ld > kMostRow ? kMostRow : ld;
 }
 
 }  // namespace
@@ -313,8 +320,22 @@ sam_status sam_linear_mxfp4(sam_dtype dtype, int64_t M, int64_t N, int64_t K, co
 sam_status sam_linear_mxfp4_backward_workspace(sam_dtype dtype, sam_dtype out, int64_t M, int64_t N, int64_t K, uint64_t* bytes)
 {
     if (!bytes) return api_fail(SAM_ERR_INVALID_ARG, "bytes is null");
+    sam_status st = check_linear(dtype, out, M, N, K);
+    if (st != SAM_OK) return st;
     Layout L;
-    const sam_status st = backward_layout(dtype, out, M, N, K, &L);
+    st = backward_layout(dtype, out, M, N, K, worst_stride(N, elem(dtype)), worst_stride(K, elem(dtype)), &L);
+    if (st != SAM_OK) return st;
+    *bytes = L.total;
+    return api_ok();
+}
+
+sam_status sam_linear_mxfp4_backward_workspace_strided(sam_dtype dtype, sam_dtype out, int64_t M, int64_t N, int64_t K,
+                                                       int64_t lddy, int64_t lddx, uint64_t* bytes)
+{
+    if (!bytes) return api_fail(SAM_ERR_INVALID_ARG, "bytes is null");
+    if (M == 1) lddy = N, lddx = K;   // a single row's strides reach nothing
+    Layout L;
+    const sam_status st = backward_layout(dtype, out, M, N, K, lddy, lddx, &L);
     if (st != SAM_OK) return st;
     *bytes = L.total;
     return api_ok();
@@ -324,14 +345,11 @@ sam_status sam_linear_mxfp4_backward(sam_dtype dtype, int64_t M, int64_t N, int6
                                      const uint8_t* codes, const uint8_t* scales, sam_dtype out, void* dX, int64_t lddx,
                                      void* workspace, uint64_t workspace_bytes, void* stream)
 {
+    if (M == 1) lddy = N, lddx = K;
     Layout L;
-    sam_status st = backward_layout(dtype, out, M, N, K, &L);
+    sam_status st = backward_layout(dtype, out, M, N, K, lddy, lddx, &L);
     if (st != SAM_OK) return st;
     if (M == 0) return api_ok();
-    if (M > 1 && (lddy < N || lddx < K || lddy > kMostRow || lddx > kMostRow))
-        return api_fail(SAM_ERR_INVALID_ARG, "row stride lddy=%lld (rows of %lld) or lddx=%lld (rows of %lld)", (long long)lddy,
-                        (long long)N, (long long)lddx, (long long)K);
-    if (M == 1) lddy = N, lddx = K;
     const long long kb = blocks_of(K);
     const int es = elem(dtype), eo = elem(out);
     const Buf bufs[] = {
