@@ -282,7 +282,8 @@ sam_status sam_gemm_ex_variant_workspace(int32_t id, int32_t split_k,
  *           of K values (SAM_OP_T, ldw >= K).
  *   A       device, n_adapters x rank rows of K values, compact.
  *   B       device, n_adapters x rank rows of N values, compact.
- *   ids     device, M int32. 4-byte aligned, like scale.
+ *   ids     device, M int32. 4-byte aligned, like scale. With n_adapters 0
+ *           not looked at (NULL).
  *   scale   device, n_adapters floats, or NULL for 1.
  *   out     the type of Y: SAM_F32 or dtype (rounded once, to nearest even).
  *   Y       device, M rows of N values, row stride ldy >= N; write-only.

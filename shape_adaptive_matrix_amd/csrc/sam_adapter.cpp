@@ -485,7 +485,7 @@ sam_status sam_adapter_gemm(sam_dtype dtype, sam_op trans_w, int64_t M, int64_t 
         {W, span(wr, ldw, wc, 2), "W", 16, false},
         {A, 2ull * n_adapters * rank * K, "A", 16, false},
         {B, 2ull * n_adapters * rank * N, "B", 16, false},
-        {ids, 4ull * M, "ids", 4, false},
+        {ids, n_adapters ? 4ull * M : 0, "ids", 4, false},
         {scale, scale ? 4ull * n_adapters : 0, "scale", 4, false},
         {Y, span(M, ldy, N, out == SAM_F32 ? 4 : 2), "Y", 16, true},
         {workspace, workspace ? L.total : 0, "workspace", 16, true},
@@ -555,7 +555,7 @@ sam_status sam_adapter_backward(sam_dtype dtype, sam_op trans_w, int64_t M, int6
         {W, c.want_dx ? span(wr, ldw, wc, 2) : 0, "W", 16, false},
         {A, 2ull * nr * K, "A", 16, false},
         {B, 2ull * nr * N, "B", 16, false},
-        {ids, 4ull * M, "ids", 4, false},
+        {ids, n_adapters ? 4ull * M : 0, "ids", 4, false},
         {scale, scale ? 4ull * n_adapters : 0, "scale", 4, false},
         {dX, dX ? span(M, lddx, K, out == SAM_F32 ? 4 : 2) : 0, "dX", 16, true},
         {dA, dA ? 4ull * nr * K : 0, "dA", 16, true},

@@ -378,7 +378,7 @@ __device__ __forceinline__ void finish_rows(const FinishArgs& a, int wg)
     const int p = WS == 4 ? wave : 0;
     const int s0 = a.split * p / WS, s1 = a.split * (p + 1) / WS;
     const int i0 = a.r * p / WS, i1 = a.r * (p + 1) / WS;
-    int id = a.ids[m];
+    int id = a.n ? a.ids[m] : -1;
     if ((unsigned)id >= (unsigned)a.n || i0 == i1) id = -1;
 
     float4 w[UP];

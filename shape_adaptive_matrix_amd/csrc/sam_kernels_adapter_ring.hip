@@ -52,7 +52,7 @@ struct AdapterHook {
     static __device__ __forceinline__ void before(const AdapterRing& x, int m0, int wave, int lane)
     {
         if (wave * 64 < BM)
-            dma::lds_load4(dma::rsrc_words(x.ids + m0, (long long)(x.M - m0) * 4),
+            dma::lds_load4(dma::rsrc_words(x.ids + m0, x.n ? (long long)(x.M - m0) * 4 : 0),   // no adapters: no ids
                            dma::lds_addr(tile_ids<BM>() + wave * 64), (wave * 64 + lane) * 4);
     }
 

@@ -70,7 +70,7 @@ struct Region {
 
 struct Layout {
     Region codes, scales, wscales, parts;   // forward
-    Region w, ids, inner;                   // backward
+    Region w, inner;                        // backward
     unsigned long long total = 0;
     void take(Region& r, unsigned long long bytes)
     {
@@ -137,7 +137,6 @@ sam_status backward_layout(int dtype, int out, long long M, long long N, long lo
     if (dtype == SAM_F32) {
         st = sam_gemm_ex_workspace(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, lddy, row, lddx, 1.0f, 0.0f, &inner);
     } else {
-        L->take(L->ids, 4ull * M);
         st = sam_adapter_gemm_workspace((sam_dtype)dtype, SAM_OP_N, M, K, N, 0, 1, lddy, row, &inner);
     }
     if (st != SAM_OK) return st;
@@ -376,9 +375,9 @@ sam_status sam_linear_mxfp4_backward(sam_dtype dtype, int64_t M, int64_t N, int6
     if (dtype == SAM_F32)
         return sam_gemm_ex(SAM_F32, SAM_OP_N, SAM_OP_N, M, K, N, 1.0f, dY, lddy, w, row, 0.0f, static_cast<float*>(dX), lddx,
                            inner, L.inner.bytes, stream);
-    // The adapters' projection without adapters; ids that it does not look up.
-    return sam_adapter_gemm(dtype, SAM_OP_N, M, K, N, 0, 1, dY, lddy, w, row, nullptr, nullptr,
-                            reinterpret_cast<const int32_t*>(ws + L.ids.off), nullptr, out, dX, lddx, inner, L.inner.bytes, stream);
+    // The plain projection with results of either type: that of the adapters, of which there are none.
+    return sam_adapter_gemm(dtype, SAM_OP_N, M, K, N, 0, 1, dY, lddy, w, row, nullptr, nullptr, nullptr, nullptr, out, dX, lddx,
+                            inner, L.inner.bytes, stream);
 }
 
 }  // extern "C"
