@@ -95,7 +95,8 @@ __device__ __forceinline__ float log_p(float v, float m, float L, const TokenArg
 {
     if (L == -INFINITY) return L;
     if (v == -INFINITY) return v - L;
-    const float d = v - (m == -INFINITY ? 0.0f : m);
+    const float pivot = m == -INFINITY ? 0.0f : m, d = v - pivot;
+    if (d == -INFINITY) return 2.0f * ((0.5f * v - 0.5f * pivot) * a.inv_hi) - L;   // over FP32's range before the division
     return d * a.inv_hi + d * a.inv_lo - L;
 }
 
