@@ -510,8 +510,10 @@ sam_status sam_linear_mxfp4_backward_workspace_strided(
  * without any other has entropy 0, m = L = -inf and log probabilities -inf. A row that
  * holds NaN or +inf has NaN results, but its top_index are entries all the
  * same (NaN counts as the largest). V up to 2^31 - 65536, T from 2^-40 to
- * 2^40; rows == 0 is a no-op. Sums are FP32; no atomics on results, a fixed order. Results
- * overlap nothing else. Workspace: sam_token_logprobs_workspace() bytes,
+ * 2^40; rows == 0 is a no-op. Sums are FP32 and kept without the largest entry's
+ * own 1: log p, entropy and L near 0 are as exact as the probabilities beside
+ * that entry. No atomics on results, a fixed order. Results overlap nothing
+ * else. Workspace: sam_token_logprobs_workspace() bytes,
  * SAM_ERR_WORKSPACE when short. Asynchronous on `stream`. */
 sam_status sam_token_logprobs(sam_dtype dtype, int64_t rows, int64_t V,
                               int64_t top, const void* logits, int64_t ldz,

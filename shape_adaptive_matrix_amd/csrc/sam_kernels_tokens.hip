@@ -84,11 +84,52 @@ __device__ __forceinline__ void to_largest(Sums& x, float M, float scale)
     x.m = M;
 }
 
-__device__ __forceinline__ Sums wave_total(Sums x, float scale)
+// Sums of several threads. The largest value's own 1 is left out of r, so that
+// beside it nothing of the others is lost where they come to little (p near 1);
+// with no value r is -1. h as in Sums.
+struct Rest {
+    float m, r, h;
+};
+
+// What y adds to a sum relative to M >= y.m: all of it, or (own) what is left
+// beside the 1 of M itself.
+__device__ __forceinline__ void relative_to(Rest& y, float M, bool own, float scale)
 {
-    to_largest(x, wave_max(x.m), scale);
-    return {x.m, wave_sum(x.s), wave_sum(x.h)};
+    if (own) return;
+    Sums x = {y.m, 1.0f + y.r, y.h};
+    to_largest(x, M, scale);
+    y.r = x.s;
+    y.h = x.h;
 }
+
+// The first of the lanes whose value is the largest, M.
+__device__ __forceinline__ int lane_of(float v, float M)
+{
+    const u64 who = __ballot(v == M);
+    return who ? __builtin_ctzll(who) : 0;
+}
+
+__device__ __forceinline__ Rest wave_total(Rest y, float scale)
+{
+    const float M = wave_max(y.m);
+    relative_to(y, M, (int)(threadIdx.x & 63) == lane_of(y.m, M), scale);
+    return {M, wave_sum(y.r), wave_sum(y.h)};
+}
+
+// log(1 + r), also where 1 + r is rounded: what that takes from r it takes from
+// the logarithm too, in the same proportion (W. Kahan's way).
+__device__ __forceinline__ float log_of_sum(float r)
+{
+    const float w = 1.0f + r;
+    return w == 1.0f ? r : logf(w) * (r / (w - 1.0f));
+}
+
+// Below this rest the thread that has the largest value is summed once more
+// without it, by its wave: its own sum, which holds that 1, is off by some
+// 2^-24 (of 256 values some 2^-22), and with it log p, the entropy and 1 - p of a
+// row whose p is near 1. One more trip to memory for such rows: 4096 x 32768
+// bf16, all of them so, 51 us instead of 49; 2048 x 131072 FP32 160, 155.
+constexpr float kSmallRest = 0.25f;
 
 // log p of a value of a row with norm (m, L); with m = -inf the pivot is 0.
 __device__ __forceinline__ float log_p(float v, float m, float L, const TokenArgs& a)
@@ -101,11 +142,11 @@ __device__ __forceinline__ float log_p(float v, float m, float L, const TokenArg
 }
 
 // What a row's results are made of, by one thread.
-__device__ __forceinline__ void write_row(const TokenArgs& a, long long row, const Sums& x, float L, float z_token)
+__device__ __forceinline__ void write_row(const TokenArgs& a, long long row, const Rest& x, float L, float z_token)
 {
     const bool has = (unsigned)a.token[row] < (unsigned)a.V;
     a.logprob[row] = has ? log_p(z_token, x.m, L, a) : 0.0f;
-    a.entropy[row] = L == -INFINITY ? 0.0f : fmaxf(L - kLn2 * (x.h / x.s), L != L ? L : 0.0f);
+    a.entropy[row] = L == -INFINITY ? 0.0f : fmaxf(L - kLn2 * (x.h / (1.0f + x.r)), L != L ? L : 0.0f);
     a.norm[2 * row] = x.m;
     a.norm[2 * row + 1] = L;
 }
@@ -229,7 +270,7 @@ __device__ __forceinline__ float bound_of(const unsigned (&k)[G], int top)
 // A row, or a part of one (a.parts > 1), on NT threads that hold P pieces
 // each of it, and the next P on the way.
 template <int DT, int NT, int P, bool TOP>
-__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6 : 8))) tokens_kernel(TokenArgs a)
+__global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(!TOP ? 8 : (NT == 64 ? 4 : 6)))) tokens_kernel(TokenArgs a)
 {
     typedef Piece<DT> Pc;
     typedef typename Pc::T T;
@@ -244,7 +285,7 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
     __shared__ __attribute__((aligned(16))) u64 room[TOP ? ROOM + 8 : 1];
     __shared__ unsigned short ids[TOP ? kEntries : 1], best[TOP ? NT : 1];
     __shared__ int counts[NW], pieces_found, entries;
-    __shared__ Sums wave_sums[NW];
+    __shared__ Rest wave_sums[NW];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const long long row = blockIdx.x / (unsigned)a.parts;
@@ -376,24 +417,51 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
         best[tid] = x.s != x.s ? 0xFFFF : (unsigned short)(order_of(x.m) >> 16);
         if (tid == 0) pieces_found = entries = 0;
     }
-    x = wave_total(x, a.scale);
+    // The wave's sums, without the largest value.
+    const float largest = wave_max(x.m);
+    const int owner = lane_of(x.m, largest);
+    to_largest(x, largest, a.scale);
+    Rest rest = {largest, wave_sum(lane == owner ? x.s - 1.0f : x.s), wave_sum(x.h)};
+    if (fabsf(rest.r) < kSmallRest) {
+        float s = lane == owner ? 0.0f : x.s, h = lane == owner ? 0.0f : x.h;
+        auto take = [&](float v) {
+            const float d = (v - largest) * a.scale, e = v != largest ? pow2(d) : 0.0f;
+            s += e;
+            h = __fmaf_rn(e, fmaxf(d, -1000.0f), h);
+        };
+        const float its_edge = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(edge), owner));
+        if (lane == 0) take(its_edge);
+        for (int i = lane; i < segments * P; i += 64) {
+            const int piece = p0 + i * NT + 64 * wave + owner;
+            if (piece >= p1) continue;
+            float v[E];
+            Pc::get(zb[piece], v);
+#pragma unroll
+            for (int j = 0; j < E; ++j) take(v[j]);
+        }
+        rest.r = wave_sum(s);
+        rest.h = wave_sum(h);
+    }
     if (NW > 1 || TOP) {
-        if (lane == 0) wave_sums[wave] = x;
+        if (lane == 0) wave_sums[wave] = rest;
         lds_barrier();
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, wave_sums[w].m);
-        Sums all = {M, 0.0f, 0.0f};
+        Rest all = {M, 0.0f, 0.0f};
+        bool found = false;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            Sums y = wave_sums[w];
-            to_largest(y, M, a.scale);
-            all.s += y.s;
+            Rest y = wave_sums[w];
+            const bool own = !found && y.m == M;
+            found |= own;
+            relative_to(y, M, own, a.scale);
+            all.r += y.r;
             all.h += y.h;
         }
-        x = all;
+        rest = all;
     }
-    const float L = logf(x.s);
+    const float L = log_of_sum(rest.r);
     int total = 0;
     if constexpr (TOP) {
         u64* list = room + KEYS;
@@ -531,15 +599,15 @@ __global__ void __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(TOP ? 6
         for_places<NT>(list, total, [&](u64 e, int place) {
             if (place >= a.top) return;
             if (a.parts > 1) a.list[out * a.top + place] = e;
-            else write_entry(a, row, place, e, x.m, L);
+            else write_entry(a, row, place, e, rest.m, L);
         });
-        if (a.parts == 1 && total < a.top && wave == 0) write_masked<DT>(a, row, total, x.m, L);
+        if (a.parts == 1 && total < a.top && wave == 0) write_masked<DT>(a, row, total, rest.m, L);
     }
     if (tid == 0) {
         if (a.parts == 1) {
-            write_row(a, row, x, L, z_token);
+            write_row(a, row, rest, L, z_token);
         } else {
-            a.part[row * a.parts + part] = make_float4(x.m, x.s, x.h, __int_as_float(min(total, a.top)));
+            a.part[row * a.parts + part] = make_float4(rest.m, rest.r, rest.h, __int_as_float(min(total, a.top)));
             if (part == 0) a.z_token[row] = z_token;
         }
     }
@@ -560,7 +628,7 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(TokenArgs a)
     const u64* from = a.list + row * a.parts * a.top;
     // Everything that most calls need is asked for at once; what a list holds
     // past its end is dropped later.
-    const float4 mine = lane < a.parts ? a.part[row * a.parts + lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+    const float4 mine = lane < a.parts ? a.part[row * a.parts + lane] : make_float4(-INFINITY, -1.0f, 0.0f, 0.0f);
     const float z_token = a.z_token[row];
     const int all = a.parts * a.top;
     u64 own[EARLY], low = 0;
@@ -570,8 +638,8 @@ __global__ void __launch_bounds__(256) tokens_join_kernel(TokenArgs a)
         for (int i = 0; i < EARLY; ++i) own[i] = from[min(tid + 256 * i, all - 1)];
     }
     const int have = __float_as_int(mine.w);
-    const Sums x = wave_total({mine.x, mine.y, mine.z}, a.scale);   // every wave the same
-    const float L = logf(x.s);
+    const Rest x = wave_total({mine.x, mine.y, mine.z}, a.scale);   // every wave the same
+    const float L = log_of_sum(x.r);
     if constexpr (TOP) {
         const bool is_full = lane < a.parts && have == a.top;
         const int full = __popcll(__ballot(is_full));
@@ -657,6 +725,11 @@ __global__ void __launch_bounds__(kStripThreads) tokens_grad_kernel(TokenGradArg
         const float lp = (x - pivot) * a.scale - l2, p = pow2(lp);
         return p * (c0 + c1 * fmaxf(lp, -1000.0f));
     };
+    // The token: u (1 - p) by expm1, which loses nothing where p is near 1.
+    auto own = [&](float x) {
+        const float lp = (x - pivot) * a.scale - l2, p = pow2(lp);
+        return p * (c1 * fmaxf(lp, -1000.0f) - v * H * a.inv) - u * a.inv * expm1f(lp * kLn2);
+    };
     u4 r[kStripEach];
     const int first = strip * kStripThreads * kStripEach + tid;
     const unsigned long long at = reinterpret_cast<unsigned long long>(z + sp.head);
@@ -694,8 +767,13 @@ __global__ void __launch_bounds__(kStripThreads) tokens_grad_kernel(TokenGradArg
             for (int i = 0; i < E; ++i) x[i] = one(x[i]);
             const int k = t - (sp.head + piece * E);
             if (u != 0.0f && (unsigned)k < (unsigned)E) {
+                float y[E], w = 0.0f;
+                Pc::get(r[q], y);
 #pragma unroll
-                for (int i = 0; i < E; ++i) x[i] += i == k ? u * a.inv : 0.0f;
+                for (int i = 0; i < E; ++i) w = i == k ? y[i] : w;
+                w = own(w);
+#pragma unroll
+                for (int i = 0; i < E; ++i) x[i] = i == k ? w : x[i];
             }
         }
         __builtin_nontemporal_store(Pc::put(x), reinterpret_cast<u4*>(g + sp.head) + piece);
@@ -704,7 +782,7 @@ __global__ void __launch_bounds__(kStripThreads) tokens_grad_kernel(TokenGradArg
         int j = -1;
         if (tid < sp.head) j = tid;
         if (tid >= 32 && tid - 32 < a.V - sp.tail0) j = sp.tail0 + tid - 32;
-        if (j >= 0) g[j] = (T)(off ? 0.0f : one((float)z[j]) + (j == t ? u * a.inv : 0.0f));
+        if (j >= 0) g[j] = (T)(off ? 0.0f : (u != 0.0f && j == t ? own((float)z[j]) : one((float)z[j])));
     }
 }
 

@@ -30,7 +30,7 @@ struct TokenArgs {
     // Rows cut over workgroups: what each leaves of its part of a row, and
     // then `top` candidates of each, the best first.
     int parts;
-    float4* part;          // [rows][parts]: m, sum exp, sum of exp times exponent, number of candidates
+    float4* part;          // [rows][parts]: m, sum exp without m's own 1, sum of exp times exponent, number of candidates
     float* z_token;        // [rows]: the token's logit
     unsigned long long* list;   // [rows][parts][top]
 };
