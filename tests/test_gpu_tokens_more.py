@@ -101,3 +101,49 @@ def test_confident_rows(R, V, top, dtype, far):
     grad = sam.token_logprobs_grad(z, tokens, got[2], got[1], u, v, T)
     ref.close(grad.gather(1, at[:, None])[:, 0], want["grad"], "gradient at the token")
     check(z, tokens, u, v, T, top)                               # and everything else
+
+
+@pytest.mark.parametrize("R,V,dtype", [(300, 262147, "f32"), (260, 1000003, "f32"), (257, 530001, "bf16"), (257, 530001, "f16")])
+def test_long_rows_on_a_workgroup(R, V, dtype):
+    """Rows so long that what a thread keeps stands for several turns' pieces: random, masked, constant, NaN."""
+    z, t, u, v = make(R, V, dtype, 60)
+    z[0], z[1], z[2, 7:] = -math.inf, 2.5, -math.inf
+    z[3], z[4, ::2] = torch.arange(V, device="cuda") / V, -math.inf
+    z[5], z[6] = -torch.arange(V, device="cuda") / V, torch.finfo(TYPES[dtype]).min
+    z[7, V // 2:V // 2 + 300] += 40                              # the best next to each other
+    z[8, 5], z[9, V - 1], z[10, V // 3] = math.nan, math.inf, math.nan
+    rows = torch.cat((torch.arange(16, device="cuda"), torch.tensor([R // 2, R - 1], device="cuda")))
+    for top in (20, 128):
+        got = sam.token_logprobs(z, t, 1.0, top)
+        want = ref.reference(z[rows], t[rows], 1.0, top)
+        bad = torch.zeros(len(rows), dtype=torch.bool, device="cuda")
+        bad[8:11] = True
+        assert torch.equal(got[4][rows], want["top_index"])
+        for x, name in zip(got, ("logprob", "entropy", "norm", "top_logprob")):
+            a, b = want[name]
+            ref.close(x[rows][~bad], (a[~bad], b[~bad]), name)
+        assert got[0][8:11].isnan().all() and got[3][8:11].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("top", [20, 128])
+def test_candidates_of_many_parts(top, dtype):
+    """Few rows cut over 64 workgroups, whose lists are joined: rising and falling rows, where almost every list's entries
+    reach the bound, the best in one part, equal values, masked parts."""
+    V = 1000003 if dtype == "f32" else 2000003
+    ramp = (torch.arange(V, device="cuda").double() / V * 40 - 20).float()
+    g = torch.Generator(device="cuda").manual_seed(61)
+    noise = torch.randn(2, V, device="cuda", generator=g)
+    one = noise[0].clone()
+    one[V // 2:V // 2 + 5000] += 60
+    masked = noise[1].clone()
+    masked[: V // 4 * 3] = -math.inf
+    rows = [ramp, ramp.flip(0), one, torch.zeros(V, device="cuda"), masked, torch.full((V,), -math.inf, device="cuda"), noise[0]]
+    tokens = torch.tensor([V - 1, 0], dtype=torch.int32, device="cuda")
+    for a, b in zip(rows, rows[1:] + rows[:1]):
+        z = torch.stack((a, b)).to(TYPES[dtype])
+        got = sam.token_logprobs(z, tokens, 1.0, top)
+        want = ref.reference(z, tokens, 1.0, top)
+        assert torch.equal(got[4], want["top_index"])
+        for x, name in zip(got, ("logprob", "entropy", "norm", "top_logprob")):
+            ref.close(x, want[name], name)
