@@ -509,8 +509,8 @@ sam_status sam_linear_mxfp4_backward_workspace_strided(
  * nothing in the entropy; as most likely entries they come last. A row
  * without any other has entropy 0, m = L = -inf and log probabilities -inf. A row that
  * holds NaN or +inf has NaN results, but its top_index are entries all the
- * same (NaN counts as the largest). V up to 2^31 - 65536, T from 2^-40 to
- * 2^40; rows == 0 is a no-op. Sums are FP32 and kept without the largest entry's
+ * same (NaN counts as the largest). V up to 2^31 - 65536, rows *
+ * ceil(V / 16384) under 2^22, T from 2^-40 to 2^40; rows == 0 is a no-op. Sums are FP32 and kept without the largest entry's
  * own 1: log p, entropy and L near 0 are as exact as the probabilities beside
  * that entry. No atomics on results, a fixed order. Results overlap nothing
  * else. Workspace: sam_token_logprobs_workspace() bytes,
