@@ -400,34 +400,6 @@ sam_status enqueue(const Call& c, const Layout& L, Ptrs p, void* ws, hipStream_t
     return api_ok();
 }
 
-struct Buf {
-    const void* p;
-    unsigned long long bytes;
-    const char* name;
-    int align;
-    bool written;
-};
-
-// Null, alignment and overlap: nothing that is written may overlap anything else.
-sam_status check_buffers(const Buf* b, int n)
-{
-    for (int i = 0; i < n; ++i) {
-        if (b[i].bytes && !b[i].p) return api_fail(SAM_ERR_INVALID_ARG, "%s is null", b[i].name);
-        if (b[i].bytes && (b[i].align == 16 ? !aligned16(b[i].p) : !aligned4(b[i].p)))
-            return api_fail(SAM_ERR_MISALIGNED, "%s must be %d-byte aligned", b[i].name, b[i].align);
-    }
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < n; ++j)
-            if (i != j && b[i].written && ranges_overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
-                return api_fail(SAM_ERR_INVALID_ARG, "%s overlaps %s", b[i].name, b[j].name);
-    return SAM_OK;
-}
-
-unsigned long long span(long long rows, long long ld, long long cols, int es)
-{
-    return rows > 0 ? ((unsigned long long)(rows - 1) * ld + cols) * es : 0;
-}
-
 // A single row's stride reaches nothing: it is neither a reason to refuse it
 // nor one to copy it.
 long long stride_of(long long rows, long long ld, long long cols)

@@ -13,14 +13,6 @@ int elem(int dtype) { return dtype == SAM_F32 ? 4 : 2; }
 
 bool aligned_to(const void* p, int n) { return (unsigned long long)p % (unsigned)n == 0; }
 
-struct Buf {
-    const void* p;
-    unsigned long long bytes;
-    const char* name;
-    int align;
-    bool written;
-};
-
 sam_status check(int dtype, int64_t rows, int64_t V, int64_t top, int64_t ldz, int t_dtype, float T, const Buf* b, int n)
 {
     for (int t : {dtype, t_dtype})
@@ -33,21 +25,7 @@ sam_status check(int dtype, int64_t rows, int64_t V, int64_t top, int64_t ldz, i
     // Within these 1 / T, T^2 and their products with the other factors are ordinary numbers.
     if (!(T >= 0x1p-40f) || !(T <= 0x1p40f))
         return api_fail(SAM_ERR_INVALID_ARG, "temperature must be positive, between 2^-40 and 2^40");
-    for (int i = 0; i < n; ++i) {
-        if (b[i].bytes && !b[i].p) return api_fail(SAM_ERR_INVALID_ARG, "%s is null", b[i].name);
-        if (b[i].bytes && !aligned_to(b[i].p, b[i].align))
-            return api_fail(SAM_ERR_MISALIGNED, "%s must be %d-byte aligned", b[i].name, b[i].align);
-    }
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < n; ++j)
-            if (i != j && b[i].written && ranges_overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
-                return api_fail(SAM_ERR_INVALID_ARG, "%s overlaps %s", b[i].name, b[j].name);
-    return SAM_OK;
-}
-
-unsigned long long span(int64_t rows, int64_t ld, int64_t cols, int es)
-{
-    return rows > 0 ? ((unsigned long long)(rows - 1) * ld + cols) * es : 0;
+    return check_buffers(b, n);
 }
 
 DistillArgs arguments(int64_t rows, int64_t V, int64_t top, const void* z, int64_t ldz, int t_dtype, const void* t,

@@ -9,34 +9,6 @@ namespace {
 
 int elem(int dtype) { return dtype == SAM_F32 ? 4 : 2; }
 
-struct Buf {
-    const void* p;
-    unsigned long long bytes;
-    const char* name;
-    int align;
-    bool written;
-};
-
-unsigned long long span(int64_t rows, int64_t ld, int64_t cols, int es)
-{
-    return rows > 0 ? ((unsigned long long)(rows - 1) * ld + cols) * es : 0;
-}
-
-// Null, alignment and overlap: nothing that is written may overlap anything else.
-sam_status check_buffers(const Buf* b, int n)
-{
-    for (int i = 0; i < n; ++i) {
-        if (b[i].bytes && !b[i].p) return api_fail(SAM_ERR_INVALID_ARG, "%s is null", b[i].name);
-        if (b[i].bytes && (unsigned long long)b[i].p % (unsigned)b[i].align)
-            return api_fail(SAM_ERR_MISALIGNED, "%s must be %d-byte aligned", b[i].name, b[i].align);
-    }
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < n; ++j)
-            if (i != j && b[i].written && ranges_overlap(b[i].p, b[i].bytes, b[j].p, b[j].bytes))
-                return api_fail(SAM_ERR_INVALID_ARG, "%s overlaps %s", b[i].name, b[j].name);
-    return SAM_OK;
-}
-
 sam_status check_sizes(int dtype, int64_t rows, int64_t V, int64_t ldz, float T)
 {
     if (dtype < SAM_F32 || dtype > SAM_F16) return api_fail(SAM_ERR_INVALID_ARG, "bad dtype %d", dtype);
