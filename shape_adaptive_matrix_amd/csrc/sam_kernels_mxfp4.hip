@@ -3,10 +3,11 @@
 //
 // Bound by memory: 2 or 4 bytes a value on one side, 17 / 32 of a byte on the
 // other. The scaled conversions of gfx950 take a pair of values by a power of
-// two to E2M1 (to nearest, ties to even, saturating) and back; they were
-// compared with the definition for every finite 16-bit value and 4 million
-// FP32 ones at six distances from the block's exponent. A scale of code 0
-// (2^-127) is the float with all bits zero to them.
+// two to E2M1 (to nearest, ties to even, saturating) and back; the tests hold
+// them against the definition for every 16-bit pattern at four distances from
+// its block's largest value, for 262144 FP32 bit patterns, and on and next to
+// the borders between codes. A scale of code 0 (2^-127) is the float with all
+// bits zero to them.
 #include "sam_mxfp4.h"
 #include "sam_quant4.h"
 

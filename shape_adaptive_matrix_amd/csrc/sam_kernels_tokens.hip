@@ -6,7 +6,8 @@
 // and finds the most likely entries on the way:
 //
 //  * Every thread keeps, in 16 bits each, the largest value of its 16-byte
-//    pieces (of rows too long for that, of four pieces). Behind the row the
+//    pieces (of rows too long for that, of the four pieces of a turn, or of
+//    those of several turns: at most 32 numbers). Behind the row the
 //    top-th largest of the threads' own largest values, found bit by bit, is a
 //    lower bound of the row's top-th largest value that few pieces reach.
 //  * Those pieces are read again (of 32768 values and 64 alternatives about 75
