@@ -40,8 +40,8 @@ PEAK_HBM_GBS = 8000.0
 
 
 KERNEL_SOURCES = ["sam_kernels.hip", "sam_kernels_dma.hip", "sam_kernels_dma_t.hip", "sam_ring16.h", "sam_sk.h",
-                  "sam_kernels_stream.hip", "sam_kernels_f32ring.hip", "sam_kernels_mx.hip", "sam_kernels_kq.hip",
-                  "sam_kernels_kp.hip", "sam_dma.h", "sam_internal.h", "sam_variants.h", "sam_variants_mx.h"]
+                  "sam_kernels_stream.hip", "sam_kernels_f32ring.hip", "sam_kernels_mx.hip", "sam_mx8.h",
+                  "sam_kernels_kq.hip", "sam_kernels_kp.hip", "sam_dma.h", "sam_internal.h", "sam_variants.h", "sam_variants_mx.h"]
 
 # Kernel function of a plan, by the leading letters of its variant name.
 KERNEL_OF = {"t": "sam::gemm_kernel", "r": "sam::gemm16_dma_kernel", "q": "sam::gemm16_dma_kernel",
@@ -62,7 +62,7 @@ SOURCES_OF_KERNEL = {
                                   "sam_variants.h"],
     "sam::gemm16_dma_kernel": ["sam_ring16.h", "sam_kernels_dma.hip", "sam_dma.h", "sam_sk.h", "sam_internal.h",
                                "sam_variants.h"],
-    "sam::gemm_mx8_kernel": ["sam_kernels_mx.hip", "sam_dma.h", "sam_internal.h", "sam_variants.h",
+    "sam::gemm_mx8_kernel": ["sam_mx8.h", "sam_kernels_mx.hip", "sam_dma.h", "sam_internal.h", "sam_variants.h",
                              "sam_variants_mx.h"],
 }
 
