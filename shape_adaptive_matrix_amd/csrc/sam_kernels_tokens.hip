@@ -129,7 +129,7 @@ __device__ __forceinline__ float log_of_sum(float r)
 // without it, by its wave: its own sum, which holds that 1, is off by some
 // 2^-24 (of 256 values some 2^-22), and with it log p, the entropy and 1 - p of a
 // row whose p is near 1. One more trip to memory for such rows: 4096 x 32768
-// bf16, all of them so, 51 us instead of 49; 2048 x 131072 FP32 160, 155.
+// bf16, all of them so, 52 us instead of 49; 2048 x 131072 FP32 160, 155.
 constexpr float kSmallRest = 0.25f;
 
 // log p of a value of a row with norm (m, L); with m = -inf the pivot is 0.
